@@ -34,8 +34,8 @@
  *  - Every call: num_q_heads = 16, num_kv_heads = 8, head_dim = 128,
  *    page_size = 16 (the Qwen3 decoder; the tuned kernels).
  *  - pkv_append, pkv_decode_attn, pkv_decode_append_attn,
- *    pkv_decode_append_rope_attn and pkv_prefill_chunk_attn also take
- *    page_size = 16, head_dim 64 or 128,
+ *    pkv_decode_append_rope_attn, pkv_append_rope, pkv_prefill_chunk_attn and
+ *    the calls of the 8-bit cache also take page_size = 16, head_dim 64 or 128,
  *    any num_kv_heads and num_q_heads = G * num_kv_heads with G from 1 to 8
  *    (other decoder backbones; decode runs the same persistent split-KV
  *    kernel with the head counts read at run time, early prefetch included;
@@ -74,11 +74,11 @@
  *    it not so, the wait would run out after about one second and report
  *    PKV_ERR_DEVICE_TIMEOUT; it never hangs.
  *  - A workspace serves one kind of attention call: decode calls
- *    (pkv_decode_attn, pkv_decode_append_attn) or prefill calls
+ *    (pkv_decode_attn, pkv_decode_append_attn, pkv_decode_attn_fp8) or prefill calls
  *    (pkv_prefill_chunk_attn), not both: each kind relies on its own split
  *    scratch (counters, and for decode tagged records) having been left
- *    cleared by the previous call of that kind. pkv_append uses only the
- *    status word and may share either.
+ *    cleared by the previous call of that kind. The appends and pkv_expand_fp8
+ *    use only the status word and may share either.
  */
 #ifndef PKV_H_
 #define PKV_H_
@@ -291,6 +291,128 @@ int pkv_decode_append_rope_attn(const void* q, const void* k_new, const void* v_
  * unaligned table; nothing is written then.
  */
 int pkv_rope_table(float* table, int32_t max_pos, int32_t head_dim, double theta, pkv_stream_t stream);
+
+/*
+ * pkv_append_rope -- write the key and value rows of new tokens into their
+ * slots with the rotary position embedding (and the per-head RMS norm of
+ * Qwen3-style decoders) applied on the way, and rotate the tokens' query rows.
+ *
+ * Source: as for pkv_append; the decoder is a Qwen3-style causal LM with RoPE
+ * theta 1e6 ("Fun-ASR-Nano Native Runtime Design", section "Decoder And
+ * Prompt"). The pages name RoPE and theta only; rotate-half pairs and the
+ * norms of the q and k rows before the rotation are those of Qwen3 decoders.
+ * It is the step before pkv_prefill_chunk_attn (whose queries and cached keys
+ * are already rotated) and before pkv_decode_attn.
+ *
+ * For token t, position p = positions[t], every row x of head_dim values, fp32:
+ *   u = x * w,  w = q_weight or k_weight     (u = x where the weight is NULL)
+ *   y1 = fmaf(u1, c, -(u2 * s)),  y2 = fmaf(u2, c, u1 * s)   for the pairs
+ *     (u1, u2) = (u[i], u[i + head_dim/2]), c = table[p][i],
+ *     s = table[p][head_dim/2 + i]           (y = u where the table is NULL)
+ *   y *= 1 / sqrt(mean(x^2) + eps)           (only where a weight is given)
+ * and y is rounded to bf16 (ties to even) once. Without weights the key rows
+ * written are those of pkv_decode_append_rope_attn, bit for bit; without
+ * weights and table they are pkv_append's. Value rows are copied bit for bit.
+ *
+ *  q:            bf16, token t's [num_q_heads][head_dim] at q + t * q_stride,
+ *                or NULL (with q_out NULL): no query rows
+ *  k_new, v_new: bf16, token t's [num_kv_heads][head_dim] at k_new + t *
+ *                k_stride, v_new + t * v_stride
+ *  *_stride:     elements between tokens, at least one token's row count *
+ *                head_dim and a multiple of 8 (rows of a fused q/k/v
+ *                projection need no copy); not used for n_tokens = 1
+ *  positions:    int32 [n_tokens]; needed with a table only. A position
+ *                outside [0, rope_max_pos) is clamped and, unless the token has
+ *                neither a query row nor a slot, sets PKV_ERR_OUT_OF_BOUNDS
+ *  slot_mapping: int32 [n_tokens]; as for pkv_append: a negative slot skips
+ *                the token's k and v (its query rows are still written), one
+ *                past the pool sets PKV_ERR_OUT_OF_BOUNDS and is skipped. The
+ *                slots that are not negative must differ from each other (of
+ *                two equal ones either row's values may end up in the slot)
+ *  n_tokens:     >= 0 (0 launches nothing); n_tokens * (num_q_heads + 2 *
+ *                num_kv_heads) < 2^31
+ *  rope_cos_sin: fp32 [rope_max_pos][head_dim] (pkv_rope_table), or NULL
+ *  q_weight, k_weight: bf16 [head_dim], each may be NULL
+ *  eps:          >= 0, read where a weight is given
+ *  q_out:        bf16 [n_tokens][num_q_heads][head_dim]; may be q itself where
+ *                q's tokens are contiguous
+ *  k_pages, v_pages: the bf16 pools, updated in place
+ *  workspace:    as for pkv_append (may be NULL)
+ * Every buffer but positions and slot_mapping is 16-byte aligned.
+ */
+int pkv_append_rope(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                    int64_t v_stride, const int32_t* positions, const int32_t* slot_mapping, int32_t n_tokens,
+                    const float* rope_cos_sin, int32_t rope_max_pos, const void* q_weight, const void* k_weight,
+                    float eps, void* q_out, void* k_pages, void* v_pages, const pkv_cache_desc* desc,
+                    pkv_stream_t stream, void* workspace, size_t workspace_bytes);
+
+/*
+ * The 8-bit paged KV cache. The source pages have no counterpart: decode is
+ * bound by the bytes of the cache, and this cache has half of them.
+ *
+ *  - k_pages, v_pages: e4m3 [num_pages][num_kv_heads][page_size][head_dim]
+ *    (4 exponent bits, 3 mantissa bits, largest value 448, no infinities).
+ *  - kv_scales: one byte per row, [num_pages][num_kv_heads][2][page_size]: the
+ *    K rows' scales, then the V rows'. Byte b stands for 2^(b - 127) (e8m0).
+ *  - A row x stands for 2^e v: e is the least integer with max |x_i| <= 448 *
+ *    2^e over the finite x_i, clamped to [-80, 100] (-80 for a row of zeros),
+ *    and v_i = x_i * 2^-e rounded to e4m3, ties to even, saturating at 448
+ *    (infinities saturate too; NaN stays NaN). 2^e v is exact in bf16.
+ *  - Layout, block tables, slots and geometry as for the bf16 pools: page_size
+ *    16, head_dim 64 or 128, 1 to 8 query heads per KV head.
+ *  - max_pages_per_seq < 2^27 in these calls.
+ */
+
+/*
+ * pkv_append_rope_fp8 -- pkv_append_rope into the 8-bit cache: key rows are
+ * quantised from the fp32 y above (no bf16 rounding in between), value rows
+ * from their bf16 values. The query rows are as for pkv_append_rope. Without
+ * table and weights it is the plain append of the 8-bit cache.
+ */
+int pkv_append_rope_fp8(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                        int64_t v_stride, const int32_t* positions, const int32_t* slot_mapping, int32_t n_tokens,
+                        const float* rope_cos_sin, int32_t rope_max_pos, const void* q_weight, const void* k_weight,
+                        float eps, void* q_out, void* k_pages, void* v_pages, void* kv_scales,
+                        const pkv_cache_desc* desc, pkv_stream_t stream, void* workspace, size_t workspace_bytes);
+
+/*
+ * pkv_decode_attn_fp8 -- pkv_decode_attn over the 8-bit cache: the same sums
+ * over the rows that the cache stands for, in fp32, with the keys and values
+ * unrounded and the softmax weights rounded to fp16 (2^-12) before they
+ * multiply V. Arguments, lengths of zero, errors and the workspace
+ * (pkv_decode_workspace_bytes) are pkv_decode_attn's; a workspace may serve
+ * both in turn. The kernel waits for the kernel before it (no early prefetch).
+ */
+int pkv_decode_attn_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
+                        const int32_t* block_table, const int32_t* seq_lens, void* out, float scale,
+                        pkv_stream_t stream, const pkv_cache_desc* desc, int32_t batch, int32_t max_pages_per_seq,
+                        void* workspace, size_t workspace_bytes);
+
+/*
+ * pkv_expand_fp8 -- pages of the 8-bit cache as bf16 pages, exactly: the
+ * prefix that pkv_prefill_chunk_attn reads when a prompt is cached in 8 bits.
+ *
+ * For every request s and page p < ceil(seq_lens[s] / page_size), the rows of
+ * page block_table[s][p] of the 8-bit cache that lie before seq_lens[s] are
+ * written to the same rows of page out_block_table[s][p] of k_out and v_out
+ * (bf16 [out_num_pages][num_kv_heads][page_size][head_dim]). Rows at or past
+ * seq_lens[s] and other pages are left as they were.
+ *
+ *  block_table, out_block_table: int32 [num_seqs][max_pages_per_seq]; entries
+ *                past a request's last page are never read. A page id outside
+ *                its pool sets PKV_ERR_OUT_OF_BOUNDS and the page is skipped.
+ *                No two pages of a call may have the same output page
+ *  seq_lens:     int32 [num_seqs]; clamped to [0, max_pages_per_seq *
+ *                page_size] with PKV_ERR_OUT_OF_BOUNDS
+ *  num_seqs:     >= 0 (0 launches nothing); num_seqs * max_pages_per_seq *
+ *                max(num_kv_heads, 8) < 2^31
+ *  desc:         the 8-bit cache's geometry (num_pages its pages)
+ *  workspace:    as for pkv_append (may be NULL)
+ */
+int pkv_expand_fp8(const void* k_pages, const void* v_pages, const void* kv_scales, const int32_t* block_table,
+                   const int32_t* seq_lens, int32_t num_seqs, int32_t max_pages_per_seq, void* k_out, void* v_out,
+                   const int32_t* out_block_table, int32_t out_num_pages, const pkv_cache_desc* desc,
+                   pkv_stream_t stream, void* workspace, size_t workspace_bytes);
 
 /*
  * Workspace bytes pkv_prefill_chunk_attn needs: the status header, split

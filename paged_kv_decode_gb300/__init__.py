@@ -37,6 +37,7 @@ __all__ = [
     "PkvError", "desc", "Workspace", "append", "decode_attn", "prefill_chunk_attn",
     "decode_workspace_bytes", "prefill_workspace_bytes", "workspace_init", "read_status", "status_string",
     "decode_attn_noalloc", "decode_append_attn", "mixed_step_attn", "mixed_workspace_bytes", "rope_cos_sin",
+    "append_rope", "append_rope_fp8", "decode_attn_fp8", "expand_fp8",
 ]
 
 
@@ -272,6 +273,189 @@ def _decode_append(q, k_new, v_new, k_pages, v_pages, block_table, seq_lens, out
                                              _ptr(out), float(scale), _stream(stream), ctypes.byref(d), B,
                                              block_table.shape[1], _ptr(ws), ws.numel(), flags)
         _check(rc, "pkv_decode_append_rope_attn")
+
+
+# ---------------------------------------------------------------------------- append with rotation, 8-bit cache
+def _run(what: str, dev, stream, fn, *args):
+    """Call fn(*args with the stream in the place of _STREAM) with `dev` current, on `stream` or dev's current one."""
+    import torch
+
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if s.device != dev:
+        raise ValueError(f"{what}: the stream is on {s.device}, the tensors are on {dev}")
+    args = [s.cuda_stream if a is _STREAM else a for a in args]
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    _check(rc, what)
+
+
+_STREAM = object()
+
+
+def _ws(workspace: Optional[Workspace], dev):
+    """(pointer, bytes) of a workspace on dev; (None, 0) without one."""
+    if workspace is None:
+        return None, 0
+    t = workspace.tensor
+    if t.device != dev:
+        raise ValueError(f"the workspace is on {t.device}, expected {dev}")
+    return t.data_ptr(), t.numel()
+
+
+def _token_rows(t, name, dev, n: int, heads: Optional[int], d: int) -> int:
+    """Check the new tokens' rows [n, heads, d] (a token's rows contiguous, tokens any distance apart, as in a fused
+    projection's output); returns the elements between tokens."""
+    import torch
+
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [{n}, {'heads' if heads is None else heads}, {d}], got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the rows of a token must be contiguous")
+    return t.stride(0)
+
+
+def _fp8_pools(k_pages, v_pages, kv_scales):
+    """Check the pools and scales of an 8-bit cache; returns their device."""
+    import torch
+
+    _need(k_pages, torch.float8_e4m3fn, "k_pages")
+    dev = k_pages.device
+    _need(v_pages, torch.float8_e4m3fn, "v_pages", dev)
+    _need(kv_scales, torch.float8_e8m0fnu, "kv_scales", dev)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("pools are [num_pages, num_kv_heads, page_size, head_dim]")
+    p, h, ps, _ = k_pages.shape
+    if kv_scales.shape != (p, h, 2, ps):
+        raise ValueError(f"kv_scales must be [{p}, {h}, 2, {ps}], got {tuple(kv_scales.shape)}")
+    return dev
+
+
+def _append_rope(what, fn, k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages, kv_scales, workspace, q,
+                 q_out, q_weight, k_weight, eps, stream, dev):
+    import torch
+
+    _, hkv, _, d = k_pages.shape
+    _need(slot_mapping, torch.int32, "slot_mapping", dev)
+    n = slot_mapping.numel()
+    k_stride = _token_rows(k_new, "k_new", dev, n, hkv, d)
+    v_stride = _token_rows(v_new, "v_new", dev, n, hkv, d)
+    q_stride = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None:
+        q_stride = _token_rows(q, "q", dev, n, None, d)
+        _need(q_out, torch.bfloat16, "q_out", dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+            raise ValueError("q_out may be q itself only where q is contiguous")
+    elif q_weight is not None:
+        raise ValueError("q_weight without q")
+    max_pos = 0
+    if cos_sin is not None:
+        _need(cos_sin, torch.float32, "cos_sin", dev)
+        if cos_sin.dim() != 2 or cos_sin.shape[1] != d:
+            raise ValueError("cos_sin must be [max_pos, head_dim]")
+        max_pos = cos_sin.shape[0]
+        _need(positions, torch.int32, "positions", dev)
+        if positions.numel() != n:
+            raise ValueError("positions and slot_mapping differ in length")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, torch.bfloat16, name, dev)
+            if w.shape != (d,):
+                raise ValueError(f"{name} must be [{d}]")
+    ds = _desc_of(k_pages, None if q is None else q.shape[1])
+    ws, nbytes = _ws(workspace, dev)
+    scales = () if kv_scales is None else (kv_scales.data_ptr(),)
+    _run(what, dev, stream, fn, _ptr(q), q_stride, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
+         None if cos_sin is None else positions.data_ptr(), slot_mapping.data_ptr(), n, _ptr(cos_sin), max_pos,
+         _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(), *scales,
+         ctypes.byref(ds), _STREAM, ws, nbytes)
+
+
+def append_rope(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages,
+                workspace: Optional[Workspace] = None, q=None, q_out=None, q_weight=None, k_weight=None,
+                eps: float = 1e-6, stream=None):
+    """append of new tokens with the rotary embedding on the way: k_new / v_new [n, Hkv, D] (tokens may lie apart, as
+    in a fused projection's output) go to slots slot_mapping [n], keys rotated at positions [n] by cos_sin (from
+    rope_cos_sin; None: no rotation, positions unused). With q [n, Hq, D] the query rows are rotated into q_out.
+    q_weight / k_weight [D]: RMS norm of each head's row (with eps) before the rotation, as in Qwen3 decoders."""
+    import torch
+
+    _need(k_pages, torch.bfloat16, "k_pages")
+    dev = k_pages.device
+    _need(v_pages, torch.bfloat16, "v_pages", dev)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("pools are [num_pages, num_kv_heads, page_size, head_dim]")
+    _append_rope("pkv_append_rope", _lib.load().pkv_append_rope, k_new, v_new, positions, slot_mapping, cos_sin, k_pages,
+                 v_pages, None, workspace, q, q_out, q_weight, k_weight, eps, stream, dev)
+
+
+def append_rope_fp8(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages, kv_scales,
+                    workspace: Optional[Workspace] = None, q=None, q_out=None, q_weight=None, k_weight=None,
+                    eps: float = 1e-6, stream=None):
+    """append_rope into the 8-bit cache: pools torch.float8_e4m3fn [P, Hkv, 16, D] and kv_scales torch.float8_e8m0fnu
+    [P, Hkv, 2, 16] (a power of two per K row, then per V row). Rows are quantised from fp32 (format: include/pkv.h);
+    with cos_sin None it is the plain append of the 8-bit cache."""
+    dev = _fp8_pools(k_pages, v_pages, kv_scales)
+    _append_rope("pkv_append_rope_fp8", _lib.load().pkv_append_rope_fp8, k_new, v_new, positions, slot_mapping, cos_sin,
+                 k_pages, v_pages, kv_scales, workspace, q, q_out, q_weight, k_weight, eps, stream, dev)
+
+
+def decode_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, scale: float, workspace: Workspace,
+                    stream=None):
+    """decode_attn over the 8-bit cache (pools and kv_scales as for append_rope_fp8): out [B, Hq, D] from q [B, Hq, D].
+    The workspace is decode_attn's (decode_workspace_bytes) and may serve both in turn."""
+    import torch
+
+    dev = _fp8_pools(k_pages, v_pages, kv_scales)
+    _need(q, torch.bfloat16, "q", dev)
+    _need(out, torch.bfloat16, "out", dev)
+    _need(block_table, torch.int32, "block_table", dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
+    if q.dim() != 3 or q.shape[2] != k_pages.shape[3] or out.shape != q.shape or block_table.dim() != 2 \
+            or block_table.shape[0] != q.shape[0] or seq_lens.numel() != q.shape[0]:
+        raise ValueError("shape mismatch")
+    d = _desc_of(k_pages, q.shape[1])
+    ws, nbytes = _ws(workspace, dev)
+    _run("pkv_decode_attn_fp8", dev, stream, _lib.load().pkv_decode_attn_fp8, q.data_ptr(), k_pages.data_ptr(),
+         v_pages.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+         float(scale), _STREAM, ctypes.byref(d), q.shape[0], block_table.shape[1], ws, nbytes)
+
+
+def expand_fp8(k_pages, v_pages, kv_scales, block_table, seq_lens, k_out, v_out, out_block_table,
+               workspace: Optional[Workspace] = None, stream=None):
+    """Rows before seq_lens [S] of the 8-bit pages block_table [S, max_pages] as bf16, exactly, into pages
+    out_block_table [S, max_pages] of k_out / v_out [P', Hkv, 16, D] (what prefill_chunk_attn then reads)."""
+    import torch
+
+    dev = _fp8_pools(k_pages, v_pages, kv_scales)
+    _need(k_out, torch.bfloat16, "k_out", dev)
+    _need(v_out, torch.bfloat16, "v_out", dev)
+    _need(block_table, torch.int32, "block_table", dev)
+    _need(out_block_table, torch.int32, "out_block_table", dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
+    if k_out.dim() != 4 or k_out.shape[1:] != k_pages.shape[1:] or v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out are [pages, num_kv_heads, page_size, head_dim] of the cache's geometry")
+    if block_table.dim() != 2 or out_block_table.shape != block_table.shape \
+            or seq_lens.numel() != block_table.shape[0]:
+        raise ValueError("shape mismatch")
+    d = _desc_of(k_pages)
+    ws, nbytes = _ws(workspace, dev)
+    _run("pkv_expand_fp8", dev, stream, _lib.load().pkv_expand_fp8, k_pages.data_ptr(), v_pages.data_ptr(),
+         kv_scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), block_table.shape[0], block_table.shape[1],
+         k_out.data_ptr(), v_out.data_ptr(), out_block_table.data_ptr(), k_out.shape[0], ctypes.byref(d), _STREAM, ws,
+         nbytes)
 
 
 def prefill_chunk_attn(q, k_pages, v_pages, block_table, prefix_lens, cu_q_lens, out, scale: float, max_q_len: int,

@@ -25,6 +25,7 @@ class CacheDesc(ctypes.Structure):
 
 
 _vp, _i32, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
+_i64 = ctypes.c_int64
 _dp = ctypes.POINTER(CacheDesc)
 
 # name -> (restype, argtypes), in the order of include/pkv.h
@@ -40,6 +41,12 @@ PROTOTYPES = {
     "pkv_decode_append_rope_attn": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _f32, _vp, _dp,
                                                    _i32, _i32, _vp, _sz, ctypes.c_uint32]),
     "pkv_rope_table": (ctypes.c_int, [_vp, _i32, _i32, ctypes.c_double, _vp]),
+    "pkv_append_rope": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _f32, _vp,
+                                       _vp, _vp, _dp, _vp, _vp, _sz]),
+    "pkv_append_rope_fp8": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _f32,
+                                           _vp, _vp, _vp, _vp, _dp, _vp, _vp, _sz]),
+    "pkv_decode_attn_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _dp, _i32, _i32, _vp, _sz]),
+    "pkv_expand_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _dp, _vp, _vp, _sz]),
     "pkv_prefill_workspace_bytes": (_sz, [_dp, _i32, _i32]),
     "pkv_prefill_chunk_attn": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _f32, _vp, _dp, _i32,
                                               _i32, _vp, _sz]),

@@ -52,6 +52,28 @@ int encode_page_maps(const void* k_pages, const void* v_pages, int head_dim, int
   return PKV_OK;
 }
 
+int encode_page_maps_fp8(const void* k_pages, const void* v_pages, int head_dim, int num_pages, int hkv,
+                         CUtensorMap* kmap, CUtensorMap* vmap) {
+  const long long tiles = static_cast<long long>(num_pages) * hkv;
+  if (tiles > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // tile coordinates are 32-bit
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  EncodeTiledFn enc = encoder();
+  if (enc == nullptr) return PKV_ERR_CUDA;
+  const cuuint64_t row = static_cast<cuuint64_t>(head_dim);
+  const cuuint64_t dims[3] = {row, static_cast<cuuint64_t>(kPageSize), static_cast<cuuint64_t>(tiles)};
+  const cuuint64_t strides[2] = {row, row * kPageSize};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(head_dim), kPageSize, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const void* pools[2] = {k_pages, v_pages};
+  CUtensorMap* maps[2] = {kmap, vmap};
+  for (int i = 0; i < 2; ++i)
+    if (enc(maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pools[i]), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return PKV_ERR_CUDA;
+  return PKV_OK;
+}
+
 // The kernel's group for g query heads per KV head: the next of 1, 2, 4, 8.
 static int group_pad(int g) { return g <= 1 ? 1 : g <= 2 ? 2 : g <= 4 ? 4 : 8; }
 
@@ -75,6 +97,33 @@ size_t decode_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, i
   return off;
 }
 
+int launch_decode_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
+                      const int32_t* block_table, const int32_t* seq_lens, void* out, float scale, int num_q_heads,
+                      int num_kv_heads, int head_dim, int32_t batch, int32_t max_pages, int32_t num_pages,
+                      void* workspace, int num_sms, cudaStream_t stream) {
+  if (!decode_supported(num_q_heads, num_kv_heads, head_dim, kPageSize)) return PKV_ERR_UNSUPPORTED;
+  DecodeLaunch c = {};
+  c.q = q;
+  c.k_pages = k_pages;
+  c.v_pages = v_pages;
+  c.scales = kv_scales;
+  c.block_table = block_table;
+  c.seq_lens = seq_lens;
+  c.out = out;
+  c.scale = scale;
+  c.hq = num_q_heads;
+  c.hkv = num_kv_heads;
+  c.head_dim = head_dim;
+  c.batch = batch;
+  c.max_pages = max_pages;
+  c.num_pages = num_pages;
+  c.workspace = workspace;
+  c.num_sms = num_sms;
+  c.stream = stream;
+  const int G = group_pad(num_q_heads / num_kv_heads);
+  return head_dim == 64 ? launch_decode_fp8_d64(c, G) : launch_decode_fp8_d128(c, G);
+}
+
 int launch_decode(const void* q, const void* k_new, const void* v_new, const void* k_pages, const void* v_pages,
                   const int32_t* block_table, const int32_t* seq_lens, const float* rope, int32_t rope_max_pos,
                   void* out, float scale, int num_q_heads, int num_kv_heads, int head_dim, int32_t batch,
@@ -87,6 +136,7 @@ int launch_decode(const void* q, const void* k_new, const void* v_new, const voi
   c.v_new = v_new;
   c.k_pages = k_pages;
   c.v_pages = v_pages;
+  c.scales = nullptr;
   c.block_table = block_table;
   c.seq_lens = seq_lens;
   c.rope = rope;

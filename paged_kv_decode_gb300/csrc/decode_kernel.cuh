@@ -84,6 +84,7 @@
 #include <type_traits>
 
 #include "pkv_device.cuh"
+#include "pkv_fp8.cuh"
 #include "pkv_kernels.h"
 #include "pkv_mma.cuh"
 #include "pkv_tc.cuh"
@@ -146,6 +147,7 @@ struct DecodeArgs {
   int num_pages;
   int hkv;  // KV heads (run-time geometries)
   int gq;   // query heads per KV head (run-time geometries; at most the kernel's group)
+  const uint8_t* scales;  // 8-bit cache: [num_pages][hkv][2][16] e8m0 scales, else nullptr
   int* status;
   int* counters;       // [batch * hkv], zero between calls (counted merge)
   float* partials;     // [2 * gridDim.x][G * (D + 4)] (counted merge)
@@ -157,23 +159,27 @@ struct DecodeArgs {
 // at compile time (otherwise DecodeArgs::hkv / gq), and the launch shape: two
 // CTAs per SM with kRing stages per consumer, or (kWide, for a few long requests)
 // one CTA per SM with twice the stages, so each (request, KV head) has half as
-// many holders to merge and each CTA twice the bytes in flight.
-template <int D_, int G_, bool kFixed_, bool kWide_ = false>
+// many holders to merge and each CTA twice the bytes in flight. kFp8: the 8-bit
+// cache (pkv_fp8.cuh); a page is half as large, so a consumer's ring holds twice
+// as many.
+template <int D_, int G_, bool kFixed_, bool kWide_ = false, bool kFp8_ = false>
 struct DecGeo {
   static constexpr int D = D_;
   static constexpr int G = G_;
   static constexpr bool kFixed = kFixed_;
   static constexpr bool kWide = kWide_;
+  static constexpr bool kFp8 = kFp8_;
   static constexpr int kCtasPerSm = kWide ? 1 : kDecCtasPerSm;
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
   static_assert(G == 1 || G == 2 || G == 4 || G == 8, "one 8-column MMA tile of heads");
   static_assert(!kFixed || (D == kHeadDim && G == kGroup), "the fixed geometry is 16 / 8 / 128");
   static constexpr int kKS = D / 16;                    // 16-dim steps of both MMA products
-  static constexpr int kRing = (D == 128 ? PKV_DEC_RING : 2 * PKV_DEC_RING) * (kWide ? 2 : 1);  // per consumer
+  static constexpr int kRing = (D == 128 ? PKV_DEC_RING : 2 * PKV_DEC_RING) * (kWide ? 2 : 1) *
+                               (kFp8 ? 2 : 1);  // per consumer
   static constexpr int kStages = kCons * kRing;
-  static constexpr int kTile = kPageSize * D * 2;       // one (page, KV head) tile of K or V
+  static constexpr int kTile = kPageSize * D * (kFp8 ? 1 : 2);  // one (page, KV head) tile of K or V
   static constexpr int kStage = 2 * kTile;              // K tile + V tile
-  static constexpr int kRowB = D * 2;                   // one K or V row
+  static constexpr int kRowB = D * 2;                   // one query row (and bf16 K or V row)
   static constexpr int kRec = D + 4;                    // floats per query-head record: m, l, pad, pad, o[D]
   static constexpr int kPiece = G * kRec;               // a counted record of one piece (all heads)
   static constexpr int kPieceB = kPiece * 4;
@@ -188,7 +194,9 @@ struct DecGeo {
   static constexpr int kSmemMerge = kMergeFloats * 4;
   static constexpr int kSmemQ = 2 * kQBuf;              // this piece's rows and the next piece's
   static constexpr int kSmemCs = 2 * kCsB;              // rows for this piece's and the next piece's position
-  static constexpr int kSmemFixed = kSmemAlign + kSmemRing + kSmemBars + kSmemMerge + kSmemQ + kSmemCs + kSmemMisc;
+  static constexpr int kSmemScales = kFp8 ? kStages * kScaleBytes : 0;  // the stages' row scales
+  static constexpr int kSmemFixed =
+      kSmemAlign + kSmemRing + kSmemBars + kSmemMerge + kSmemQ + kSmemCs + kSmemScales + kSmemMisc;
   static constexpr int kMergeCap = kSmemRing / kPieceB;  // records staged per batch of a counted merge
   // Lane layout of the record merges: 4-word groups of a record's o, group x at words 4x .. 4x + 3
   // (head 4x / D, dims 4x mod D ..); lane l holds groups l, l + 32, ...
@@ -423,7 +431,8 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
   float* merge = reinterpret_cast<float*>(smem + Geo::kSmemRing + Geo::kSmemBars);
   unsigned char* qbuf = reinterpret_cast<unsigned char*>(merge + Geo::kMergeFloats);
   unsigned char* csbuf = qbuf + Geo::kSmemQ;
-  int* flag = reinterpret_cast<int*>(csbuf + Geo::kSmemCs);  // [0..1] merge flags, [2] a wait failed, [4..5] share
+  unsigned char* scbuf = csbuf + Geo::kSmemCs;  // (8-bit cache) kScaleBytes per stage
+  int* flag = reinterpret_cast<int*>(scbuf + Geo::kSmemScales);  // [0..1] merge flags, [2] a wait failed, [4..5] share
   int* pref = flag + kSmemMisc / 4;
   int* sl = pref + a.batch + 1;
   int* pcp = sl + a.batch;  // [batch + 1] non-empty (request, KV head) pairs before each request
@@ -622,10 +631,18 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
               const int pid = id_ok ? id : 0;
               const int z = pid * hkv + hh;  // tile of the pool
               unsigned char* dst = ring + slot * Geo::kStage;
-              mbar_arrive_expect_tx(&full[slot], Geo::kStage);
-              // one copy per tile: its D / 64 16-row x 64-dim halves, 128-byte swizzled
-              tma_load_4d_hint(dst, &kmap, 0, 0, 0, z, &full[slot], policy);
-              tma_load_4d_hint(dst + Geo::kTile, &vmap, 0, 0, 0, z, &full[slot], policy);
+              if constexpr (Geo::kFp8) {
+                mbar_arrive_expect_tx(&full[slot], Geo::kStage + kScaleBytes);
+                tma_load_3d_hint(dst, &kmap, 0, 0, z, &full[slot], policy);
+                tma_load_3d_hint(dst + Geo::kTile, &vmap, 0, 0, z, &full[slot], policy);
+                bulk_load_hint(scbuf + slot * kScaleBytes, a.scales + static_cast<size_t>(z) * kScaleBytes,
+                               kScaleBytes, &full[slot], policy);
+              } else {
+                mbar_arrive_expect_tx(&full[slot], Geo::kStage);
+                // one copy per tile: its D / 64 16-row x 64-dim halves, 128-byte swizzled
+                tma_load_4d_hint(dst, &kmap, 0, 0, 0, z, &full[slot], policy);
+                tma_load_4d_hint(dst + Geo::kTile, &vmap, 0, 0, 0, z, &full[slot], policy);
+              }
             }
           }
           __syncwarp();
@@ -699,8 +716,11 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
 
   // ============================================================== consumer warps
   const int r = lane >> 2, cq = lane & 3;  // MMA fragment row and column pair of this lane
-  uint32_t koff[kKS], voff[kKS];
-  mma_offsets<kKS>(koff, voff);
+  uint32_t koff[Geo::kFp8 ? kKS / 2 : kKS], voff[kKS];
+  if constexpr (Geo::kFp8)
+    fp8_offsets<D>(koff);
+  else
+    mma_offsets<kKS>(koff, voff);
 
   int k = 0;  // pages of this warp's sequence visited so far
   bool failed = false;
@@ -784,7 +804,10 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
     const uint32_t ccur = csb + (j & 1) * Geo::kCsB;
     const bool qrow = r < gq;
     uint32_t qf[kKS][2];
-    if constexpr (!kRope) {
+    float qs0 = 0.f, qs1 = 0.f;  // (8-bit cache) score scales of heads 2 cq, 2 cq + 1
+    if constexpr (Geo::kFp8) {
+      fp8_query<kKS>(qcur + r * D * 2, qrow, a.qscale, qf, qs0, qs1);
+    } else if constexpr (!kRope) {
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         qf[ks][0] = qrow ? lds32(qcur + r * Geo::kRowB + (16 * ks + 2 * cq) * 2) : 0u;
@@ -815,10 +838,11 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       }
     }
 
-    float o[kKS][4];  // O^T: dims 16 ks + r (+8) x heads 2 cq, 2 cq + 1
+    float o[kKS][4];  // O^T: dims 16 ks + r (+8) x heads 2 cq, 2 cq + 1 (8-bit cache: dims 16 ks + 2r (+1))
 #pragma unroll
     for (int ks = 0; ks < kKS; ++ks) o[ks][0] = o[ks][1] = o[ks][2] = o[ks][3] = 0.f;
     float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
+    int vmax = 0;  // (8-bit cache) the largest value scale so far: o is 2^(kWeightShift + 127 - vmax) too large
 
     const int w0 = static_cast<int>((pc.fstart - lo) % kCons);  // consumer of the piece's first page
     const int p_first = pc.p0 + (warp - w0 + kCons) % kCons;    // this warp's first page of the piece
@@ -867,13 +891,24 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
           fence_proxy_async_smem();  // the row stores before the stage's next tensor copy
           __syncwarp();
         }
-        mma_page<kKS>(kt, kt + Geo::kTile, koff, voff, qf, n_valid, a.qscale, o, m0, m1, l0, l1);
+        if constexpr (Geo::kFp8)
+          mma_page_fp8<kKS>(kt, kt + Geo::kTile, smem_u32(scbuf + slot * kScaleBytes), koff, qf, n_valid, qs0, qs1, o,
+                            m0, m1, l0, l1, vmax);
+        else
+          mma_page<kKS>(kt, kt + Geo::kTile, koff, voff, qf, n_valid, a.qscale, o, m0, m1, l0, l1);
       }
       __syncwarp();  // the stage and the p buffer are free again
       if (lane == 0 && !failed) mbar_arrive(&empty[slot]);
       ++k;
     }
 
+    if constexpr (Geo::kFp8) {
+      const float up = field_pow2(vmax - kWeightShift);  // (a warp without pages: o is zero)
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[ks][e] *= up;
+    }
     // ---- warp states: lane (r, cq) holds heads 2 cq, 2 cq + 1 (MMA columns); l summed over r
 #pragma unroll
     for (int m = 4; m < 32; m <<= 1) {
@@ -892,8 +927,8 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
           float* rw = mw + (hd - h0) * kRec;
 #pragma unroll
           for (int ks = 0; ks < kKS; ++ks) {
-            rw[4 + 16 * ks + r] = o[ks][e];
-            rw[4 + 16 * ks + r + 8] = o[ks][e + 2];
+            rw[4 + 16 * ks + (Geo::kFp8 ? 2 * r : r)] = o[ks][e];
+            rw[4 + 16 * ks + (Geo::kFp8 ? 2 * r + 1 : r + 8)] = o[ks][e + 2];
           }
           if (r == 0) {
             rw[0] = e ? m1 : m0;
@@ -1171,6 +1206,7 @@ struct DecodeLaunch {
   const void* v_new;
   const void* k_pages;
   const void* v_pages;
+  const void* scales;  // 8-bit cache only
   const int32_t* block_table;
   const int32_t* seq_lens;
   const float* rope;
@@ -1189,6 +1225,19 @@ struct DecodeLaunch {
 // kernel's group (1, 2, 4 or 8).
 int launch_decode_d64(const DecodeLaunch& c, int G);
 int launch_decode_d128(const DecodeLaunch& c, int G);
+// The same for the 8-bit cache (decode_fp8_d64.cu, decode_fp8_d128.cu).
+int launch_decode_fp8_d64(const DecodeLaunch& c, int G);
+int launch_decode_fp8_d128(const DecodeLaunch& c, int G);
+
+// One instantiation (the 8-bit cache has no fused append: its append quantises whole rows first).
+using DecodeKern = void (*)(const CUtensorMap, const CUtensorMap, const DecodeArgs);
+template <class Geo, bool kFused, bool kRope, bool kPolled>
+constexpr DecodeKern decode_instance() {
+  if constexpr (Geo::kFp8 && kFused)
+    return nullptr;
+  else
+    return decode_kernel<Geo, kFused, kRope, kPolled>;
+}
 
 // Workspace layout of a decode call: status | counters [batch * hkv] (256-byte
 // padded) | counted records [2 * grid][G * (D + 4)] fp32 | polled records
@@ -1202,7 +1251,7 @@ inline size_t decode_counter_bytes(int32_t batch, int hkv) {
 
 template <class Geo>
 int launch_decode_geo(const DecodeLaunch& c) {
-  using GeoW = DecGeo<Geo::D, Geo::G, Geo::kFixed, true>;
+  using GeoW = DecGeo<Geo::D, Geo::G, Geo::kFixed, true, Geo::kFp8>;
   if (c.batch == 0) return PKV_OK;
   if (c.rope != nullptr && c.k_new == nullptr) return PKV_ERR_NULL_ARG;
   // Polled merge when a pair is expected to span at most kPollMax CTAs (equal
@@ -1218,22 +1267,22 @@ int launch_decode_geo(const DecodeLaunch& c) {
   const int grid_used = wide ? (c.num_sms < kMaxGrid ? c.num_sms : kMaxGrid) : grid;
   const bool polled = grid_used <= kPollMax * pairs;
   const size_t smem = wide ? GeoW::smem_bytes(c.batch) : Geo::smem_bytes(c.batch);
-  using Kern = void (*)(const CUtensorMap, const CUtensorMap, const DecodeArgs);
   // (the wide rows are never taken at head_dim 64; they name the narrow kernels there so that
   // no wide head_dim-64 instantiation is built)
   using GW = typename std::conditional<Geo::D == 128, GeoW, Geo>::type;
-  static const Kern kKerns[4][3] = {
-      {decode_kernel<Geo, false, false, false>, decode_kernel<Geo, true, false, false>,
-       decode_kernel<Geo, true, true, false>},
-      {decode_kernel<Geo, false, false, true>, decode_kernel<Geo, true, false, true>,
-       decode_kernel<Geo, true, true, true>},
-      {decode_kernel<GW, false, false, false>, decode_kernel<GW, true, false, false>,
-       decode_kernel<GW, true, true, false>},
-      {decode_kernel<GW, false, false, true>, decode_kernel<GW, true, false, true>,
-       decode_kernel<GW, true, true, true>}};
+  static const DecodeKern kKerns[4][3] = {
+      {decode_instance<Geo, false, false, false>(), decode_instance<Geo, true, false, false>(),
+       decode_instance<Geo, true, true, false>()},
+      {decode_instance<Geo, false, false, true>(), decode_instance<Geo, true, false, true>(),
+       decode_instance<Geo, true, true, true>()},
+      {decode_instance<GW, false, false, false>(), decode_instance<GW, true, false, false>(),
+       decode_instance<GW, true, true, false>()},
+      {decode_instance<GW, false, false, true>(), decode_instance<GW, true, false, true>(),
+       decode_instance<GW, true, true, true>()}};
   const int variant = c.k_new == nullptr ? 0 : c.rope == nullptr ? 1 : 2;
   const int shape = (wide ? 2 : 0) + (polled ? 1 : 0);
-  const Kern kern = kKerns[shape][variant];
+  const DecodeKern kern = kKerns[shape][variant];
+  if (kern == nullptr) return PKV_ERR_UNSUPPORTED;
   static bool attr_set[64][4][3] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -1270,13 +1319,15 @@ int launch_decode_geo(const DecodeLaunch& c) {
   a.num_pages = c.num_pages;
   a.hkv = c.hkv;
   a.gq = c.hq / c.hkv;
+  a.scales = static_cast<const uint8_t*>(c.scales);
   a.status = reinterpret_cast<int*>(ws);
   a.counters = reinterpret_cast<int*>(ws + PKV_STATUS_BYTES);
   a.partials = reinterpret_cast<float*>(ws + PKV_STATUS_BYTES + decode_counter_bytes(c.batch, c.hkv));
   a.tagged = reinterpret_cast<uint32_t*>(reinterpret_cast<unsigned char*>(a.partials) +
                                          static_cast<size_t>(2) * grid * Geo::kPieceB);
   CUtensorMap kmap, vmap;
-  const int rc = encode_page_maps(c.k_pages, c.v_pages, Geo::D, c.num_pages, c.hkv, &kmap, &vmap);
+  const int rc = Geo::kFp8 ? encode_page_maps_fp8(c.k_pages, c.v_pages, Geo::D, c.num_pages, c.hkv, &kmap, &vmap)
+                           : encode_page_maps(c.k_pages, c.v_pages, Geo::D, c.num_pages, c.hkv, &kmap, &vmap);
   if (rc != PKV_OK) return rc;
   const int launch_grid = c.num_sms * occ < kMaxGrid ? c.num_sms * occ : kMaxGrid;
   return launch_pdl(kern, dim3(launch_grid), dim3(kDecThreads), smem, c.stream, kmap, vmap, a) == cudaSuccess

@@ -309,6 +309,144 @@ int pkv_mixed_step_attn(const void* q, const void* k_pages, const void* v_pages,
                              dec_batch > 0 ? &dec : nullptr);
 }
 
+// Longest block table of the 8-bit calls: its positions fit 32 bits.
+constexpr int32_t kMaxTablePages = (1 << 27) - 1;
+
+// Shared by the bf16 and the 8-bit append with rotation (kv_scales is nullptr for the bf16 one).
+static int append_rope(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                       int64_t v_stride, const int32_t* positions, const int32_t* slot_mapping, int32_t n_tokens,
+                       const float* cos_sin, int32_t rope_max_pos, const void* q_weight, const void* k_weight, float eps,
+                       void* q_out, void* k_pages, void* v_pages, void* kv_scales, bool fp8, const pkv_cache_desc* desc,
+                       pkv_stream_t stream, void* workspace, size_t workspace_bytes) {
+  int rc = check_desc_decode(desc);
+  if (rc != PKV_OK) return rc;
+  const long long hq = q != nullptr ? desc->num_q_heads : 0, hkv = desc->num_kv_heads, d = desc->head_dim;
+  if (n_tokens < 0 || static_cast<long long>(n_tokens) * (hq + 2 * hkv) >= (1LL << 31)) return PKV_ERR_BAD_SHAPE;
+  if (!(eps >= 0.f)) return PKV_ERR_BAD_SHAPE;
+  if (cos_sin != nullptr && rope_max_pos < 1) return PKV_ERR_BAD_SHAPE;
+  if (static_cast<long long>(desc->num_pages) * desc->page_size > (1LL << 31)) return PKV_ERR_UNSUPPORTED;
+  if (workspace != nullptr && workspace_bytes < PKV_STATUS_BYTES) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if (n_tokens == 0) return PKV_OK;
+  if (!k_new || !v_new || !slot_mapping || !k_pages || !v_pages || (fp8 && !kv_scales)) return PKV_ERR_NULL_ARG;
+  if ((q != nullptr) != (q_out != nullptr)) return PKV_ERR_NULL_ARG;
+  if (cos_sin != nullptr && positions == nullptr) return PKV_ERR_NULL_ARG;
+  // rows of one token are contiguous; tokens may lie further apart (one token's stride is not used)
+  if (n_tokens > 1 && ((q != nullptr && q_stride < hq * d) || k_stride < hkv * d || v_stride < hkv * d))
+    return PKV_ERR_BAD_SHAPE;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(cos_sin) || !aligned16(q_weight) ||
+      !aligned16(k_weight) || !aligned16(q_out) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(kv_scales))
+    return PKV_ERR_MISALIGNED;
+  if (n_tokens > 1 && ((q != nullptr && q_stride % 8 != 0) || k_stride % 8 != 0 || v_stride % 8 != 0))
+    return PKV_ERR_MISALIGNED;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != PKV_OK) return rc;
+  pkv::AppendRopeArgs a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  a.q_stride = n_tokens > 1 ? q_stride : 0;
+  a.k_stride = n_tokens > 1 ? k_stride : 0;
+  a.v_stride = n_tokens > 1 ? v_stride : 0;
+  a.positions = positions;
+  a.slot_mapping = slot_mapping;
+  a.cos_sin = cos_sin;
+  a.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  a.k_weight = static_cast<const __nv_bfloat16*>(k_weight);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.scales = static_cast<uint8_t*>(kv_scales);
+  a.status = static_cast<int*>(workspace);
+  a.eps = eps;
+  a.n_tokens = n_tokens;
+  a.hq = static_cast<int>(hq);
+  a.hkv = desc->num_kv_heads;
+  a.rope_max_pos = rope_max_pos;
+  a.num_pages = desc->num_pages;
+  return pkv::launch_append_rope(a, desc->head_dim, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int pkv_append_rope(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                    int64_t v_stride, const int32_t* positions, const int32_t* slot_mapping, int32_t n_tokens,
+                    const float* rope_cos_sin, int32_t rope_max_pos, const void* q_weight, const void* k_weight,
+                    float eps, void* q_out, void* k_pages, void* v_pages, const pkv_cache_desc* desc,
+                    pkv_stream_t stream, void* workspace, size_t workspace_bytes) {
+  return append_rope(q, q_stride, k_new, k_stride, v_new, v_stride, positions, slot_mapping, n_tokens, rope_cos_sin,
+                     rope_max_pos, q_weight, k_weight, eps, q_out, k_pages, v_pages, nullptr, false, desc, stream,
+                     workspace, workspace_bytes);
+}
+
+int pkv_append_rope_fp8(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                        int64_t v_stride, const int32_t* positions, const int32_t* slot_mapping, int32_t n_tokens,
+                        const float* rope_cos_sin, int32_t rope_max_pos, const void* q_weight, const void* k_weight,
+                        float eps, void* q_out, void* k_pages, void* v_pages, void* kv_scales,
+                        const pkv_cache_desc* desc, pkv_stream_t stream, void* workspace, size_t workspace_bytes) {
+  return append_rope(q, q_stride, k_new, k_stride, v_new, v_stride, positions, slot_mapping, n_tokens, rope_cos_sin,
+                     rope_max_pos, q_weight, k_weight, eps, q_out, k_pages, v_pages, kv_scales, true, desc, stream,
+                     workspace, workspace_bytes);
+}
+
+int pkv_decode_attn_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
+                        const int32_t* block_table, const int32_t* seq_lens, void* out, float scale,
+                        pkv_stream_t stream, const pkv_cache_desc* desc, int32_t batch, int32_t max_pages_per_seq,
+                        void* workspace, size_t workspace_bytes) {
+  int rc = check_desc_decode(desc);
+  if (rc != PKV_OK) return rc;
+  if (batch < 0 || max_pages_per_seq < 1 || max_pages_per_seq > kMaxTablePages) return PKV_ERR_BAD_SHAPE;
+  if (batch > pkv::decode_max_batch()) return PKV_ERR_UNSUPPORTED;
+  if (!table_fits(batch, max_pages_per_seq, desc->num_kv_heads)) return PKV_ERR_BAD_SHAPE;
+  if (workspace == nullptr) return PKV_ERR_NULL_ARG;
+  if (batch == 0) return PKV_OK;
+  if (!q || !k_pages || !v_pages || !kv_scales || !block_table || !seq_lens || !out) return PKV_ERR_NULL_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(kv_scales) || !aligned16(out) ||
+      !aligned16(workspace))
+    return PKV_ERR_MISALIGNED;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != PKV_OK) return rc;
+  if (workspace_bytes < decode_ws(desc, batch, sms)) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  return pkv::launch_decode_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, scale, desc->num_q_heads,
+                                desc->num_kv_heads, desc->head_dim, batch, max_pages_per_seq, desc->num_pages,
+                                workspace, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int pkv_expand_fp8(const void* k_pages, const void* v_pages, const void* kv_scales, const int32_t* block_table,
+                   const int32_t* seq_lens, int32_t num_seqs, int32_t max_pages_per_seq, void* k_out, void* v_out,
+                   const int32_t* out_block_table, int32_t out_num_pages, const pkv_cache_desc* desc,
+                   pkv_stream_t stream, void* workspace, size_t workspace_bytes) {
+  int rc = check_desc_decode(desc);
+  if (rc != PKV_OK) return rc;
+  if (num_seqs < 0 || max_pages_per_seq < 1 || max_pages_per_seq > kMaxTablePages || out_num_pages < 1)
+    return PKV_ERR_BAD_SHAPE;
+  if (!table_fits(num_seqs, max_pages_per_seq, desc->num_kv_heads)) return PKV_ERR_BAD_SHAPE;
+  if (workspace != nullptr && workspace_bytes < PKV_STATUS_BYTES) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if (num_seqs == 0) return PKV_OK;
+  if (!k_pages || !v_pages || !kv_scales || !block_table || !seq_lens || !k_out || !v_out || !out_block_table)
+    return PKV_ERR_NULL_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(kv_scales) || !aligned16(k_out) || !aligned16(v_out))
+    return PKV_ERR_MISALIGNED;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != PKV_OK) return rc;
+  pkv::ExpandArgs a = {};
+  a.k_pages = static_cast<const uint8_t*>(k_pages);
+  a.v_pages = static_cast<const uint8_t*>(v_pages);
+  a.scales = static_cast<const uint8_t*>(kv_scales);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.out_block_table = out_block_table;
+  a.status = static_cast<int*>(workspace);
+  a.num_seqs = num_seqs;
+  a.max_pages = max_pages_per_seq;
+  a.hkv = desc->num_kv_heads;
+  a.num_pages = desc->num_pages;
+  a.out_pages = out_num_pages;
+  return pkv::launch_expand_fp8(a, desc->head_dim, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int pkv_rope_table(float* table, int32_t max_pos, int32_t head_dim, double theta, pkv_stream_t stream) {
   if (table == nullptr) return PKV_ERR_NULL_ARG;
   if (max_pos < 1 || head_dim < 2 || head_dim > 1024 || (head_dim % 2) != 0 || !(theta > 0.0))

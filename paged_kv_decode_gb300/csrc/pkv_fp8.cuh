@@ -1,0 +1,255 @@
+// pkv_fp8.cuh -- the 8-bit paged KV cache: its number format and the
+// tensor-core MMA step of one of its pages.
+//
+// A cached row x of D values (one token of one KV head, K or V) is stored as D
+// e4m3 values (4 exponent bits, 3 mantissa bits, largest 448, no infinities)
+// and one power of two 2^e, kept as the byte e + 127 (e8m0): x_i = 2^e v_i with
+// e the least integer such that max |x_i| <= 448 * 2^e, and v_i = x_i 2^-e
+// rounded to nearest even. A power of two is enough because e4m3 is itself a
+// floating-point format: against a free scale it costs at most one of the
+// row's 18 binades of range and no precision. In return a value is rounded
+// once, e is found without a division, 2^e v is exact in bf16 and in fp32, and
+// a page's 32 scales per KV head fill one 32-byte memory sector.
+// e is clamped to [kExpMin, kExpMax]: a row below 448 * 2^kExpMin rounds on a
+// fixed grid of 2^(kExpMin - 9), values above 448 * 2^kExpMax saturate (as
+// infinities do), NaN stays NaN and takes no part in the maximum. The clamp
+// keeps the scales normal floats and the weighted sums of values inside fp32's
+// range.
+//
+// Pools: e4m3 [num_pages][num_kv_heads][16][D] for K and for V, scales
+// [num_pages][num_kv_heads][2][16] bytes (16 K rows, then 16 V rows).
+// PTX forms as in the PTX ISA (cvt e4m3x2, ldmatrix, movmatrix, mma.sync).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "pkv_device.cuh"
+#include "pkv_mma.cuh"
+
+namespace pkv {
+
+constexpr int kExpMin = -80;
+constexpr int kExpMax = 100;
+constexpr int kScaleBytes = 2 * kPageSize;  // scales of one (page, KV head): 16 K rows, 16 V rows
+
+// Tensor maps of the 8-bit pools, [page * hkv + KV head][16 rows][head_dim] bytes; one box is a whole
+// (page, KV head) tile of K or V, swizzled over its rows' head_dim bytes (128-byte swizzle at head_dim
+// 128, 64-byte at 64: the layouts swz8() reads). PKV_ERR_UNSUPPORTED past 2^31 tiles.
+int encode_page_maps_fp8(const void* k_pages, const void* v_pages, int head_dim, int num_pages, int hkv,
+                         CUtensorMap* kmap, CUtensorMap* vmap);
+
+// e (clamped) of a row whose largest finite magnitude is `a`. 448 = 1.75 * 2^8: the mantissa decides
+// between floor(log2 a) - 8 and the next; exact for every float, 0 and subnormals land on kExpMin.
+__device__ __forceinline__ int row_exponent(float a) {
+  const uint32_t u = __float_as_uint(a);
+  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(max(e, kExpMin), kExpMax);
+}
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// lo and hi (already scaled) as two e4m3 values, lo in the low byte; to nearest even, saturating
+__device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// two e4m3 values (16 bits) -> two fp16 values, exactly
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+// four e4m3 values (32 bits) -> two pairs
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+// c += a * b, m16n8k16, fp16 operands, fp32 accumulators
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes) with an L2 policy.
+__device__ __forceinline__ void bulk_load_hint(void* smem_dst, const void* gmem_src, uint32_t bytes, uint64_t* bar,
+                                               uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(gmem_src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// Byte offset of 16-byte chunk c (16 dims) of token row t in a swizzled tile of D-byte rows.
+template <int D>
+__device__ __forceinline__ uint32_t swz8(int t, int c) {
+  static_assert(D == 64 || D == 128, "head_dim 64 or 128");
+  return static_cast<uint32_t>(t * D + ((D == 128 ? c ^ (t & 7) : c ^ ((t >> 1) & 3)) << 4));
+}
+
+// This lane's ldmatrix row address inside a tile, per pair of 16-dim chunks i: matrices (tokens 0-7, chunk
+// 2i), (tokens 8-15, 2i), (tokens 0-7, 2i + 1), (tokens 8-15, 2i + 1); the same for K and (transposed) V.
+template <int D>
+__device__ __forceinline__ void fp8_offsets(uint32_t (&off)[D / 32]) {
+  const int lane = threadIdx.x & 31, mi = lane >> 3, mr = lane & 7;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) off[i] = swz8<D>(mr + ((mi & 1) << 3), 2 * i + (mi >> 1));
+}
+
+// The query rows as the B operand of the score product: lane (r, c) holds head r's dims 16 ks + 4c .. 4c + 3
+// (staged at `row`, bf16), as fp16 scaled by the power of two that brings the row's largest value into
+// [1, 2): bf16's 8 significant bits fit fp16's 11, and what falls below fp16's range is under 2^-24 of the
+// row's largest value. qs0, qs1: qscale times the powers taken out of heads 2c and 2c + 1.
+template <int KS>
+__device__ __forceinline__ void fp8_query(uint32_t row, bool live, float qscale, uint32_t (&qf)[KS][2], float& qs0,
+                                          float& qs1) {
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  uint32_t x[KS][2];
+  uint32_t most = 0;  // magnitude bits of the largest value (bf16 magnitudes order as integers)
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      x[ks][e] = live ? lds32(row + (16 * ks + 4 * c + 2 * e) * 2) : 0u;
+      most = max(most, max(x[ks][e] & 0x7fffu, (x[ks][e] >> 16) & 0x7fffu));
+    }
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  // field E of the largest value; the factor 2^(127 - E) and its inverse stay normal floats
+  const uint32_t E = min(max(most >> 7, 1u), 253u);
+  const float down = __uint_as_float((254u - E) << 23), up = __uint_as_float(E << 23);
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float2 f = bf2_to_f2(x[ks][e]);
+      qf[ks][e] = pack_f16x2(f.x * down, f.y * down);
+    }
+  qs0 = qscale * __shfl_sync(0xffffffffu, up, 8 * c);      // lane (2c, 0)
+  qs1 = qscale * __shfl_sync(0xffffffffu, up, 8 * c + 4);  // lane (2c + 1, 0)
+}
+
+// Weights enter the value product 2^kWeightShift above their own size, so that fp16 holds them to 2^-38 of
+// the largest (its subnormals end at 2^-24) while the largest, 2^14, stays below fp16's 65504.
+constexpr int kWeightShift = 14;
+
+// 2^(e - 127) from an exponent field that may have fallen below the normal floats' (then 0)
+__device__ __forceinline__ float field_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(max(e, 0)) << 23); }
+
+// One page: the scores of its 16 tokens for the 8 head columns, the online-softmax update of this lane's
+// heads (2c, 2c + 1), and the value product. kt, vt: shared addresses of the swizzled tiles; st: of the 32
+// scale bytes; nv: its tokens before seq_len.
+//
+// With k_j = 2^(ek_j) k8_j and v_j = 2^(ev_j) v8_j, s_j = qscale 2^(ek_j) <q, k8_j> (log2 domain), the sums
+// are l = sum_j 2^(s_j - m) in fp32, m the running maximum of s, and
+//   o = sum_j [2^(s_j - m) 2^(ev_j - E + kWeightShift)] v8_j
+// on the tensor cores, E the running maximum of ev over the warp's tokens (vmax holds its byte; when it grows
+// o is scaled down with the other rescaling). The key's power multiplies the fp32 score and the value's the
+// fp32 weight, so neither costs a rounding. The e4m3 operands become fp16 in registers (exact), so K and V
+// enter the products unrounded; the bracket is rounded to fp16 (2^-11 of it), tighter than the bf16
+// output's own rounding.
+//
+// ldmatrix moves 16-byte rows of 8 x 16-bit units. For K a lane's 32 bits are dims 4c .. 4c + 3 of token r:
+// as the pairs (k slots 2c, 2c + 1) and (8 + 2c, 9 + 2c) of the A operand, with the query's slots permuted
+// alike. For V, transposed, they are dims 2r, 2r + 1 of tokens 2c and 2c + 1: a byte permute gives the two
+// token pairs, dim 2r as row r of the A operand and dim 2r + 1 as row r + 8, so o[ks] holds dims
+// 16 ks + 2r (elements 0, 1) and 16 ks + 2r + 1 (elements 2, 3).
+template <int KS>
+__device__ __forceinline__ void mma_page_fp8(uint32_t kt, uint32_t vt, uint32_t st, const uint32_t (&off)[KS / 2],
+                                             const uint32_t (&qf)[KS][2], int nv, float qs0, float qs1,
+                                             float (&o)[KS][4], float& m0, float& m1, float& l0, float& l1,
+                                             int& vmax) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const bool v0 = r < nv, v1 = r + 8 < nv;
+  const uint32_t ek0 = lds8(st + r), ek1 = lds8(st + r + 8);
+  const int ev0 = v0 ? static_cast<int>(lds8(st + kPageSize + r)) : 0;
+  const int ev1 = v1 ? static_cast<int>(lds8(st + kPageSize + r + 8)) : 0;
+  float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < KS / 2; ++i) {
+    uint32_t x[4], a0, a1, a2, a3;
+    ldsm4(kt + off[i], x);
+    e4m3x4_to_f16x4(x[0], a0, a2);
+    e4m3x4_to_f16x4(x[1], a1, a3);
+    mma_f16(sa, a0, a1, a2, a3, qf[2 * i][0], qf[2 * i][1]);
+    e4m3x4_to_f16x4(x[2], a0, a2);
+    e4m3x4_to_f16x4(x[3], a1, a3);
+    mma_f16(sb, a0, a1, a2, a3, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+  }
+  const float k0 = __uint_as_float(ek0 << 23), k1 = __uint_as_float(ek1 << 23);  // 2^ek
+  const float s00 = v0 ? (sa[0] + sb[0]) * (k0 * qs0) : -CUDART_INF_F;  // token r, head 2c
+  const float s01 = v0 ? (sa[1] + sb[1]) * (k0 * qs1) : -CUDART_INF_F;  // token r, head 2c + 1
+  const float s10 = v1 ? (sa[2] + sb[2]) * (k1 * qs0) : -CUDART_INF_F;  // token r + 8
+  const float s11 = v1 ? (sa[3] + sb[3]) * (k1 * qs1) : -CUDART_INF_F;
+
+  float x0 = fmaxf(s00, s10), x1 = fmaxf(s01, s11);
+#pragma unroll
+  for (int m = 4; m < 32; m <<= 1) {
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, m));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, m));
+  }
+  const int e_new = max(vmax, __reduce_max_sync(0xffffffffu, max(ev0, ev1)));
+  const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+  const float p00 = ex2(s00 - n0), p01 = ex2(s01 - n1);  // token r
+  const float p10 = ex2(s10 - n0), p11 = ex2(s11 - n1);  // token r + 8
+  const float f0 = field_pow2(ev0 - e_new + kWeightShift + 127), f1 = field_pow2(ev1 - e_new + kWeightShift + 127);
+  const uint32_t pk0 = pack_f16x2(p00 * f0, p01 * f0);
+  const uint32_t pk1 = pack_f16x2(p10 * f1, p11 * f1);
+  if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1 || e_new != vmax)) {
+    const float al0 = ex2(m0 - n0), al1 = ex2(m1 - n1);  // 0 on the first page
+    l0 *= al0;
+    l1 *= al1;
+    const float down = field_pow2(vmax - e_new + 127);
+    const float o0 = al0 * down, o1 = al1 * down;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      o[ks][0] *= o0;
+      o[ks][1] *= o1;
+      o[ks][2] *= o0;
+      o[ks][3] *= o1;
+    }
+    m0 = n0;
+    m1 = n1;
+    vmax = e_new;
+  }
+  l0 += p00 + p10;
+  l1 += p01 + p11;
+
+  const uint32_t pb0 = movm_t(pk0), pb1 = movm_t(pk1);
+  uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;  // value rows past seq_len read as zero
+  if (nv < kPageSize) {
+    mlo = (2 * c < nv ? 0x0000ffffu : 0u) | (2 * c + 1 < nv ? 0xffff0000u : 0u);
+    mhi = (2 * c + 8 < nv ? 0x0000ffffu : 0u) | (2 * c + 9 < nv ? 0xffff0000u : 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < KS / 2; ++i) {
+    uint32_t y[4], a0, a1, a2, a3;
+    ldsm4_t(vt + off[i], y);
+    e4m3x4_to_f16x4(__byte_perm(y[0] & mlo, 0, 0x3120), a0, a1);
+    e4m3x4_to_f16x4(__byte_perm(y[1] & mhi, 0, 0x3120), a2, a3);
+    mma_f16(o[2 * i], a0, a1, a2, a3, pb0, pb1);
+    e4m3x4_to_f16x4(__byte_perm(y[2] & mlo, 0, 0x3120), a0, a1);
+    e4m3x4_to_f16x4(__byte_perm(y[3] & mhi, 0, 0x3120), a2, a3);
+    mma_f16(o[2 * i + 1], a0, a1, a2, a3, pb0, pb1);
+  }
+}
+
+}  // namespace pkv

@@ -1,6 +1,7 @@
 // pkv_kernels.h -- internal launchers behind the C ABI (host side).
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -24,8 +25,48 @@ int launch_decode(const void* q, const void* k_new, const void* v_new, const voi
                   void* out, float scale, int num_q_heads, int num_kv_heads, int head_dim, int32_t batch,
                   int32_t max_pages, int32_t num_pages, void* workspace, int num_sms, cudaStream_t stream,
                   uint32_t flags);
+// The 8-bit cache (decode_fp8_d64.cu, decode_fp8_d128.cu): the same geometries and workspace.
+int launch_decode_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
+                      const int32_t* block_table, const int32_t* seq_lens, void* out, float scale, int num_q_heads,
+                      int num_kv_heads, int head_dim, int32_t batch, int32_t max_pages, int32_t num_pages,
+                      void* workspace, int num_sms, cudaStream_t stream);
 int decode_max_batch();
 
+// Append with the rotary embedding and per-head norm (append_rope.cu): head_dim 64 or 128, page size 16.
+struct AppendRopeArgs {
+  const __nv_bfloat16* q;  // [n_tokens][hq][D], token stride q_stride elements; hq = 0: no query rows
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  long long q_stride, k_stride, v_stride;
+  const int32_t* positions;     // with cos_sin
+  const int32_t* slot_mapping;  // negative: the token's k and v are not written
+  const float* cos_sin;         // [rope_max_pos][D], or nullptr: no rotation
+  const __nv_bfloat16* q_weight;  // [D], or nullptr: no norm
+  const __nv_bfloat16* k_weight;
+  __nv_bfloat16* q_out;  // [n_tokens][hq][D]
+  void* k_pages;         // bf16, or e4m3 where scales is given
+  void* v_pages;
+  uint8_t* scales;
+  int* status;
+  float eps;
+  int n_tokens, hq, hkv, rope_max_pos, num_pages;
+};
+int launch_append_rope(const AppendRopeArgs& a, int head_dim, int num_sms, cudaStream_t stream);
+
+// Pages of the 8-bit cache as bf16 pages (expand_fp8.cu): head_dim 64 or 128, page size 16.
+struct ExpandArgs {
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const uint8_t* scales;
+  const int32_t* block_table;  // [num_seqs][max_pages]
+  const int32_t* seq_lens;
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  const int32_t* out_block_table;
+  int* status;
+  int num_seqs, max_pages, hkv, num_pages, out_pages;
+};
+int launch_expand_fp8(const ExpandArgs& a, int head_dim, int num_sms, cudaStream_t stream);
 
 // Rotary-embedding table (rope.cu): fp32 [max_pos][head_dim], row p = cos(p w_i) for i < head_dim / 2,
 // then sin(p w_i), w_i = theta^(-2 i / head_dim), angles in double rounded to float once.
