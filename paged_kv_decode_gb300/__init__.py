@@ -276,111 +276,148 @@ def _decode_append(q, k_new, v_new, k_pages, v_pages, block_table, seq_lens, out
 
 
 # ---------------------------------------------------------------------------- append with rotation, 8-bit cache
-def _run(what: str, dev, stream, fn, *args):
-    """Call fn(*args with the stream in the place of _STREAM) with `dev` current, on `stream` or dev's current one."""
+# (These calls' kernels are short, so the checks of the good case read each attribute once, in line; only a check that
+# fails goes through the helpers that say why.)
+def _refuse(dev: int, *tensors):
+    """Raise for the first of the (tensor, dtype, name) triples that is not contiguous, of that type and on cuda:dev."""
     import torch
 
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device != dev:
-        raise ValueError(f"{what}: the stream is on {s.device}, the tensors are on {dev}")
-    args = [s.cuda_stream if a is _STREAM else a for a in args]
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args)
+    for t, dtype, name in tensors:
+        _need(t, dtype, name, torch.device("cuda", dev))
+    raise ValueError("bad tensor")  # (not reached: one of them is refused)
+
+
+def _device_of(pool, dtype, name: str) -> int:
+    """Index of the CUDA device that a pool is on."""
+    if pool is None or not pool.is_cuda:
+        _need(pool, dtype, name)
+    return pool.get_device()
+
+
+def _good(t, dtype, dev: int) -> bool:
+    return t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+
+
+def _run(what: str, dev: int, stream, fn, before, after):
+    """fn(*before, stream, *after) with device `dev` current, on `stream` or the device's current one."""
+    import torch
+
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"{what}: the stream is on {stream.device}, the tensors are on cuda:{dev}")
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*before, s, *after)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args)
-    _check(rc, what)
+            rc = fn(*before, s, *after)
+    if rc != PKV_OK:
+        _check(rc, what)
 
 
-_STREAM = object()
-
-
-def _ws(workspace: Optional[Workspace], dev):
+def _ws(workspace: Optional[Workspace], dev: int):
     """(pointer, bytes) of a workspace on dev; (None, 0) without one."""
     if workspace is None:
         return None, 0
     t = workspace.tensor
-    if t.device != dev:
-        raise ValueError(f"the workspace is on {t.device}, expected {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"the workspace is on {t.device}, expected cuda:{dev}")
     return t.data_ptr(), t.numel()
 
 
-def _token_rows(t, name, dev, n: int, heads: Optional[int], d: int) -> int:
+def _token_rows(t, name, dev: int, n: int, heads: int, d: int) -> int:
     """Check the new tokens' rows [n, heads, d] (a token's rows contiguous, tokens any distance apart, as in a fused
     projection's output); returns the elements between tokens."""
     import torch
 
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [{n}, {'heads' if heads is None else heads}, {d}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.shape != (n, heads, d):
+        raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {tuple(t.shape)}")
+    token, head, one = t.stride()
+    if one != 1 or (head != d and heads > 1):
         raise ValueError(f"{name}: the rows of a token must be contiguous")
-    return t.stride(0)
+    return token
 
 
-def _fp8_pools(k_pages, v_pages, kv_scales):
-    """Check the pools and scales of an 8-bit cache; returns their device."""
+def _pool_shape(k_pages, v_pages):
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
+        raise ValueError("pools are [num_pages, num_kv_heads, page_size, head_dim]")
+    return shape
+
+
+def _fp8_cache(k_pages, v_pages, kv_scales):
+    """Check the pools and scales of an 8-bit cache; returns their device's index and the pools' shape."""
     import torch
 
-    _need(k_pages, torch.float8_e4m3fn, "k_pages")
-    dev = k_pages.device
-    _need(v_pages, torch.float8_e4m3fn, "v_pages", dev)
-    _need(kv_scales, torch.float8_e8m0fnu, "kv_scales", dev)
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
-        raise ValueError("pools are [num_pages, num_kv_heads, page_size, head_dim]")
-    p, h, ps, _ = k_pages.shape
+    e4m3, e8m0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    dev = _device_of(k_pages, e4m3, "k_pages")
+    if not (_good(k_pages, e4m3, dev) and _good(v_pages, e4m3, dev) and _good(kv_scales, e8m0, dev)):
+        _refuse(dev, (k_pages, e4m3, "k_pages"), (v_pages, e4m3, "v_pages"), (kv_scales, e8m0, "kv_scales"))
+    shape = _pool_shape(k_pages, v_pages)
+    p, h, ps, _ = shape
     if kv_scales.shape != (p, h, 2, ps):
         raise ValueError(f"kv_scales must be [{p}, {h}, 2, {ps}], got {tuple(kv_scales.shape)}")
-    return dev
+    return dev, shape
 
 
 def _append_rope(what, fn, k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages, kv_scales, workspace, q,
-                 q_out, q_weight, k_weight, eps, stream, dev):
+                 q_out, q_weight, k_weight, eps, stream, dev, shape):
     import torch
 
-    _, hkv, _, d = k_pages.shape
-    _need(slot_mapping, torch.int32, "slot_mapping", dev)
+    i32, bf16 = torch.int32, torch.bfloat16
+    num_pages, hkv, ps, d = shape
+    if not _good(slot_mapping, i32, dev):
+        _refuse(dev, (slot_mapping, i32, "slot_mapping"))
     n = slot_mapping.numel()
     k_stride = _token_rows(k_new, "k_new", dev, n, hkv, d)
     v_stride = _token_rows(v_new, "v_new", dev, n, hkv, d)
-    q_stride = 0
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
+    hq, q_stride, q_ptr, q_out_ptr = hkv, 0, None, None
     if q is not None:
-        q_stride = _token_rows(q, "q", dev, n, None, d)
-        _need(q_out, torch.bfloat16, "q_out", dev)
-        if q_out.shape != q.shape:
+        if q_out is None:
+            raise ValueError("q and q_out come together")
+        if not _good(q_out, bf16, dev):
+            _refuse(dev, (q_out, bf16, "q_out"))
+        out_shape = q_out.shape
+        hq = out_shape[1] if len(out_shape) == 3 else 0
+        q_stride = _token_rows(q, "q", dev, n, hq, d)
+        if out_shape != (n, hq, d):
             raise ValueError("q_out must have q's shape")
-        if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+        if q_out_ptr == q_ptr and not q.is_contiguous():
             raise ValueError("q_out may be q itself only where q is contiguous")
-    elif q_weight is not None:
-        raise ValueError("q_weight without q")
-    max_pos = 0
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight come with q")
+    max_pos, pos_ptr, table_ptr = 0, None, None
     if cos_sin is not None:
-        _need(cos_sin, torch.float32, "cos_sin", dev)
-        if cos_sin.dim() != 2 or cos_sin.shape[1] != d:
+        if not (_good(cos_sin, torch.float32, dev) and _good(positions, i32, dev)):
+            _refuse(dev, (cos_sin, torch.float32, "cos_sin"), (positions, i32, "positions"))
+        table_shape = cos_sin.shape
+        if len(table_shape) != 2 or table_shape[1] != d:
             raise ValueError("cos_sin must be [max_pos, head_dim]")
-        max_pos = cos_sin.shape[0]
-        _need(positions, torch.int32, "positions", dev)
         if positions.numel() != n:
             raise ValueError("positions and slot_mapping differ in length")
+        max_pos, pos_ptr, table_ptr = table_shape[0], positions.data_ptr(), cos_sin.data_ptr()
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, torch.bfloat16, name, dev)
+        if w is not None and not (_good(w, bf16, dev) and w.shape == (d,)):
             if w.shape != (d,):
                 raise ValueError(f"{name} must be [{d}]")
-    ds = _desc_of(k_pages, None if q is None else q.shape[1])
-    ws, nbytes = _ws(workspace, dev)
-    scales = () if kv_scales is None else (kv_scales.data_ptr(),)
-    _run(what, dev, stream, fn, _ptr(q), q_stride, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
-         None if cos_sin is None else positions.data_ptr(), slot_mapping.data_ptr(), n, _ptr(cos_sin), max_pos,
-         _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(), *scales,
-         ctypes.byref(ds), _STREAM, ws, nbytes)
+            _refuse(dev, (w, bf16, name))
+    ds = _lib.CacheDesc(hq, hkv, d, ps, num_pages)
+    before = [q_ptr, q_stride, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, pos_ptr, slot_mapping.data_ptr(),
+              n, table_ptr, max_pos, _ptr(q_weight), _ptr(k_weight), eps, q_out_ptr, k_pages.data_ptr(),
+              v_pages.data_ptr()]
+    if kv_scales is not None:
+        before.append(kv_scales.data_ptr())
+    before.append(ctypes.byref(ds))
+    _run(what, dev, stream, fn, before, _ws(workspace, dev))
 
 
 def append_rope(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages,
@@ -392,13 +429,13 @@ def append_rope(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages
     q_weight / k_weight [D]: RMS norm of each head's row (with eps) before the rotation, as in Qwen3 decoders."""
     import torch
 
-    _need(k_pages, torch.bfloat16, "k_pages")
-    dev = k_pages.device
-    _need(v_pages, torch.bfloat16, "v_pages", dev)
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
-        raise ValueError("pools are [num_pages, num_kv_heads, page_size, head_dim]")
+    bf16 = torch.bfloat16
+    dev = _device_of(k_pages, bf16, "k_pages")
+    if not (_good(k_pages, bf16, dev) and _good(v_pages, bf16, dev)):
+        _refuse(dev, (k_pages, bf16, "k_pages"), (v_pages, bf16, "v_pages"))
     _append_rope("pkv_append_rope", _lib.load().pkv_append_rope, k_new, v_new, positions, slot_mapping, cos_sin, k_pages,
-                 v_pages, None, workspace, q, q_out, q_weight, k_weight, eps, stream, dev)
+                 v_pages, None, workspace, q, q_out, q_weight, k_weight, eps, stream, dev,
+                 _pool_shape(k_pages, v_pages))
 
 
 def append_rope_fp8(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages, kv_scales,
@@ -407,9 +444,9 @@ def append_rope_fp8(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_p
     """append_rope into the 8-bit cache: pools torch.float8_e4m3fn [P, Hkv, 16, D] and kv_scales torch.float8_e8m0fnu
     [P, Hkv, 2, 16] (a power of two per K row, then per V row). Rows are quantised from fp32 (format: include/pkv.h);
     with cos_sin None it is the plain append of the 8-bit cache."""
-    dev = _fp8_pools(k_pages, v_pages, kv_scales)
+    dev, shape = _fp8_cache(k_pages, v_pages, kv_scales)
     _append_rope("pkv_append_rope_fp8", _lib.load().pkv_append_rope_fp8, k_new, v_new, positions, slot_mapping, cos_sin,
-                 k_pages, v_pages, kv_scales, workspace, q, q_out, q_weight, k_weight, eps, stream, dev)
+                 k_pages, v_pages, kv_scales, workspace, q, q_out, q_weight, k_weight, eps, stream, dev, shape)
 
 
 def decode_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, scale: float, workspace: Workspace,
@@ -418,19 +455,19 @@ def decode_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, 
     The workspace is decode_attn's (decode_workspace_bytes) and may serve both in turn."""
     import torch
 
-    dev = _fp8_pools(k_pages, v_pages, kv_scales)
-    _need(q, torch.bfloat16, "q", dev)
-    _need(out, torch.bfloat16, "out", dev)
-    _need(block_table, torch.int32, "block_table", dev)
-    _need(seq_lens, torch.int32, "seq_lens", dev)
-    if q.dim() != 3 or q.shape[2] != k_pages.shape[3] or out.shape != q.shape or block_table.dim() != 2 \
-            or block_table.shape[0] != q.shape[0] or seq_lens.numel() != q.shape[0]:
+    dev, (num_pages, hkv, ps, d) = _fp8_cache(k_pages, v_pages, kv_scales)
+    bf16, i32 = torch.bfloat16, torch.int32
+    if not (_good(q, bf16, dev) and _good(out, bf16, dev) and _good(block_table, i32, dev)
+            and _good(seq_lens, i32, dev)):
+        _refuse(dev, (q, bf16, "q"), (out, bf16, "out"), (block_table, i32, "block_table"), (seq_lens, i32, "seq_lens"))
+    qs, bs = q.shape, block_table.shape
+    if len(qs) != 3 or qs[2] != d or out.shape != qs or len(bs) != 2 or bs[0] != qs[0] or seq_lens.numel() != qs[0]:
         raise ValueError("shape mismatch")
-    d = _desc_of(k_pages, q.shape[1])
+    ds = _lib.CacheDesc(qs[1], hkv, d, ps, num_pages)
     ws, nbytes = _ws(workspace, dev)
-    _run("pkv_decode_attn_fp8", dev, stream, _lib.load().pkv_decode_attn_fp8, q.data_ptr(), k_pages.data_ptr(),
-         v_pages.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-         float(scale), _STREAM, ctypes.byref(d), q.shape[0], block_table.shape[1], ws, nbytes)
+    _run("pkv_decode_attn_fp8", dev, stream, _lib.load().pkv_decode_attn_fp8,
+         (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
+          seq_lens.data_ptr(), out.data_ptr(), scale), (ctypes.byref(ds), qs[0], bs[1], ws, nbytes))
 
 
 def expand_fp8(k_pages, v_pages, kv_scales, block_table, seq_lens, k_out, v_out, out_block_table,
@@ -439,23 +476,23 @@ def expand_fp8(k_pages, v_pages, kv_scales, block_table, seq_lens, k_out, v_out,
     out_block_table [S, max_pages] of k_out / v_out [P', Hkv, 16, D] (what prefill_chunk_attn then reads)."""
     import torch
 
-    dev = _fp8_pools(k_pages, v_pages, kv_scales)
-    _need(k_out, torch.bfloat16, "k_out", dev)
-    _need(v_out, torch.bfloat16, "v_out", dev)
-    _need(block_table, torch.int32, "block_table", dev)
-    _need(out_block_table, torch.int32, "out_block_table", dev)
-    _need(seq_lens, torch.int32, "seq_lens", dev)
-    if k_out.dim() != 4 or k_out.shape[1:] != k_pages.shape[1:] or v_out.shape != k_out.shape:
+    dev, shape = _fp8_cache(k_pages, v_pages, kv_scales)
+    bf16, i32 = torch.bfloat16, torch.int32
+    if not (_good(k_out, bf16, dev) and _good(v_out, bf16, dev) and _good(block_table, i32, dev)
+            and _good(out_block_table, i32, dev) and _good(seq_lens, i32, dev)):
+        _refuse(dev, (k_out, bf16, "k_out"), (v_out, bf16, "v_out"), (block_table, i32, "block_table"),
+                (out_block_table, i32, "out_block_table"), (seq_lens, i32, "seq_lens"))
+    out_shape, bs = k_out.shape, block_table.shape
+    if len(out_shape) != 4 or out_shape[1:] != shape[1:] or v_out.shape != out_shape:
         raise ValueError("k_out and v_out are [pages, num_kv_heads, page_size, head_dim] of the cache's geometry")
-    if block_table.dim() != 2 or out_block_table.shape != block_table.shape \
-            or seq_lens.numel() != block_table.shape[0]:
+    if len(bs) != 2 or out_block_table.shape != bs or seq_lens.numel() != bs[0]:
         raise ValueError("shape mismatch")
-    d = _desc_of(k_pages)
-    ws, nbytes = _ws(workspace, dev)
-    _run("pkv_expand_fp8", dev, stream, _lib.load().pkv_expand_fp8, k_pages.data_ptr(), v_pages.data_ptr(),
-         kv_scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), block_table.shape[0], block_table.shape[1],
-         k_out.data_ptr(), v_out.data_ptr(), out_block_table.data_ptr(), k_out.shape[0], ctypes.byref(d), _STREAM, ws,
-         nbytes)
+    num_pages, hkv, ps, d = shape
+    ds = _lib.CacheDesc(hkv, hkv, d, ps, num_pages)
+    _run("pkv_expand_fp8", dev, stream, _lib.load().pkv_expand_fp8,
+         (k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+          bs[0], bs[1], k_out.data_ptr(), v_out.data_ptr(), out_block_table.data_ptr(), out_shape[0],
+          ctypes.byref(ds)), _ws(workspace, dev))
 
 
 def prefill_chunk_attn(q, k_pages, v_pages, block_table, prefix_lens, cu_q_lens, out, scale: float, max_q_len: int,

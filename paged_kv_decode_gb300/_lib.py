@@ -68,6 +68,8 @@ def header_functions(path: str = HEADER):
 def load():
     """Load libpkv.so (built by paged_kv_decode_gb300.build). Raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

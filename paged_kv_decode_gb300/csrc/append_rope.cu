@@ -15,15 +15,24 @@
 // quantised from the fp32 y as pkv_fp8.cuh says (one rounding, no bf16 in
 // between); value rows are copied or quantised, never rotated.
 //
-// The op reads and writes every row once and is bound by memory. D / 16 lanes
-// take a row, lane l dims 8l .. 8l + 7 and D/2 + 8l .. D/2 + 8l + 7: both halves
-// of a pair are in one lane (no exchange for the rotation), every access is 16
-// bytes, and the row's sum of squares and largest magnitude are 2 or 3 shuffles
-// away. A group of lanes takes up to kRows rows of one kind of one token, so
-// that the table row and the weights are loaded once for them and the loads of
-// all rows are in flight together.
+// The op reads and writes every row once and is bound by memory; what stands in
+// the way is the arithmetic between, so it is kept to about 100 instructions per
+// warp and 4 rows. D / 16 lanes take a row, lane l dims 8l .. 8l + 7 and
+// D/2 + 8l .. D/2 + 8l + 7: both halves of a pair are in one lane (no exchange
+// for the rotation), every access is 16 bytes, and the row's sum of squares and
+// largest magnitude are 2 or 3 shuffles away. The rows that a warp's lanes hold
+// at once (a batch: 4 rows at D = 128, 8 at 64) are all q, all k or all v, so
+// that each kind runs its own straight code, in packed pairs of fp32.
+// The batches of all tokens form one list that the warps split evenly. Each
+// warp keeps the next kDepth of its batches on the way in a shared-memory ring
+// of its own (cp.async; a lane reads back what it copied), with the table rows
+// of their tokens beside them: the bytes in flight do not depend on registers
+// or occupancy, and a token's positions and slots are loaded 32 at a time, so
+// that no batch waits for a chain of loads.
 #include <cuda_runtime.h>
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "pkv_device.cuh"
 #include "pkv_fp8.cuh"
@@ -32,178 +41,316 @@
 namespace pkv {
 namespace {
 
-constexpr int kAppendThreads = 256;
+// Launch shape: on 4096 tokens of 16/8/128 into bf16 (8-bit)
+// pools, rings of 4 / 6 / 8 batches measured 13.6 / 14.0 / 14.5 (13.7 / 14.6 / 15.3) us, and 2 / 3 / 4 / 5 blocks
+// per SM 19.3 / 16.8 / 14.0 / 14.2 us.
+constexpr int kWarps = 4;                // per block
+constexpr int kBlocksPerSm = 4;
+constexpr int kDepth = 4;                // batches on the way per warp
+constexpr int kTables = kDepth / 2 + 2;  // tokens that kDepth + 1 batches touch (a token has at least 2)
+constexpr int kBatchBytes = 1024;        // 32 lanes x 16 values
 
-__device__ __forceinline__ void unpack8(const uint4& x, float* y) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+// A lane's 16 values: pairs 0 .. 3 are dims 8l .. 8l + 7, pairs 4 .. 7 dims D/2 + 8l .. D/2 + 8l + 7.
+struct Row {
+  float2 y[8];
+};
+__device__ __forceinline__ Row unpack(const uint4& lo, const uint4& hi) {
+  return {{bf2_to_f2(lo.x), bf2_to_f2(lo.y), bf2_to_f2(lo.z), bf2_to_f2(lo.w), bf2_to_f2(hi.x), bf2_to_f2(hi.y),
+           bf2_to_f2(hi.z), bf2_to_f2(hi.w)}};
+}
+__device__ __forceinline__ uint4 pack4(const float2* y) {
+  return make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y), pack_bf16x2(y[2].x, y[2].y),
+                    pack_bf16x2(y[3].x, y[3].y));
+}
+__device__ __forceinline__ uint32_t quant4(const float2& a, const float2& b, float f) {
+  const float2 f2 = make_float2(f, f);
+  const float2 x = __fmul2_rn(a, f2), y = __fmul2_rn(b, f2);
+  return static_cast<uint32_t>(to_e4m3x2(x.x, x.y)) | static_cast<uint32_t>(to_e4m3x2(y.x, y.y)) << 16;
+}
+
+// Largest finite magnitude of the row's values (over its lanes).
+template <int L>
+__device__ __forceinline__ float row_max(const Row& x) {
+  float most = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = bf2_to_f2(w[i]);
-    y[2 * i] = f.x;
-    y[2 * i + 1] = f.y;
+  for (int i = 0; i < 8; ++i) most = fmaxf(most, fmaxf(fabsf(x.y[i].x), fabsf(x.y[i].y)));  // (drops NaN)
+#pragma unroll
+  for (int m = 1; m < L; m <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
+  if (__any_sync(0xffffffffu, most == CUDART_INF_F)) {  // rare: again without the infinities
+    float fin = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(x.y[i].x), b = fabsf(x.y[i].y);
+      fin = fmaxf(fin, fmaxf(a < CUDART_INF_F ? a : 0.f, b < CUDART_INF_F ? b : 0.f));
+    }
+#pragma unroll
+    for (int m = 1; m < L; m <<= 1) fin = fmaxf(fin, __shfl_xor_sync(0xffffffffu, fin, m));
+    most = fin;
   }
-}
-__device__ __forceinline__ uint4 pack8(const float* y) {
-  return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                    pack_bf16x2(y[6], y[7]));
-}
-__device__ __forceinline__ uint2 quant8(const float* y, float inv) {
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    w[i] = static_cast<uint32_t>(to_e4m3x2(y[4 * i] * inv, y[4 * i + 1] * inv)) |
-           static_cast<uint32_t>(to_e4m3x2(y[4 * i + 2] * inv, y[4 * i + 3] * inv)) << 16;
-  return make_uint2(w[0], w[1]);
+  return most;
 }
 
-template <int D, bool kFp8, int kRows>
-__global__ void __launch_bounds__(kAppendThreads) append_rope_kernel(const AppendRopeArgs a) {
+// The token's table row: c, s and -s of the lane's 8 pairs.
+struct Turn {
+  float2 c[4], s[4], n[4];
+};
+
+template <int D, bool kFp8>
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) append_rope_kernel(const AppendRopeArgs a) {
   constexpr int L = D / 16;  // lanes per row
+  constexpr int R = 32 / L;  // rows per batch
+  __shared__ __align__(16) unsigned char ring_s[kWarps][kDepth * kBatchBytes];
+  __shared__ __align__(16) unsigned char table_s[kWarps][kTables * D * 4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = lane % L, g = lane / L;
+  const unsigned bq = (a.hq + R - 1) / R, bk = (a.hkv + R - 1) / R;  // batches of a token: bq of q, bk of k, bk of v
+  const unsigned per_token = bq + 2 * bk;
+  const unsigned long long total = static_cast<unsigned long long>(a.n_tokens) * per_token;  // below 2^31 (host check)
+  const unsigned warps = gridDim.x * kWarps, me = blockIdx.x * kWarps + warp;
+  const unsigned lo = static_cast<unsigned>(total * me / warps), hi = static_cast<unsigned>(total * (me + 1) / warps);
+  const uint32_t ring = smem_u32(ring_s[warp]) + lane * 16, ring_end = ring + kDepth * kBatchBytes;
+  const uint32_t table = smem_u32(table_s[warp]);
+  const bool turn = a.cos_sin != nullptr;
+  const unsigned last_token = static_cast<unsigned>(a.n_tokens) - 1;
   grid_dependency_wait();
   allow_dependents();
-  const int lane = threadIdx.x & 31;
-  const int l = lane % L;
-  const unsigned cq = (a.hq + kRows - 1) / kRows, ck = (a.hkv + kRows - 1) / kRows;  // units per token
-  const unsigned per_token = cq + 2 * ck;
-  const unsigned units = static_cast<unsigned>(a.n_tokens) * per_token;  // below 2^31 (host check)
-  const unsigned stride = gridDim.x * (kAppendThreads / L);
-  // (warp-uniform bound: the row reductions shuffle over the whole warp)
-  for (unsigned base = blockIdx.x * (kAppendThreads / L) + (threadIdx.x >> 5) * (32 / L); base < units;
-       base += stride) {
-    const unsigned u = base + lane / L;
-    const bool live = u < units;
-    const unsigned uu = live ? u : units - 1;
-    const unsigned t = uu / per_token;
-    unsigned c = uu - t * per_token;
-    const int kind = c < cq ? 0 : c < cq + ck ? 1 : 2;  // q, k, v
-    c -= kind == 0 ? 0 : kind == 1 ? cq : cq + ck;
-    const int heads = kind == 0 ? a.hq : a.hkv;
-    const int h0 = static_cast<int>(c) * kRows;
-    const __nv_bfloat16* src = kind == 0   ? a.q + t * a.q_stride
-                               : kind == 1 ? a.k_new + t * a.k_stride
-                                           : a.v_new + t * a.v_stride;
-    uint4 xl[kRows], xh[kRows];
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int h = h0 + j < heads ? h0 + j : heads - 1;
-      const uint4* row = reinterpret_cast<const uint4*>(src + static_cast<size_t>(h) * D);
-      xl[j] = row[l];
-      xh[j] = row[L + l];
-    }
-    int slot = -1;
-    if (kind != 0) {
-      slot = __ldg(a.slot_mapping + t);
-      if (slot >= 0 && slot / kPageSize >= a.num_pages) {
-        if (live) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
-        slot = -1;
+  if (lo >= hi) return;
+
+  // Batch i of a token: its kind (0 q, 1 k, 2 v) and how many batches lie before it in that kind.
+  auto place = [&](unsigned i, int& kind, unsigned& before) {
+    kind = i < bq ? 0 : i < bq + bk ? 1 : 2;
+    before = i - (kind == 0 ? 0 : kind == 1 ? bq : bq + bk);
+  };
+  auto batches_of = [&](int kind) { return kind == 0 ? bq : bk; };
+
+  // ---- what is on the way: batch `next`, of kind nkind of token nt, the lane's row nh, goes to ring address nring
+  unsigned next = lo, nt = lo / per_token, nleft;
+  int nkind, nh, ntable = 0;
+  uint32_t nring = ring;
+  const char* nsrc;  // the lane's chunk of row 0 of that kind
+  unsigned pos_base = nt;
+  int pos = 0;  // of token pos_base + lane
+  if (turn) pos = __ldg(a.positions + min(pos_base + lane, last_token));
+  bool fresh = true;  // token nt's table row is still to be copied
+  auto source = [&]() {
+    nsrc = reinterpret_cast<const char*>(nkind == 0   ? a.q + nt * a.q_stride
+                                         : nkind == 1 ? a.k_new + nt * a.k_stride
+                                                      : a.v_new + nt * a.v_stride) +
+           l * 16;
+  };
+  {
+    unsigned before;
+    place(lo - nt * per_token, nkind, before);
+    nleft = batches_of(nkind) - before;
+    nh = before * R + g;
+    source();
+  }
+  auto fetch = [&]() {
+    if (next < hi) {
+      const char* row = nsrc + static_cast<unsigned>(min(nh, (nkind == 0 ? a.hq : a.hkv) - 1) * (D * 2));
+      cp_async16(nring, row);
+      cp_async16(nring + kBatchBytes / 2, row + D);
+      if (fresh && turn) {
+        if (nt - pos_base >= 32) {
+          pos_base = nt;
+          pos = __ldg(a.positions + min(pos_base + lane, last_token));
+        }
+        const int p = min(max(__shfl_sync(0xffffffffu, pos, nt - pos_base), 0), a.rope_max_pos - 1);
+        if (lane < D / 4)
+          cp_async16(table + (ntable * D + lane * 4) * 4, a.cos_sin + static_cast<size_t>(p) * D + lane * 4);
+      }
+      fresh = false;
+      nring += kBatchBytes;
+      if (nring == ring_end) nring = ring;
+      ++next;
+      nh += R;
+      if (--nleft == 0) {
+        nh = g;
+        if (++nkind == 3) {
+          nkind = bq > 0 ? 0 : 1;
+          ++nt;
+          fresh = true;
+          ntable = ntable + 1 == kTables ? 0 : ntable + 1;
+        }
+        nleft = batches_of(nkind);
+        source();
       }
     }
-    const bool turn = a.cos_sin != nullptr && kind != 2;
-    float cs[8], sn[8];
-    if (turn) {
-      int p = __ldg(a.positions + t);
-      if (p < 0 || p >= a.rope_max_pos) {
-        if (live && (kind == 0 || slot >= 0)) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
-        p = p < 0 ? 0 : a.rope_max_pos - 1;
-      }
-      const float4* row = reinterpret_cast<const float4*>(a.cos_sin + static_cast<size_t>(p) * D);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        *reinterpret_cast<float4*>(cs + 4 * i) = __ldg(row + 2 * l + i);
-        *reinterpret_cast<float4*>(sn + 4 * i) = __ldg(row + D / 8 + 2 * l + i);
-      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int j = 0; j < kDepth; ++j) fetch();
+  auto landed = [&]() {  // the oldest batch on the way, and with a token's first batch its table row
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    __syncwarp();
+  };
+
+  // ---- the batches in order
+  unsigned t = lo / per_token, info_base = t;
+  int slots = 0, poss = 0;  // of token info_base + lane
+  auto load_info = [&]() {
+    const unsigned x = min(info_base + lane, last_token);
+    slots = __ldg(a.slot_mapping + x);
+    if (turn) poss = __ldg(a.positions + x);
+  };
+  load_info();
+  uint32_t rring = ring;
+  int rtable = 0;
+  bool enter = true;  // token t's slot and table row are still to be read
+  int in_page = -1;   // slot in its page, -1: k and v are not written
+  size_t tile0 = 0;
+  Turn cs;
+  int weights_of = -1;  // kind whose weights w holds
+  Row w;
+  int kind;
+  unsigned before;
+  place(lo - t * per_token, kind, before);
+
+  // n batches of kind K from the lane's row h on
+  auto batches = [&](auto kind_c, unsigned n, int h) {
+    constexpr int K = decltype(kind_c)::value;
+    constexpr bool kQuant = kFp8 && K != 0;
+    const int heads = K == 0 ? a.hq : a.hkv;
+    const bool norms = K == 0 ? a.q_weight != nullptr : K == 1 ? a.k_weight != nullptr : false;
+    const bool turns = K != 2 && turn;
+    if (norms && weights_of != K) {
+      const uint4* wp = reinterpret_cast<const uint4*>(K == 0 ? a.q_weight : a.k_weight) + l;
+      w = unpack(__ldg(wp), __ldg(wp + L));
+      weights_of = K;
     }
-    const __nv_bfloat16* w = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
-    float wl[8], wh[8];
-    if (w != nullptr) {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + l), wl);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + L + l), wh);
-    }
+    // the lane's chunk of row 0 of that kind of this token; rows of heads are D (q_out) or 16 D (a page) apart
+    constexpr int kElem = kQuant ? 1 : 2;
+    char* out = K == 0 ? reinterpret_cast<char*>(a.q_out + static_cast<size_t>(t) * (a.hq * D))
+                       : static_cast<char*>(K == 1 ? a.k_pages : a.v_pages) +
+                             (tile0 * kPageSize + max(in_page, 0)) * (D * kElem);
+    out += l * 8 * kElem;
+    constexpr int kHeadStep = (K == 0 ? D : kPageSize * D) * kElem;
+#pragma unroll 1
+    for (; n > 0; --n, h += R) {
+      landed();
+      uint4 xl, xh;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(xl.x), "=r"(xl.y), "=r"(xl.z), "=r"(xl.w)
+                   : "r"(rring));
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(xh.x), "=r"(xh.y), "=r"(xh.z), "=r"(xh.w)
+                   : "r"(rring + kBatchBytes / 2));
+      rring += kBatchBytes;
+      if (rring == ring_end) rring = ring;
+      const bool writes = h < heads && (K == 0 || in_page >= 0);
+      char* to = out + static_cast<size_t>(static_cast<unsigned>(h)) * kHeadStep;
+      if (!kQuant && !norms && !turns) {  // copied bit for bit
+        if (writes) {
+          reinterpret_cast<uint4*>(to)[0] = xl;
+          reinterpret_cast<uint4*>(to)[L] = xh;
+        }
+      } else {
+        Row x = unpack(xl, xh);
+        float norm = 1.f;
+        if (norms) {
+          float2 sq = __fmul2_rn(x.y[0], x.y[0]), sr = __fmul2_rn(x.y[1], x.y[1]);
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      float y[16];  // dims 8l .., then D/2 + 8l ..
-      unpack8(xl[j], y);
-      unpack8(xh[j], y + 8);
-      float norm = 1.f;
-      float sq = 0.f;
-      if (w != nullptr) {
+          for (int j = 2; j < 8; j += 2) {
+            sq = __ffma2_rn(x.y[j], x.y[j], sq);
+            sr = __ffma2_rn(x.y[j + 1], x.y[j + 1], sr);
+          }
+          float sum = (sq.x + sq.y) + (sr.x + sr.y);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sq = fmaf(y[i], y[i], sq);
-      }
+          for (int m = 1; m < L; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+          norm = __frsqrt_rn(sum * (1.f / D) + a.eps);
 #pragma unroll
-      for (int m = 1; m < L; m <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-      if (w != nullptr) {
-        norm = __frsqrt_rn(sq * (1.f / D) + a.eps);
+          for (int j = 0; j < 8; ++j) x.y[j] = __fmul2_rn(x.y[j], w.y[j]);
+        }
+        if (turns) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] *= wl[i];
-          y[8 + i] *= wh[i];
+          for (int j = 0; j < 4; ++j) {
+            const float2 x1 = x.y[j], x2 = x.y[4 + j];
+            x.y[j] = __ffma2_rn(x1, cs.c[j], __fmul2_rn(x2, cs.n[j]));
+            x.y[4 + j] = __ffma2_rn(x2, cs.c[j], __fmul2_rn(x1, cs.s[j]));
+          }
+        }
+        if constexpr (kQuant) {
+          // rounding is monotonic: the largest of the rounded products by norm is the largest value's
+          const int e = row_exponent(row_max<L>(x) * norm);
+          const float f8 = norm * pow2i(-e);
+          if (writes) {
+            reinterpret_cast<uint2*>(to)[0] = make_uint2(quant4(x.y[0], x.y[1], f8), quant4(x.y[2], x.y[3], f8));
+            reinterpret_cast<uint2*>(to)[L] = make_uint2(quant4(x.y[4], x.y[5], f8), quant4(x.y[6], x.y[7], f8));
+            if (l == 0) a.scales[(tile0 + h) * kScaleBytes + (K - 1) * kPageSize + in_page] = static_cast<uint8_t>(e + 127);
+          }
+        } else {
+          if (norms) {
+            const float2 n2 = make_float2(norm, norm);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x.y[j] = __fmul2_rn(x.y[j], n2);
+          }
+          if (writes) {
+            reinterpret_cast<uint4*>(to)[0] = pack4(x.y);
+            reinterpret_cast<uint4*>(to)[L] = pack4(x.y + 4);
+          }
         }
       }
+      fetch();
+    }
+  };
+#pragma unroll 1
+  for (unsigned f = lo; f < hi;) {
+    if (enter) {
+      landed();
+      if (t - info_base >= 32) {
+        info_base = t;
+        load_info();
+      }
+      const int slot = __shfl_sync(0xffffffffu, slots, t - info_base);
+      const int p = __shfl_sync(0xffffffffu, poss, t - info_base);
+      const bool inside = slot >= 0 && slot / kPageSize < a.num_pages;
+      if (slot >= 0 && !inside) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
+      if (turn && (p < 0 || p >= a.rope_max_pos) && (a.hq > 0 || inside)) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
+      in_page = inside ? slot % kPageSize : -1;
+      tile0 = static_cast<size_t>(inside ? slot / kPageSize : 0) * a.hkv;
       if (turn) {
+        const float4* row = reinterpret_cast<const float4*>(table_s[warp]) + rtable * (D / 4) + 2 * l;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x1 = y[i], x2 = y[8 + i];
-          y[i] = __fmaf_rn(x1, cs[i], -__fmul_rn(x2, sn[i]));
-          y[8 + i] = __fmaf_rn(x2, cs[i], __fmul_rn(x1, sn[i]));
+        for (int j = 0; j < 2; ++j) {
+          const float4 c = row[j], s = row[D / 8 + j];
+          cs.c[2 * j] = make_float2(c.x, c.y);
+          cs.c[2 * j + 1] = make_float2(c.z, c.w);
+          cs.s[2 * j] = make_float2(s.x, s.y);
+          cs.s[2 * j + 1] = make_float2(s.z, s.w);
+          cs.n[2 * j] = make_float2(-s.x, -s.y);
+          cs.n[2 * j + 1] = make_float2(-s.z, -s.w);
         }
       }
-      if (w != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] *= norm;
-      }
-      const bool mine = live && h0 + j < heads;
-      const int h = h0 + j;
-      if (kind == 0) {
-        if (mine) {
-          uint4* dst = reinterpret_cast<uint4*>(a.q_out + (static_cast<size_t>(t) * a.hq + h) * D);
-          dst[l] = pack8(y);
-          dst[L + l] = pack8(y + 8);
-        }
-      }
-      if constexpr (kFp8) {
-        float most = 0.f;  // over the finite values
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float m = fabsf(y[i]);
-          most = fmaxf(most, m < CUDART_INF_F ? m : 0.f);
-        }
-#pragma unroll
-        for (int m = 1; m < L; m <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
-        if (kind != 0 && mine && slot >= 0) {
-          const int e = row_exponent(most);
-          const float inv = pow2i(-e);
-          const size_t tile = static_cast<size_t>(slot / kPageSize) * a.hkv + h;
-          uint8_t* pool = static_cast<uint8_t*>(kind == 1 ? a.k_pages : a.v_pages);
-          uint2* dst = reinterpret_cast<uint2*>(pool + (tile * kPageSize + slot % kPageSize) * D);
-          dst[l] = quant8(y, inv);
-          dst[L + l] = quant8(y + 8, inv);
-          if (l == 0)
-            a.scales[tile * kScaleBytes + (kind - 1) * kPageSize + slot % kPageSize] = static_cast<uint8_t>(e + 127);
-        }
-      } else if (kind != 0 && mine && slot >= 0) {
-        const size_t tile = static_cast<size_t>(slot / kPageSize) * a.hkv + h;
-        __nv_bfloat16* pool = static_cast<__nv_bfloat16*>(kind == 1 ? a.k_pages : a.v_pages);
-        uint4* dst = reinterpret_cast<uint4*>(pool + (tile * kPageSize + slot % kPageSize) * D);
-        // (value rows and plain key rows keep their bits, NaN payloads included)
-        const bool as_is = kind == 2 || (!turn && w == nullptr);
-        dst[l] = as_is ? xl[j] : pack8(y);
-        dst[L + l] = as_is ? xh[j] : pack8(y + 8);
-      }
+      enter = false;
+    }
+    const unsigned n = min(batches_of(kind) - before, hi - f);
+    const int h = static_cast<int>(before) * R + g;
+    if (kind == 0)
+      batches(std::integral_constant<int, 0>(), n, h);
+    else if (kind == 1)
+      batches(std::integral_constant<int, 1>(), n, h);
+    else
+      batches(std::integral_constant<int, 2>(), n, h);
+    f += n;
+    before = 0;
+    if (++kind == 3) {
+      kind = bq > 0 ? 0 : 1;
+      ++t;
+      enter = true;
+      rtable = rtable + 1 == kTables ? 0 : rtable + 1;
     }
   }
 }
 
-template <int D, bool kFp8, int kRows>
-int launch_rows(const AppendRopeArgs& a, int num_sms, cudaStream_t stream) {
-  const long long units =
-      static_cast<long long>(a.n_tokens) * ((a.hq + kRows - 1) / kRows + 2 * ((a.hkv + kRows - 1) / kRows));
-  const long long per_block = kAppendThreads / (D / 16);
-  long long blocks = (units + per_block - 1) / per_block;
-  const long long cap = static_cast<long long>(num_sms) * 16;
+template <int D, bool kFp8>
+int launch(const AppendRopeArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr int R = 512 / D;
+  const long long batches = static_cast<long long>(a.n_tokens) * ((a.hq + R - 1) / R + 2 * ((a.hkv + R - 1) / R));
+  long long blocks = (batches + kWarps - 1) / kWarps;  // a batch per warp, until every SM is full
+  const long long cap = static_cast<long long>(num_sms) * kBlocksPerSm;
   if (blocks > cap) blocks = cap;
-  return launch_pdl(append_rope_kernel<D, kFp8, kRows>, dim3(static_cast<unsigned>(blocks)), dim3(kAppendThreads), 0,
-                    stream, a) == cudaSuccess
+  return launch_pdl(append_rope_kernel<D, kFp8>, dim3(static_cast<unsigned>(blocks)), dim3(kWarps * 32), 0, stream,
+                    a) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }
@@ -212,10 +359,8 @@ int launch_rows(const AppendRopeArgs& a, int num_sms, cudaStream_t stream) {
 
 int launch_append_rope(const AppendRopeArgs& a, int head_dim, int num_sms, cudaStream_t stream) {
   const bool fp8 = a.scales != nullptr;
-  if (head_dim == 64)
-    return fp8 ? launch_rows<64, true, 2>(a, num_sms, stream) : launch_rows<64, false, 2>(a, num_sms, stream);
-  if (head_dim == 128)
-    return fp8 ? launch_rows<128, true, 2>(a, num_sms, stream) : launch_rows<128, false, 2>(a, num_sms, stream);
+  if (head_dim == 64) return fp8 ? launch<64, true>(a, num_sms, stream) : launch<64, false>(a, num_sms, stream);
+  if (head_dim == 128) return fp8 ? launch<128, true>(a, num_sms, stream) : launch<128, false>(a, num_sms, stream);
   return PKV_ERR_UNSUPPORTED;
 }
 
