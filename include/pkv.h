@@ -221,7 +221,8 @@ int pkv_decode_append_attn(const void* q, const void* k_new, const void* v_new, 
                            void* workspace, size_t workspace_bytes, uint32_t flags);
 
 /*
- * Flag for pkv_decode_append_attn. Every kernel of the library is launched
+ * Flag for pkv_decode_append_attn (pkv_decode_attn_fp8 has a wider promise, see
+ * there). Every kernel of the library is launched
  * with programmatic stream serialisation and normally waits for the previous
  * kernel in the stream before it reads any argument. With this flag the
  * caller promises that the previous kernel writes neither k_pages / v_pages
@@ -381,12 +382,21 @@ int pkv_append_rope_fp8(const void* q, int64_t q_stride, const void* k_new, int6
  * unrounded and the softmax weights rounded to fp16 (2^-12) before they
  * multiply V. Arguments, lengths of zero, errors and the workspace
  * (pkv_decode_workspace_bytes) are pkv_decode_attn's; a workspace may serve
- * both in turn. The kernel waits for the kernel before it (no early prefetch).
+ * both in turn.
+ *
+ *  flags: 0 or PKV_DECODE_EARLY_PREFETCH. Here the caller promises that the
+ *         previous kernel on the stream writes neither block_table nor
+ *         seq_lens, and of the cache at most the rows at position
+ *         seq_lens[b] - 1 of the requests (so pkv_append_rope_fp8 of the
+ *         step's tokens qualifies): the call then copies every request's pages
+ *         but the last two while that kernel is still finishing, and waits for
+ *         it before it reads those, q or anything else. Other bits are
+ *         rejected with PKV_ERR_UNSUPPORTED.
  */
 int pkv_decode_attn_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
                         const int32_t* block_table, const int32_t* seq_lens, void* out, float scale,
                         pkv_stream_t stream, const pkv_cache_desc* desc, int32_t batch, int32_t max_pages_per_seq,
-                        void* workspace, size_t workspace_bytes);
+                        void* workspace, size_t workspace_bytes, uint32_t flags);
 
 /*
  * pkv_expand_fp8 -- pages of the 8-bit cache as bf16 pages, exactly: the

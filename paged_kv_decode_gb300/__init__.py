@@ -450,9 +450,13 @@ def append_rope_fp8(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_p
 
 
 def decode_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, scale: float, workspace: Workspace,
-                    stream=None):
+                    stream=None, early_prefetch: bool = False):
     """decode_attn over the 8-bit cache (pools and kv_scales as for append_rope_fp8): out [B, Hq, D] from q [B, Hq, D].
-    The workspace is decode_attn's (decode_workspace_bytes) and may serve both in turn."""
+    The workspace is decode_attn's (decode_workspace_bytes) and may serve both in turn.
+
+    early_prefetch: the previous kernel on the stream writes neither the block table nor the lengths, and of the
+    cache at most the rows at positions seq_lens - 1 (append_rope_fp8 of the step's tokens), so the other pages may
+    be read while it finishes (PKV_DECODE_EARLY_PREFETCH)."""
     import torch
 
     dev, (num_pages, hkv, ps, d) = _fp8_cache(k_pages, v_pages, kv_scales)
@@ -467,7 +471,8 @@ def decode_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, 
     ws, nbytes = _ws(workspace, dev)
     _run("pkv_decode_attn_fp8", dev, stream, _lib.load().pkv_decode_attn_fp8,
          (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
-          seq_lens.data_ptr(), out.data_ptr(), scale), (ctypes.byref(ds), qs[0], bs[1], ws, nbytes))
+          seq_lens.data_ptr(), out.data_ptr(), scale),
+         (ctypes.byref(ds), qs[0], bs[1], ws, nbytes, EARLY_PREFETCH if early_prefetch else 0))
 
 
 def expand_fp8(k_pages, v_pages, kv_scales, block_table, seq_lens, k_out, v_out, out_block_table,

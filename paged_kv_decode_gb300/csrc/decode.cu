@@ -100,7 +100,7 @@ size_t decode_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, i
 int launch_decode_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
                       const int32_t* block_table, const int32_t* seq_lens, void* out, float scale, int num_q_heads,
                       int num_kv_heads, int head_dim, int32_t batch, int32_t max_pages, int32_t num_pages,
-                      void* workspace, int num_sms, cudaStream_t stream) {
+                      void* workspace, int num_sms, cudaStream_t stream, uint32_t flags) {
   if (!decode_supported(num_q_heads, num_kv_heads, head_dim, kPageSize)) return PKV_ERR_UNSUPPORTED;
   DecodeLaunch c = {};
   c.q = q;
@@ -120,6 +120,7 @@ int launch_decode_fp8(const void* q, const void* k_pages, const void* v_pages, c
   c.workspace = workspace;
   c.num_sms = num_sms;
   c.stream = stream;
+  c.flags = flags;
   const int G = group_pad(num_q_heads / num_kv_heads);
   return head_dim == 64 ? launch_decode_fp8_d64(c, G) : launch_decode_fp8_d128(c, G);
 }

@@ -160,8 +160,9 @@ struct DecodeArgs {
 // CTAs per SM with kRing stages per consumer, or (kWide, for a few long requests)
 // one CTA per SM with twice the stages, so each (request, KV head) has half as
 // many holders to merge and each CTA twice the bytes in flight. kFp8: the 8-bit
-// cache (pkv_fp8.cuh); a page is half as large, so a consumer's ring holds twice
-// as many.
+// cache (pkv_fp8.cuh); its pages are half as large, so the kernel works in units
+// of two pages (a stage holds both, "page" below then means such a unit): a warp's
+// step of 32 tokens pays the softmax's chain of shuffles and the barriers once.
 template <int D_, int G_, bool kFixed_, bool kWide_ = false, bool kFp8_ = false>
 struct DecGeo {
   static constexpr int D = D_;
@@ -174,10 +175,12 @@ struct DecGeo {
   static_assert(G == 1 || G == 2 || G == 4 || G == 8, "one 8-column MMA tile of heads");
   static_assert(!kFixed || (D == kHeadDim && G == kGroup), "the fixed geometry is 16 / 8 / 128");
   static constexpr int kKS = D / 16;                    // 16-dim steps of both MMA products
-  static constexpr int kRing = (D == 128 ? PKV_DEC_RING : 2 * PKV_DEC_RING) * (kWide ? 2 : 1) *
-                               (kFp8 ? 2 : 1);  // per consumer
+  static constexpr int kRing = (D == 128 ? PKV_DEC_RING : 2 * PKV_DEC_RING) * (kWide ? 2 : 1);  // per consumer
   static constexpr int kStages = kCons * kRing;
-  static constexpr int kTile = kPageSize * D * (kFp8 ? 1 : 2);  // one (page, KV head) tile of K or V
+  static constexpr int kUnitPages = kFp8 ? 2 : 1;       // pages per unit of work
+  static constexpr int kUnit = kPageSize * kUnitPages;  // tokens per unit
+  static constexpr int kPageTile = kPageSize * D * (kFp8 ? 1 : 2);  // K or V of a page and KV head
+  static constexpr int kTile = kUnitPages * kPageTile;  // one (page, KV head) tile of K or V
   static constexpr int kStage = 2 * kTile;              // K tile + V tile
   static constexpr int kRowB = D * 2;                   // one query row (and bf16 K or V row)
   static constexpr int kRec = D + 4;                    // floats per query-head record: m, l, pad, pad, o[D]
@@ -194,9 +197,16 @@ struct DecGeo {
   static constexpr int kSmemMerge = kMergeFloats * 4;
   static constexpr int kSmemQ = 2 * kQBuf;              // this piece's rows and the next piece's
   static constexpr int kSmemCs = 2 * kCsB;              // rows for this piece's and the next piece's position
-  static constexpr int kSmemScales = kFp8 ? kStages * kScaleBytes : 0;  // the stages' row scales
+  static constexpr int kSmemScales = kFp8 ? kStages * kUnitPages * kScaleBytes : 0;  // the stages' row scales
   static constexpr int kSmemFixed =
       kSmemAlign + kSmemRing + kSmemBars + kSmemMerge + kSmemQ + kSmemCs + kSmemScales + kSmemMisc;
+  // The 8-bit cache's shape, in units of two pages (16/8/128, us of a step's decode attention): a boundary costs 4 /
+  // 8 / 12 / 16 / 32 units: bs16 14.1 / 13.4 / 14.0 / 14.2 / 16.8; 2 / 3 / 4 / 8 units a round: bs16 14.4 / 13.6 /
+  // 13.4 / 14.1, 40k 19.9 / 19.1 / 19.2 / 19.7; 2 or 3 stages a consumer: bs16 14.3 / 13.4. Shares of one unit: two
+  // requests of 37 and 200 tokens take 6.2 us, 6.7 and 8.4 with at least 2 and 8.
+  static constexpr int kPieceCost = kFp8 ? 8 : PKV_DEC_PIECE_COST;
+  static constexpr int kRound = kFp8 ? 4 : kRoundPages;
+  static constexpr int kShareMin = kFp8 ? 1 : kMinShare;
   static constexpr int kMergeCap = kSmemRing / kPieceB;  // records staged per batch of a counted merge
   // Lane layout of the record merges: 4-word groups of a record's o, group x at words 4x .. 4x + 3
   // (head 4x / D, dims 4x mod D ..); lane l holds groups l, l + 32, ...
@@ -204,7 +214,7 @@ struct DecGeo {
   static constexpr int kLW = kGroups >= 32 ? kGroups / 32 : 1;
   static constexpr int kMergeBatch = 16 / kLW > 8 ? 8 : (16 / kLW < 1 ? 1 : 16 / kLW);  // polled records in flight
   static constexpr int kItems = (kMH * D + kConsThreads - 1) / kConsThreads;  // (head, dim) per thread per pass
-  static_assert(kRoundPages >= 1 && kRoundPages <= kStages, "a page's previous stage use is in an earlier round");
+  static_assert(kRound >= 1 && kRound <= kStages, "a page's previous stage use is in an earlier round");
   static_assert(kSplitB % 16 == 0 && kPieceB % 16 == 0, "16-byte loads, copies and clears of a record");
   static_assert((kSmemRing + kSmemBars) % 16 == 0 && kSmemMerge % 16 == 0 && kQBuf % 16 == 0, "alignment");
   static_assert(kMergeCap >= 1, "a record fits the ring");
@@ -228,16 +238,21 @@ __device__ __forceinline__ int request_of(long long f, const int* pref, int batc
   }
   return lo_b;
 }
-__device__ __forceinline__ int pages_of(int s) { return (s + kPageSize - 1) / kPageSize; }
+// pages (units of kTok tokens) of a length
+template <int kTok>
+__device__ __forceinline__ int pages_of(int s) {
+  return (s + kTok - 1) / kTok;
+}
 
 // Piece of the CTA share [.., hi) that starts at flattened index f.
 // pref[b] = page-head triples of requests before b (pref[batch] = total); sl = clamped lengths.
+template <int kTok>
 __device__ __forceinline__ bool find_piece(long long f, long long hi, const int* pref, const int* sl, int batch,
                                            Piece& pc) {
   if (f >= hi) return false;
   const int b = request_of(f, pref, batch);
   pc.b = b;
-  pc.np = pages_of(sl[b]);
+  pc.np = pages_of<kTok>(sl[b]);
   const long long off = f - pref[b];
   pc.h = static_cast<int>(off / pc.np);
   pc.p0 = static_cast<int>(off % pc.np);
@@ -259,7 +274,7 @@ __device__ __forceinline__ bool find_piece(long long f, long long hi, const int*
 // pages (lo(c) = c T / n). pcp[b] = non-empty pairs before request b. Measured at
 // bs16: kLam 0 / 8 / 16 / 24 / 32 / 40 / 64 gave 18.67 / 18.82 / 18.55 / 18.02 /
 // 17.91 / 18.02 / 18.95 us per layer; the counted merge (one long request) keeps 0.
-template <int kLam>
+template <int kLam, int kTok>
 struct Shares {
   static constexpr int lam = kLam;
   const int* pref;
@@ -296,7 +311,7 @@ struct Shares {
   __device__ __forceinline__ long long cost(long long f) const {  // f < T
     if (kLam == 0) return f;
     const int b = request_of(f, pref, batch);
-    return f + static_cast<long long>(lam) * (pcp[b] + (f - pref[b]) / pages_of(sl[b]));
+    return f + static_cast<long long>(lam) * (pcp[b] + (f - pref[b]) / pages_of<kTok>(sl[b]));
   }
   // first index of CTA c's share: the smallest f with C(f) >= floor(c Ctot / n)
   __device__ __forceinline__ long long lo(int c) const {
@@ -311,7 +326,7 @@ struct Shares {
   }
   // the same, given lb: the last request whose first pair costs at most y
   __device__ __forceinline__ long long lo_in(int lb, long long y) const {
-    const int np = pages_of(sl[lb]);
+    const int np = pages_of<kTok>(sl[lb]);
     if (np == 0) return pref[lb];
     const long long key = pref[lb] + static_cast<long long>(lam) * pcp[lb];
     // (y - key < (np + lam) * hkv < 2^32: the table bound keeps max_pages * hkv below 2^31)
@@ -482,7 +497,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
         }
         sl[b] = s;
       }
-      const int v = pages_of(s) * hkv;
+      const int v = pages_of<Geo::kUnit>(s) * hkv;
       int x = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -511,10 +526,10 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
     // and lo(c + 1) inside their requests.
     __syncwarp();
     const long long Tw = carry;
-    const long long gw = Tw / kMinShare > 0 ? Tw / kMinShare : 1;
+    const long long gw = Tw / Geo::kShareMin > 0 ? Tw / Geo::kShareMin : 1;
     const int nw = static_cast<int>(gw < gridDim.x ? gw : gridDim.x);
     if (static_cast<int>(blockIdx.x) < nw) {
-      Shares<kPolled ? PKV_DEC_PIECE_COST : 0> sw;
+      Shares<kPolled ? Geo::kPieceCost : 0, Geo::kUnit> sw;
       sw.init(pref, pcp, sl, batch, hkv, nw, Tw, pcarry);
       const long long y0 = sw.y_of(blockIdx.x), y1 = sw.y_of(blockIdx.x + 1);
       if (sw.lam == 0) {
@@ -539,7 +554,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
   // dominate); the CTAs between the first and last holder of a (request, KV head)
   // all hold a piece of it.
   const long long T = pref[batch];
-  const long long g_want = T / kMinShare > 0 ? T / kMinShare : 1;
+  const long long g_want = T / Geo::kShareMin > 0 ? T / Geo::kShareMin : 1;
   const int nsh = static_cast<int>(g_want < gridDim.x ? g_want : gridDim.x);
   // zero output rows of empty requests (graph-bucket padding): CTA c clears rows
   // c, c + gridDim.x, ...; in early mode only after the grid dependency
@@ -592,15 +607,24 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       const long long f = f0 + lane;
       const bool valid = f < hi;
       int hh = 0, id = 0, c = 0, wslot = -1, bb = 0;
+      int id2 = 0;       // (8-bit cache) the unit's second page,
+      bool two = false;  // where the request has one
+      bool last = false; // the unit is its request's last
       if (valid) {
         const int b = request_of(f, pref, batch);
-        const int np = pages_of(sl[b]);
+        const int np = pages_of<Geo::kUnit>(sl[b]);
         const int off = static_cast<int>(f - pref[b]);
         hh = off / np;
         const int p = off % np;
         c = static_cast<int>((f - lo) % kCons);
         bb = b;
-        id = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + p);
+        const int* row = a.block_table + static_cast<size_t>(b) * a.max_pages + p * Geo::kUnitPages;
+        id = __ldg(row);
+        if (Geo::kUnitPages == 2 && p * Geo::kUnit + kPageSize < sl[b]) {
+          id2 = __ldg(row + 1);
+          two = true;
+        }
+        last = p == np - 1;
         if (kRope && p == np - 1) wslot = (sl[b] - 1) % kPageSize;  // the new token's slot (rotated append)
       }
       const unsigned same = __match_any_sync(kFull, valid ? c : -1);
@@ -614,7 +638,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       const int k = my_base + idx;
       const int slot = c * kRing + k % kRing;
       const int use = k / kRing;
-      const int my_round = lane / kRoundPages;
+      const int my_round = lane / Geo::kRound;
       int rounds = valid ? my_round + 1 : 0;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) rounds = max(rounds, __shfl_xor_sync(kFull, rounds, o));
@@ -632,11 +656,21 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
               const int z = pid * hkv + hh;  // tile of the pool
               unsigned char* dst = ring + slot * Geo::kStage;
               if constexpr (Geo::kFp8) {
-                mbar_arrive_expect_tx(&full[slot], Geo::kStage + kScaleBytes);
+                constexpr int kPageBytes = 2 * Geo::kPageTile + kScaleBytes;
+                unsigned char* sc = scbuf + slot * (Geo::kUnitPages * kScaleBytes);
+                mbar_arrive_expect_tx(&full[slot], two ? 2 * kPageBytes : kPageBytes);
                 tma_load_3d_hint(dst, &kmap, 0, 0, z, &full[slot], policy);
                 tma_load_3d_hint(dst + Geo::kTile, &vmap, 0, 0, z, &full[slot], policy);
-                bulk_load_hint(scbuf + slot * kScaleBytes, a.scales + static_cast<size_t>(z) * kScaleBytes,
-                               kScaleBytes, &full[slot], policy);
+                bulk_load_hint(sc, a.scales + static_cast<size_t>(z) * kScaleBytes, kScaleBytes, &full[slot], policy);
+                if (two) {
+                  const bool id2_ok = id2 >= 0 && id2 < a.num_pages;
+                  if (!id2_ok) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
+                  const int z2 = (id2_ok ? id2 : 0) * hkv + hh;
+                  tma_load_3d_hint(dst + Geo::kPageTile, &kmap, 0, 0, z2, &full[slot], policy);
+                  tma_load_3d_hint(dst + Geo::kTile + Geo::kPageTile, &vmap, 0, 0, z2, &full[slot], policy);
+                  bulk_load_hint(sc + kScaleBytes, a.scales + static_cast<size_t>(z2) * kScaleBytes, kScaleBytes,
+                                 &full[slot], policy);
+                }
               } else {
                 mbar_arrive_expect_tx(&full[slot], Geo::kStage);
                 // one copy per tile: its D / 64 16-row x 64-dim halves, 128-byte swizzled
@@ -651,7 +685,19 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       // New rows come from the predecessor. Without the rotary embedding the consumer that takes
       // a request's last page writes the new row into the staged page and into the pool, so
       // every page goes out at once, whatever the slot of the new row holds now.
-      if (!kRope) {
+      if constexpr (Geo::kFp8) {
+        // In early mode the predecessor may write the rows at seq_len - 1: the requests' last units wait for it.
+        const unsigned nmask = __ballot_sync(kFull, valid && last);
+        int from = 0;  // lanes already issued
+        if (!waited && nmask != 0u) {
+          from = __ffs(nmask) - 1;
+          issue_rounds(0, from);
+          grid_dependency_wait();
+          allow_dependents();
+          waited = true;
+        }
+        issue_rounds(from, 32);
+      } else if (!kRope) {
         issue_rounds(0, 32);
       } else {
         // With it the whole warp writes the rows: every page of this chunk that holds its
@@ -707,7 +753,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       }
       pfail = __any_sync(kFull, pfail);
     }
-    if (!kRope || !waited) {
+    if (!(kRope || Geo::kFp8) || !waited) {
       grid_dependency_wait();
       allow_dependents();
     }
@@ -748,10 +794,10 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
   // CTAs cfirst .. cfirst + n - 1 hold the pieces of (request b, KV head h); the
   // record of CTA c is in slot 2c, or 2c + 1 when it is the second split piece
   // of c's share (first_has_two: the first holder's share starts before (b, h)).
-  Shares<kPolled ? PKV_DEC_PIECE_COST : 0> sh;
+  Shares<kPolled ? Geo::kPieceCost : 0, Geo::kUnit> sh;
   sh.init(pref, pcp, sl, batch, hkv, nsh, T, pcp[batch]);
   auto span_of = [&](int b, int h, int& cfirst, int& n, bool& first_has_two) {
-    const int np = pages_of(sl[b]);
+    const int np = pages_of<Geo::kUnit>(sl[b]);
     const long long fseg = pref[b] + static_cast<long long>(h) * np;
     cfirst = sh.cta(fseg);
     n = sh.cta(fseg + np - 1) - cfirst + 1;
@@ -766,7 +812,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
   bool pt0 = false, pt1 = false;
 
   Piece pc;
-  bool have = find_piece(lo, hi, pref, sl, batch, pc);
+  bool have = find_piece<Geo::kUnit>(lo, hi, pref, sl, batch, pc);
   // Polled merge: the CTA that holds the last page of a split (request, KV head)
   // merges it; that pair can only be its first piece, begun by an earlier CTA.
   const bool merger = kPolled && have && pc.p0 > 0 && pc.p1 == pc.np;
@@ -787,7 +833,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
   consumer_sync();
   for (int j = 0; have; ++j) {
     Piece nx;
-    const bool have_next = find_piece(pc.fend, hi, pref, sl, batch, nx);
+    const bool have_next = find_piece<Geo::kUnit>(pc.fend, hi, pref, sl, batch, nx);
     if (have_next) stage_q(nx, (j + 1) & 1);
     const int b = pc.b;
     const int h = pc.h;
@@ -874,8 +920,8 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
         }
       }
       if (!failed) {
-        const int rem = sl[b] - p * kPageSize;
-        const int n_valid = rem < kPageSize ? rem : kPageSize;
+        const int rem = sl[b] - p * Geo::kUnit;
+        const int n_valid = rem < Geo::kUnit ? rem : Geo::kUnit;
         const uint32_t kt = smem_u32(ring + slot * Geo::kStage);
         if (takes_new && p == pc.np - 1) {
           const int t = (sl[b] - 1) % kPageSize;  // the new token's slot
@@ -892,8 +938,9 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
           __syncwarp();
         }
         if constexpr (Geo::kFp8)
-          mma_page_fp8<kKS>(kt, kt + Geo::kTile, smem_u32(scbuf + slot * kScaleBytes), koff, qf, n_valid, qs0, qs1, o,
-                            m0, m1, l0, l1, vmax);
+          mma_unit_fp8<kKS, Geo::kUnitPages>(kt, kt + Geo::kTile,
+                                             smem_u32(scbuf + slot * (Geo::kUnitPages * kScaleBytes)), koff, qf,
+                                             n_valid, qs0, qs1, o, m0, m1, l0, l1, vmax);
         else
           mma_page<kKS>(kt, kt + Geo::kTile, koff, voff, qf, n_valid, a.qscale, o, m0, m1, l0, l1);
       }
@@ -1263,13 +1310,14 @@ int launch_decode_geo(const DecodeLaunch& c) {
   const long long pairs = static_cast<long long>(c.batch) * c.hkv;
   // (head_dim 64 stays narrow: with one CTA per SM its consumers, four per SM, page too slowly -- one
   // 40k-token request at 16/8/64 measured 19.0 us per layer wide against 17.8 narrow)
-  const bool wide = Geo::D == 128 && grid > kPollMax * pairs && pairs * c.max_pages >= kWideMinPages;
+  // (nor does the 8-bit cache: one 40k request 24.6 us wide, its one producer per SM short of copies, 19.2 narrow)
+  const bool wide = Geo::D == 128 && !Geo::kFp8 && grid > kPollMax * pairs && pairs * c.max_pages >= kWideMinPages;
   const int grid_used = wide ? (c.num_sms < kMaxGrid ? c.num_sms : kMaxGrid) : grid;
   const bool polled = grid_used <= kPollMax * pairs;
   const size_t smem = wide ? GeoW::smem_bytes(c.batch) : Geo::smem_bytes(c.batch);
   // (the wide rows are never taken at head_dim 64; they name the narrow kernels there so that
   // no wide head_dim-64 instantiation is built)
-  using GW = typename std::conditional<Geo::D == 128, GeoW, Geo>::type;
+  using GW = typename std::conditional<Geo::D == 128 && !Geo::kFp8, GeoW, Geo>::type;
   static const DecodeKern kKerns[4][3] = {
       {decode_instance<Geo, false, false, false>(), decode_instance<Geo, true, false, false>(),
        decode_instance<Geo, true, true, false>()},

@@ -390,7 +390,7 @@ int pkv_append_rope_fp8(const void* q, int64_t q_stride, const void* k_new, int6
 int pkv_decode_attn_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
                         const int32_t* block_table, const int32_t* seq_lens, void* out, float scale,
                         pkv_stream_t stream, const pkv_cache_desc* desc, int32_t batch, int32_t max_pages_per_seq,
-                        void* workspace, size_t workspace_bytes) {
+                        void* workspace, size_t workspace_bytes, uint32_t flags) {
   int rc = check_desc_decode(desc);
   if (rc != PKV_OK) return rc;
   if (batch < 0 || max_pages_per_seq < 1 || max_pages_per_seq > kMaxTablePages) return PKV_ERR_BAD_SHAPE;
@@ -406,9 +406,10 @@ int pkv_decode_attn_fp8(const void* q, const void* k_pages, const void* v_pages,
   rc = current_device(&sms);
   if (rc != PKV_OK) return rc;
   if (workspace_bytes < decode_ws(desc, batch, sms)) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if ((flags & ~static_cast<uint32_t>(PKV_DECODE_EARLY_PREFETCH)) != 0) return PKV_ERR_UNSUPPORTED;
   return pkv::launch_decode_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, scale, desc->num_q_heads,
                                 desc->num_kv_heads, desc->head_dim, batch, max_pages_per_seq, desc->num_pages,
-                                workspace, sms, reinterpret_cast<cudaStream_t>(stream));
+                                workspace, sms, reinterpret_cast<cudaStream_t>(stream), flags);
 }
 
 int pkv_expand_fp8(const void* k_pages, const void* v_pages, const void* kv_scales, const int32_t* block_table,

@@ -154,9 +154,10 @@ constexpr int kWeightShift = 14;
 // 2^(e - 127) from an exponent field that may have fallen below the normal floats' (then 0)
 __device__ __forceinline__ float field_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(max(e, 0)) << 23); }
 
-// One page: the scores of its 16 tokens for the 8 head columns, the online-softmax update of this lane's
-// heads (2c, 2c + 1), and the value product. kt, vt: shared addresses of the swizzled tiles; st: of the 32
-// scale bytes; nv: its tokens before seq_len.
+// One unit of NP pages: the scores of its 16 NP tokens for the 8 head columns, the online-softmax update of
+// this lane's heads (2c, 2c + 1), and the value product. kt, vt: shared addresses of the pages' swizzled
+// tiles, one behind the other; st: of their 32 scale bytes each; nv: the unit's tokens before seq_len (what
+// lies behind them may be anything).
 //
 // With k_j = 2^(ek_j) k8_j and v_j = 2^(ev_j) v8_j, s_j = qscale 2^(ek_j) <q, k8_j> (log2 domain), the sums
 // are l = sum_j 2^(s_j - m) in fp32, m the running maximum of s, and
@@ -172,49 +173,61 @@ __device__ __forceinline__ float field_pow2(int e) { return __uint_as_float(stat
 // alike. For V, transposed, they are dims 2r, 2r + 1 of tokens 2c and 2c + 1: a byte permute gives the two
 // token pairs, dim 2r as row r of the A operand and dim 2r + 1 as row r + 8, so o[ks] holds dims
 // 16 ks + 2r (elements 0, 1) and 16 ks + 2r + 1 (elements 2, 3).
-template <int KS>
-__device__ __forceinline__ void mma_page_fp8(uint32_t kt, uint32_t vt, uint32_t st, const uint32_t (&off)[KS / 2],
+template <int KS, int NP>
+__device__ __forceinline__ void mma_unit_fp8(uint32_t kt, uint32_t vt, uint32_t st, const uint32_t (&off)[KS / 2],
                                              const uint32_t (&qf)[KS][2], int nv, float qs0, float qs1,
                                              float (&o)[KS][4], float& m0, float& m1, float& l0, float& l1,
                                              int& vmax) {
+  constexpr int kTile = kPageSize * KS * 16;  // bytes of a page's K or V
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const bool v0 = r < nv, v1 = r + 8 < nv;
-  const uint32_t ek0 = lds8(st + r), ek1 = lds8(st + r + 8);
-  const int ev0 = v0 ? static_cast<int>(lds8(st + kPageSize + r)) : 0;
-  const int ev1 = v1 ? static_cast<int>(lds8(st + kPageSize + r + 8)) : 0;
-  float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < KS / 2; ++i) {
-    uint32_t x[4], a0, a1, a2, a3;
-    ldsm4(kt + off[i], x);
-    e4m3x4_to_f16x4(x[0], a0, a2);
-    e4m3x4_to_f16x4(x[1], a1, a3);
-    mma_f16(sa, a0, a1, a2, a3, qf[2 * i][0], qf[2 * i][1]);
-    e4m3x4_to_f16x4(x[2], a0, a2);
-    e4m3x4_to_f16x4(x[3], a1, a3);
-    mma_f16(sb, a0, a1, a2, a3, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+  if (nv < kPageSize * NP) {
+    // the request's last unit: value rows behind it become zeros (0 times a stale NaN would be NaN)
+    for (int i = nv * KS + lane; i < kPageSize * NP * KS; i += 32)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vt + i * 16), "r"(0) : "memory");
+    fence_proxy_async_smem();  // before the stage's next tensor copy
+    __syncwarp();
   }
-  const float k0 = __uint_as_float(ek0 << 23), k1 = __uint_as_float(ek1 << 23);  // 2^ek
-  const float s00 = v0 ? (sa[0] + sb[0]) * (k0 * qs0) : -CUDART_INF_F;  // token r, head 2c
-  const float s01 = v0 ? (sa[1] + sb[1]) * (k0 * qs1) : -CUDART_INF_F;  // token r, head 2c + 1
-  const float s10 = v1 ? (sa[2] + sb[2]) * (k1 * qs0) : -CUDART_INF_F;  // token r + 8
-  const float s11 = v1 ? (sa[3] + sb[3]) * (k1 * qs1) : -CUDART_INF_F;
-
-  float x0 = fmaxf(s00, s10), x1 = fmaxf(s01, s11);
+  float s[NP][4];  // tokens r and r + 8 of each page x heads 2c, 2c + 1
+  int ev[NP][2];
+  float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F;
+  int top = 0;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const uint32_t sp = st + p * kScaleBytes;
+    const bool v0 = r < nv - p * kPageSize, v1 = r + 8 < nv - p * kPageSize;
+    const uint32_t ek0 = lds8(sp + r), ek1 = lds8(sp + r + 8);
+    ev[p][0] = v0 ? static_cast<int>(lds8(sp + kPageSize + r)) : 0;
+    ev[p][1] = v1 ? static_cast<int>(lds8(sp + kPageSize + r + 8)) : 0;
+    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < KS / 2; ++i) {
+      uint32_t x[4], a0, a1, a2, a3;
+      ldsm4(kt + p * kTile + off[i], x);
+      e4m3x4_to_f16x4(x[0], a0, a2);
+      e4m3x4_to_f16x4(x[1], a1, a3);
+      mma_f16(sa, a0, a1, a2, a3, qf[2 * i][0], qf[2 * i][1]);
+      e4m3x4_to_f16x4(x[2], a0, a2);
+      e4m3x4_to_f16x4(x[3], a1, a3);
+      mma_f16(sb, a0, a1, a2, a3, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+    }
+    const float k0 = __uint_as_float(ek0 << 23), k1 = __uint_as_float(ek1 << 23);  // 2^ek
+    s[p][0] = v0 ? (sa[0] + sb[0]) * (k0 * qs0) : -CUDART_INF_F;
+    s[p][1] = v0 ? (sa[1] + sb[1]) * (k0 * qs1) : -CUDART_INF_F;
+    s[p][2] = v1 ? (sa[2] + sb[2]) * (k1 * qs0) : -CUDART_INF_F;
+    s[p][3] = v1 ? (sa[3] + sb[3]) * (k1 * qs1) : -CUDART_INF_F;
+    x0 = fmaxf(x0, fmaxf(s[p][0], s[p][2]));
+    x1 = fmaxf(x1, fmaxf(s[p][1], s[p][3]));
+    top = max(top, max(ev[p][0], ev[p][1]));
+  }
 #pragma unroll
   for (int m = 4; m < 32; m <<= 1) {
     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, m));
     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, m));
   }
-  const int e_new = max(vmax, __reduce_max_sync(0xffffffffu, max(ev0, ev1)));
+  const int e_new = max(vmax, __reduce_max_sync(0xffffffffu, top));
   const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-  const float p00 = ex2(s00 - n0), p01 = ex2(s01 - n1);  // token r
-  const float p10 = ex2(s10 - n0), p11 = ex2(s11 - n1);  // token r + 8
-  const float f0 = field_pow2(ev0 - e_new + kWeightShift + 127), f1 = field_pow2(ev1 - e_new + kWeightShift + 127);
-  const uint32_t pk0 = pack_f16x2(p00 * f0, p01 * f0);
-  const uint32_t pk1 = pack_f16x2(p10 * f1, p11 * f1);
   if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1 || e_new != vmax)) {
-    const float al0 = ex2(m0 - n0), al1 = ex2(m1 - n1);  // 0 on the first page
+    const float al0 = ex2(m0 - n0), al1 = ex2(m1 - n1);  // 0 on the first unit
     l0 *= al0;
     l1 *= al1;
     const float down = field_pow2(vmax - e_new + 127);
@@ -230,25 +243,26 @@ __device__ __forceinline__ void mma_page_fp8(uint32_t kt, uint32_t vt, uint32_t 
     m1 = n1;
     vmax = e_new;
   }
-  l0 += p00 + p10;
-  l1 += p01 + p11;
-
-  const uint32_t pb0 = movm_t(pk0), pb1 = movm_t(pk1);
-  uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;  // value rows past seq_len read as zero
-  if (nv < kPageSize) {
-    mlo = (2 * c < nv ? 0x0000ffffu : 0u) | (2 * c + 1 < nv ? 0xffff0000u : 0u);
-    mhi = (2 * c + 8 < nv ? 0x0000ffffu : 0u) | (2 * c + 9 < nv ? 0xffff0000u : 0u);
-  }
 #pragma unroll
-  for (int i = 0; i < KS / 2; ++i) {
-    uint32_t y[4], a0, a1, a2, a3;
-    ldsm4_t(vt + off[i], y);
-    e4m3x4_to_f16x4(__byte_perm(y[0] & mlo, 0, 0x3120), a0, a1);
-    e4m3x4_to_f16x4(__byte_perm(y[1] & mhi, 0, 0x3120), a2, a3);
-    mma_f16(o[2 * i], a0, a1, a2, a3, pb0, pb1);
-    e4m3x4_to_f16x4(__byte_perm(y[2] & mlo, 0, 0x3120), a0, a1);
-    e4m3x4_to_f16x4(__byte_perm(y[3] & mhi, 0, 0x3120), a2, a3);
-    mma_f16(o[2 * i + 1], a0, a1, a2, a3, pb0, pb1);
+  for (int p = 0; p < NP; ++p) {
+    const float p00 = ex2(s[p][0] - n0), p01 = ex2(s[p][1] - n1);  // token r
+    const float p10 = ex2(s[p][2] - n0), p11 = ex2(s[p][3] - n1);  // token r + 8
+    const float f0 = field_pow2(ev[p][0] - e_new + kWeightShift + 127);
+    const float f1 = field_pow2(ev[p][1] - e_new + kWeightShift + 127);
+    l0 += p00 + p10;
+    l1 += p01 + p11;
+    const uint32_t pb0 = movm_t(pack_f16x2(p00 * f0, p01 * f0)), pb1 = movm_t(pack_f16x2(p10 * f1, p11 * f1));
+#pragma unroll
+    for (int i = 0; i < KS / 2; ++i) {
+      uint32_t y[4], a0, a1, a2, a3;
+      ldsm4_t(vt + p * kTile + off[i], y);
+      e4m3x4_to_f16x4(__byte_perm(y[0], 0, 0x3120), a0, a1);
+      e4m3x4_to_f16x4(__byte_perm(y[1], 0, 0x3120), a2, a3);
+      mma_f16(o[2 * i], a0, a1, a2, a3, pb0, pb1);
+      e4m3x4_to_f16x4(__byte_perm(y[2], 0, 0x3120), a0, a1);
+      e4m3x4_to_f16x4(__byte_perm(y[3], 0, 0x3120), a2, a3);
+      mma_f16(o[2 * i + 1], a0, a1, a2, a3, pb0, pb1);
+    }
   }
 }
 

@@ -16,6 +16,7 @@ from paged_kv_decode_gb300 import _lib
 from paged_kv_decode_gb300 import workloads as W
 from paged_kv_decode_gb300.build import build_library
 from parity import bf16_to_f64
+from test_schedule import ShareMap, assign_share, simulate
 
 
 # ---------------------------------------------------------------------------------------------- CPU
@@ -52,7 +53,7 @@ def test_decode_host_argument_checks(lib):
 
     def call(desc=_desc(), q=p, kp=p, vp=p, sc=p, bt=p, sl=p, out=p, batch=2, width=4, ws=p, nb=64):
         return lib.pkv_decode_attn_fp8(q, kp, vp, sc, bt, sl, out, 1.0, None,
-                                       None if desc is None else ctypes.byref(desc), batch, width, ws, nb)
+                                       None if desc is None else ctypes.byref(desc), batch, width, ws, nb, 0)
 
     assert call(desc=None) == -1
     for bad in (_desc(head_dim=96), _desc(page_size=32), _desc(num_q_heads=36, num_kv_heads=4)):
@@ -84,6 +85,41 @@ def test_expand_host_argument_checks(lib):
         assert call(**{name: p + 8}) == -8, name
     assert call(ws=p, nb=8) == -4
     assert call(seqs=0) == 0
+
+
+class Units(ShareMap):
+    """The share map of the 8-bit decode kernel: units of 32 tokens, shares of at least one unit."""
+
+    def __init__(self, seq_lens, grid, lam, hkv=8):
+        super().__init__([(int(s) + 31) // 32 * 16 for s in seq_lens], grid, lam, hkv)  # as many pages as units
+        self.n = min(grid, max(1, self.T))
+
+
+UNIT_MIXES = [[37, 200], [1], [33], [32] * 7, [40000], [0, 700, 0, 33, 1, 2900, 0], list(range(1, 65)),
+              [3, 30000, 5, 9000], [1, 2, 3, 4, 5, 6, 7, 8, 40000], list(W.config_seq_lens(2))]
+
+
+@pytest.mark.parametrize("lam", [0, 8])
+@pytest.mark.parametrize("grid", [7, 152, 304])
+def test_decode_shares_tile_the_units_and_cannot_deadlock(lam, grid):
+    """Every unit in one share, the holders of a (request, KV head) consecutive and non-empty, and the copy schedule
+    (rounds of 4 units) of every share finishes."""
+    for lens in UNIT_MIXES:
+        for hkv in (1, 8):
+            sm = Units(lens, grid, lam, hkv)
+            lo = [sm.lo(c) for c in range(sm.n + 1)]
+            assert lo[0] == 0 and lo[-1] == sm.T and all(a <= b for a, b in zip(lo, lo[1:]))
+            starts = []
+            for b, p in enumerate(sm.pages):
+                for h in range(hkv if p else 0):
+                    fs = sm.pref[b] + h * p
+                    starts.append(fs)
+                    for c in range(sm.cta(fs), sm.cta(fs + p - 1) + 1):
+                        assert lo[c] < lo[c + 1] and lo[c] < fs + p and lo[c + 1] > fs
+            for f in range(0, sm.T, 1 + sm.T // 500):
+                assert lo[sm.cta(f)] <= f < lo[sm.cta(f) + 1]
+            for c in range(sm.n):
+                assert simulate(lo[c], lo[c + 1], starts, assign_share, 4)
 
 
 # ---------------------------------------------------------------------------------------------- GPU
@@ -306,6 +342,58 @@ def test_decode_on_two_streams_and_beside_the_bf16_call(cuda_device):
     a.check("after the bf16 call")
     want = oracle.decode(case.q[0], case.k_pages[0], case.v_pages[0], case.block_table, case.seq_lens, a.scale)
     assert np.abs(bf16_to_f64(out) - want).max() <= 1e-2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("geom", ["16q8kv128", "14q2kv64"])
+@pytest.mark.parametrize("lens", [[1, 16, 17, 32, 33], [500, 0, 1777, 48, 64], [9000]])
+def test_decode_early_prefetch_behind_the_append(cuda_device, geom, lens):
+    """Ten layers of append and decode with early prefetch, replayed as one graph, with each layer's new rows over
+    poison: the outputs and caches are the ones of the same calls without it, bit for bit."""
+    hq, hkv, d = GEOMS[geom]
+    layers, n = 10, len(lens)
+    c = Cache(30, GEOMS[geom], lens, cuda_device)
+    gen = torch.Generator().manual_seed(31)
+    rows = torch.randn(layers, n, hq + 2 * hkv, d, generator=gen).to(torch.bfloat16).to(cuda_device)
+    pos = i32(np.maximum(c.lens, 1) - 1, cuda_device)
+    j = np.maximum(c.lens, 1) - 1
+    slots = np.where(c.lens > 0, c.bt[np.arange(n), j // 16] * 16 + j % 16, -1)
+    for b in range(n):  # the new rows' slots hold NaN until the append has run
+        if slots[b] >= 0:
+            c.k.view(torch.uint8)[slots[b] // 16, :, slots[b] % 16] = NAN_CODE
+            c.s.view(torch.uint8)[slots[b] // 16, :, :, slots[b] % 16] = 0xFF
+    slots = i32(slots, cuda_device)
+    table = pkv.rope_cos_sin(1e6, int(c.lens.max()), d, cuda_device)
+
+    def run(early):
+        caches = [(c.k.clone(), c.v.clone(), c.s.clone()) for _ in range(layers)]
+        q_rot = torch.empty(layers, n, hq, d, dtype=torch.bfloat16, device=cuda_device)
+        outs = torch.full_like(q_rot, float("nan"))
+
+        def chain():
+            for i in range(layers):
+                q, k, v = rows[i, :, :hq], rows[i, :, hq: hq + hkv], rows[i, :, hq + hkv:]
+                pkv.append_rope_fp8(k, v, pos, slots, table, *caches[i], c.ws, q=q, q_out=q_rot[i])
+                pkv.decode_attn_fp8(q_rot[i], *caches[i], c.block_table, c.seq_lens, outs[i], c.scale, c.ws,
+                                    early_prefetch=early)
+
+        if early:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                chain()
+            graph.replay()
+            graph.replay()
+        else:
+            chain()
+        torch.cuda.synchronize()
+        assert c.ws.status() == 0
+        return outs, caches
+
+    want, want_caches = run(False)
+    got, got_caches = run(True)
+    assert torch.isfinite(got.float()).all() and torch.equal(got.view(torch.int16), want.view(torch.int16))
+    for a, b in zip(got_caches, want_caches):
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
 
 
 @pytest.mark.gpu
