@@ -276,150 +276,7 @@ def _decode_append(q, k_new, v_new, k_pages, v_pages, block_table, seq_lens, out
 
 
 # ---------------------------------------------------------------------------- append with rotation, 8-bit cache
-# (These calls' kernels are short, so the checks of the good case read each attribute once, in line; only a check that
-# fails goes through the helpers that say why.)
-def _refuse(dev: int, *tensors):
-    """Raise for the first of the (tensor, dtype, name) triples that is not contiguous, of that type and on cuda:dev."""
-    import torch
-
-    for t, dtype, name in tensors:
-        _need(t, dtype, name, torch.device("cuda", dev))
-    raise ValueError("bad tensor")  # (not reached: one of them is refused)
-
-
-def _device_of(pool, dtype, name: str) -> int:
-    """Index of the CUDA device that a pool is on."""
-    if pool is None or not pool.is_cuda:
-        _need(pool, dtype, name)
-    return pool.get_device()
-
-
-def _good(t, dtype, dev: int) -> bool:
-    return t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
-
-
-def _run(what: str, dev: int, stream, fn, before, after):
-    """fn(*before, stream, *after) with device `dev` current, on `stream` or the device's current one."""
-    import torch
-
-    if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        if stream.device.index != dev:
-            raise ValueError(f"{what}: the stream is on {stream.device}, the tensors are on cuda:{dev}")
-        s = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        rc = fn(*before, s, *after)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*before, s, *after)
-    if rc != PKV_OK:
-        _check(rc, what)
-
-
-def _ws(workspace: Optional[Workspace], dev: int):
-    """(pointer, bytes) of a workspace on dev; (None, 0) without one."""
-    if workspace is None:
-        return None, 0
-    t = workspace.tensor
-    if t.get_device() != dev:
-        raise ValueError(f"the workspace is on {t.device}, expected cuda:{dev}")
-    return t.data_ptr(), t.numel()
-
-
-def _token_rows(t, name, dev: int, n: int, heads: int, d: int) -> int:
-    """Check the new tokens' rows [n, heads, d] (a token's rows contiguous, tokens any distance apart, as in a fused
-    projection's output); returns the elements between tokens."""
-    import torch
-
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    if t.shape != (n, heads, d):
-        raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {tuple(t.shape)}")
-    token, head, one = t.stride()
-    if one != 1 or (head != d and heads > 1):
-        raise ValueError(f"{name}: the rows of a token must be contiguous")
-    return token
-
-
-def _pool_shape(k_pages, v_pages):
-    shape = k_pages.shape
-    if len(shape) != 4 or v_pages.shape != shape:
-        raise ValueError("pools are [num_pages, num_kv_heads, page_size, head_dim]")
-    return shape
-
-
-def _fp8_cache(k_pages, v_pages, kv_scales):
-    """Check the pools and scales of an 8-bit cache; returns their device's index and the pools' shape."""
-    import torch
-
-    e4m3, e8m0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
-    dev = _device_of(k_pages, e4m3, "k_pages")
-    if not (_good(k_pages, e4m3, dev) and _good(v_pages, e4m3, dev) and _good(kv_scales, e8m0, dev)):
-        _refuse(dev, (k_pages, e4m3, "k_pages"), (v_pages, e4m3, "v_pages"), (kv_scales, e8m0, "kv_scales"))
-    shape = _pool_shape(k_pages, v_pages)
-    p, h, ps, _ = shape
-    if kv_scales.shape != (p, h, 2, ps):
-        raise ValueError(f"kv_scales must be [{p}, {h}, 2, {ps}], got {tuple(kv_scales.shape)}")
-    return dev, shape
-
-
-def _append_rope(what, fn, k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages, kv_scales, workspace, q,
-                 q_out, q_weight, k_weight, eps, stream, dev, shape):
-    import torch
-
-    i32, bf16 = torch.int32, torch.bfloat16
-    num_pages, hkv, ps, d = shape
-    if not _good(slot_mapping, i32, dev):
-        _refuse(dev, (slot_mapping, i32, "slot_mapping"))
-    n = slot_mapping.numel()
-    k_stride = _token_rows(k_new, "k_new", dev, n, hkv, d)
-    v_stride = _token_rows(v_new, "v_new", dev, n, hkv, d)
-    hq, q_stride, q_ptr, q_out_ptr = hkv, 0, None, None
-    if q is not None:
-        if q_out is None:
-            raise ValueError("q and q_out come together")
-        if not _good(q_out, bf16, dev):
-            _refuse(dev, (q_out, bf16, "q_out"))
-        out_shape = q_out.shape
-        hq = out_shape[1] if len(out_shape) == 3 else 0
-        q_stride = _token_rows(q, "q", dev, n, hq, d)
-        if out_shape != (n, hq, d):
-            raise ValueError("q_out must have q's shape")
-        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
-        if q_out_ptr == q_ptr and not q.is_contiguous():
-            raise ValueError("q_out may be q itself only where q is contiguous")
-    elif q_out is not None or q_weight is not None:
-        raise ValueError("q_out and q_weight come with q")
-    max_pos, pos_ptr, table_ptr = 0, None, None
-    if cos_sin is not None:
-        if not (_good(cos_sin, torch.float32, dev) and _good(positions, i32, dev)):
-            _refuse(dev, (cos_sin, torch.float32, "cos_sin"), (positions, i32, "positions"))
-        table_shape = cos_sin.shape
-        if len(table_shape) != 2 or table_shape[1] != d:
-            raise ValueError("cos_sin must be [max_pos, head_dim]")
-        if positions.numel() != n:
-            raise ValueError("positions and slot_mapping differ in length")
-        max_pos, pos_ptr, table_ptr = table_shape[0], positions.data_ptr(), cos_sin.data_ptr()
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and not (_good(w, bf16, dev) and w.shape == (d,)):
-            if w.shape != (d,):
-                raise ValueError(f"{name} must be [{d}]")
-            _refuse(dev, (w, bf16, name))
-    ds = _lib.CacheDesc(hq, hkv, d, ps, num_pages)
-    before = [q_ptr, q_stride, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, pos_ptr, slot_mapping.data_ptr(),
-              n, table_ptr, max_pos, _ptr(q_weight), _ptr(k_weight), eps, q_out_ptr, k_pages.data_ptr(),
-              v_pages.data_ptr()]
-    if kv_scales is not None:
-        before.append(kv_scales.data_ptr())
-    before.append(ctypes.byref(ds))
-    _run(what, dev, stream, fn, before, _ws(workspace, dev))
-
-
+# (short kernels: the tensors are checked and the C calls made in csrc/binding.c)
 def append_rope(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages,
                 workspace: Optional[Workspace] = None, q=None, q_out=None, q_weight=None, k_weight=None,
                 eps: float = 1e-6, stream=None):
@@ -427,15 +284,8 @@ def append_rope(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages
     in a fused projection's output) go to slots slot_mapping [n], keys rotated at positions [n] by cos_sin (from
     rope_cos_sin; None: no rotation, positions unused). With q [n, Hq, D] the query rows are rotated into q_out.
     q_weight / k_weight [D]: RMS norm of each head's row (with eps) before the rotation, as in Qwen3 decoders."""
-    import torch
-
-    bf16 = torch.bfloat16
-    dev = _device_of(k_pages, bf16, "k_pages")
-    if not (_good(k_pages, bf16, dev) and _good(v_pages, bf16, dev)):
-        _refuse(dev, (k_pages, bf16, "k_pages"), (v_pages, bf16, "v_pages"))
-    _append_rope("pkv_append_rope", _lib.load().pkv_append_rope, k_new, v_new, positions, slot_mapping, cos_sin, k_pages,
-                 v_pages, None, workspace, q, q_out, q_weight, k_weight, eps, stream, dev,
-                 _pool_shape(k_pages, v_pages))
+    _check(_lib.binding().append_rope(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages, None, workspace,
+                                      q, q_out, q_weight, k_weight, eps, stream), "pkv_append_rope")
 
 
 def append_rope_fp8(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages, kv_scales,
@@ -444,9 +294,8 @@ def append_rope_fp8(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_p
     """append_rope into the 8-bit cache: pools torch.float8_e4m3fn [P, Hkv, 16, D] and kv_scales torch.float8_e8m0fnu
     [P, Hkv, 2, 16] (a power of two per K row, then per V row). Rows are quantised from fp32 (format: include/pkv.h);
     with cos_sin None it is the plain append of the 8-bit cache."""
-    dev, shape = _fp8_cache(k_pages, v_pages, kv_scales)
-    _append_rope("pkv_append_rope_fp8", _lib.load().pkv_append_rope_fp8, k_new, v_new, positions, slot_mapping, cos_sin,
-                 k_pages, v_pages, kv_scales, workspace, q, q_out, q_weight, k_weight, eps, stream, dev, shape)
+    _check(_lib.binding().append_rope_fp8(k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages, kv_scales,
+                                          workspace, q, q_out, q_weight, k_weight, eps, stream), "pkv_append_rope_fp8")
 
 
 def decode_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, scale: float, workspace: Workspace,
@@ -457,47 +306,16 @@ def decode_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, 
     early_prefetch: the previous kernel on the stream writes neither the block table nor the lengths, and of the
     cache at most the rows at positions seq_lens - 1 (append_rope_fp8 of the step's tokens), so the other pages may
     be read while it finishes (PKV_DECODE_EARLY_PREFETCH)."""
-    import torch
-
-    dev, (num_pages, hkv, ps, d) = _fp8_cache(k_pages, v_pages, kv_scales)
-    bf16, i32 = torch.bfloat16, torch.int32
-    if not (_good(q, bf16, dev) and _good(out, bf16, dev) and _good(block_table, i32, dev)
-            and _good(seq_lens, i32, dev)):
-        _refuse(dev, (q, bf16, "q"), (out, bf16, "out"), (block_table, i32, "block_table"), (seq_lens, i32, "seq_lens"))
-    qs, bs = q.shape, block_table.shape
-    if len(qs) != 3 or qs[2] != d or out.shape != qs or len(bs) != 2 or bs[0] != qs[0] or seq_lens.numel() != qs[0]:
-        raise ValueError("shape mismatch")
-    ds = _lib.CacheDesc(qs[1], hkv, d, ps, num_pages)
-    ws, nbytes = _ws(workspace, dev)
-    _run("pkv_decode_attn_fp8", dev, stream, _lib.load().pkv_decode_attn_fp8,
-         (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(),
-          seq_lens.data_ptr(), out.data_ptr(), scale),
-         (ctypes.byref(ds), qs[0], bs[1], ws, nbytes, EARLY_PREFETCH if early_prefetch else 0))
+    _check(_lib.binding().decode_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, scale, workspace,
+                                          stream, EARLY_PREFETCH if early_prefetch else 0), "pkv_decode_attn_fp8")
 
 
 def expand_fp8(k_pages, v_pages, kv_scales, block_table, seq_lens, k_out, v_out, out_block_table,
                workspace: Optional[Workspace] = None, stream=None):
     """Rows before seq_lens [S] of the 8-bit pages block_table [S, max_pages] as bf16, exactly, into pages
     out_block_table [S, max_pages] of k_out / v_out [P', Hkv, 16, D] (what prefill_chunk_attn then reads)."""
-    import torch
-
-    dev, shape = _fp8_cache(k_pages, v_pages, kv_scales)
-    bf16, i32 = torch.bfloat16, torch.int32
-    if not (_good(k_out, bf16, dev) and _good(v_out, bf16, dev) and _good(block_table, i32, dev)
-            and _good(out_block_table, i32, dev) and _good(seq_lens, i32, dev)):
-        _refuse(dev, (k_out, bf16, "k_out"), (v_out, bf16, "v_out"), (block_table, i32, "block_table"),
-                (out_block_table, i32, "out_block_table"), (seq_lens, i32, "seq_lens"))
-    out_shape, bs = k_out.shape, block_table.shape
-    if len(out_shape) != 4 or out_shape[1:] != shape[1:] or v_out.shape != out_shape:
-        raise ValueError("k_out and v_out are [pages, num_kv_heads, page_size, head_dim] of the cache's geometry")
-    if len(bs) != 2 or out_block_table.shape != bs or seq_lens.numel() != bs[0]:
-        raise ValueError("shape mismatch")
-    num_pages, hkv, ps, d = shape
-    ds = _lib.CacheDesc(hkv, hkv, d, ps, num_pages)
-    _run("pkv_expand_fp8", dev, stream, _lib.load().pkv_expand_fp8,
-         (k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-          bs[0], bs[1], k_out.data_ptr(), v_out.data_ptr(), out_block_table.data_ptr(), out_shape[0],
-          ctypes.byref(ds)), _ws(workspace, dev))
+    _check(_lib.binding().expand_fp8(k_pages, v_pages, kv_scales, block_table, seq_lens, k_out, v_out, out_block_table,
+                                     workspace, stream), "pkv_expand_fp8")
 
 
 def prefill_chunk_attn(q, k_pages, v_pages, block_table, prefix_lens, cu_q_lens, out, scale: float, max_q_len: int,

@@ -12,6 +12,7 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "pkv.h")
 
 _lock = threading.Lock()
 _lib = None
+_binding = None
 
 
 class CacheDesc(ctypes.Structure):
@@ -85,3 +86,17 @@ def load():
                 fn.argtypes = args
             _lib = lib
     return _lib
+
+
+def binding():
+    """The compiled binding of the short calls (csrc/binding.c, built with the library). Raises if it is missing."""
+    global _binding
+    if _binding is None:
+        load()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError("the compiled binding is missing or does not load; build it with "
+                               "`python -m paged_kv_decode_gb300.build`") from e
+        _binding = module
+    return _binding

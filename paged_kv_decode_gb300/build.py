@@ -1,7 +1,8 @@
-"""Build libpkv.so in-tree: nvcc for sm_103a, one object per .cu file, compiled in parallel.
+"""Build libpkv.so in-tree: nvcc for sm_103a, one object per .cu file, compiled in parallel;
+and the CPython module of csrc/binding.c (gcc), linked to it.
 
-Usage: ``python -m paged_kv_decode_gb300.build [--force]``. The library is
-placed next to this file; build products are git-ignored.
+Usage: ``python -m paged_kv_decode_gb300.build [--force]``. Both are placed
+next to this file; build products are git-ignored.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build", "pkv")
 LIB = os.path.join(PKG, "libpkv.so")
+BINDING_SRC = os.path.join(CSRC, "binding.c")
+BINDING = os.path.join(PKG, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -56,8 +60,22 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.c against the CPython headers and link it to libpkv.so (found next to it)."""
+    if force or _stale(BINDING, [BINDING_SRC, LIB] + headers()):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = [shutil.which("gcc") or "gcc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC",
+               "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE, BINDING_SRC, "-o", tmp, "-L" + PKG,
+               "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"gcc failed on binding.c:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build_library(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile every csrc/*.cu for sm_103a and link libpkv.so. Returns the library path."""
+    """Compile every csrc/*.cu for sm_103a and link libpkv.so, then the binding. Returns the library path."""
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = sources()
     if force:
@@ -74,6 +92,7 @@ def build_library(force: bool = False, verbose: bool = False, extra=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    build_binding(force)
     if verbose:
         print(LIB)
     return LIB
