@@ -95,8 +95,8 @@ class Units(ShareMap):
         self.n = min(grid, max(1, self.T))
 
 
-UNIT_MIXES = [[37, 200], [1], [33], [32] * 7, [40000], [0, 700, 0, 33, 1, 2900, 0], list(range(1, 65)),
-              [3, 30000, 5, 9000], [1, 2, 3, 4, 5, 6, 7, 8, 40000], list(W.config_seq_lens(2))]
+UNIT_MIXES = [[37, 200], [1], [33], [32] * 7, [9000], [0, 700, 0, 33, 1, 2900, 0], list(range(1, 65)),
+              [3, 8000, 5, 900], [1, 2, 3, 4, 5, 6, 7, 8, 4000], list(W.config_seq_lens(2))[:6]]
 
 
 @pytest.mark.parametrize("lam", [0, 8])
@@ -116,7 +116,7 @@ def test_decode_shares_tile_the_units_and_cannot_deadlock(lam, grid):
                     starts.append(fs)
                     for c in range(sm.cta(fs), sm.cta(fs + p - 1) + 1):
                         assert lo[c] < lo[c + 1] and lo[c] < fs + p and lo[c + 1] > fs
-            for f in range(0, sm.T, 1 + sm.T // 500):
+            for f in range(0, sm.T, 1 + sm.T // 200):
                 assert lo[sm.cta(f)] <= f < lo[sm.cta(f) + 1]
             for c in range(sm.n):
                 assert simulate(lo[c], lo[c + 1], starts, assign_share, 4)
@@ -185,7 +185,7 @@ class Cache:
 GEOMS = {"16q8kv128": (16, 8, 128), "32q32kv128": (32, 32, 128), "28q4kv128": (28, 4, 128), "12q4kv128": (12, 4, 128),
          "64q8kv128": (64, 8, 128), "16q8kv64": (16, 8, 64), "8q1kv64": (8, 1, 64), "32q32kv64": (32, 32, 64),
          "14q2kv64": (14, 2, 64)}
-LENS = {"one": [1], "page": [16], "page_and_one": [17], "odd": [15, 0, 33, 1, 0], "tiny": [37, 200],
+LENS = {"none": [0], "all_empty": [0, 0, 0], "one": [1], "page": [16], "page_and_one": [17], "odd": [15, 0, 33, 1, 0], "tiny": [37, 200],
         "mixed": [3, 700, 0, 64, 1999, 16, 1, 310]}
 
 
@@ -214,6 +214,48 @@ def test_decode_long_and_split(cuda_device, geom, lens, width):
     torch.cuda.synchronize()
     assert torch.equal(first.view(torch.int16), c.out.view(torch.int16))
     assert c.ws.status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("geom", ["16q8kv128", "14q2kv64"])
+@pytest.mark.parametrize("batch", [70, 1024])
+def test_decode_many_short_requests(cuda_device, geom, batch):
+    """More (request, KV head) pairs than CTAs, many of one unit: shares of several whole pairs."""
+    lens = np.random.default_rng(batch).integers(0, 70, size=batch)
+    c = Cache(33, GEOMS[geom], lens, cuda_device)
+    c.step()
+    torch.cuda.synchronize()
+    c.check(geom)
+
+
+@pytest.mark.gpu
+def test_decode_captured_graphs_share_a_workspace(cuda_device):
+    """Two captured steps of different sizes on one workspace, replayed in turn on one stream, inputs changed between."""
+    a = Cache(34, GEOMS["16q8kv128"], [700, 31, 0, 1200], cuda_device)
+    b = Cache(35, GEOMS["16q8kv128"], [9000], cuda_device)
+    big = a.ws if a.ws.nbytes >= b.ws.nbytes else b.ws
+    a.ws = b.ws = big
+    graphs = []
+    for c in (a, b):
+        c.step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.step()
+        graphs.append(g)
+    gen = torch.Generator().manual_seed(36)
+    for _ in range(3):
+        for c, g in ((a, graphs[0]), (b, graphs[1]), (a, graphs[0])):
+            c.q.copy_(torch.randn(c.q.shape, generator=gen).to(torch.bfloat16))
+            c.out.fill_(float("nan"))
+            g.replay()
+            torch.cuda.synchronize()
+            c.check("replay")
+    # fewer live requests than at capture: the rows behind them come back as zeros
+    a.lens = np.array([700, 0, 0, 1200], dtype=np.int32)
+    a.seq_lens.copy_(i32(a.lens, cuda_device))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    a.check("a padded replay")
 
 
 @pytest.mark.gpu
@@ -299,13 +341,19 @@ def test_decode_page_order_does_not_matter(cuda_device):
 @pytest.mark.gpu
 def test_decode_reports_bad_pages_and_lengths(cuda_device):
     c = Cache(27, GEOMS["16q8kv64"], [100, 60], cuda_device)
-    bt = c.bt.copy()
-    bt[0, 2] = c.kc.shape[0]
-    c.block_table = i32(bt, cuda_device)
-    c.step()
-    torch.cuda.synchronize()
-    assert c.ws.status() == -7
-    pkv.workspace_init(c.ws.tensor)
+    for page, bad in ((2, c.kc.shape[0]), (3, -1), (6, 1 << 30)):  # first and second pages of their units
+        bt = c.bt.copy()
+        bt[0, page] = bad
+        c.block_table = i32(bt, cuda_device)
+        c.step()
+        torch.cuda.synchronize()
+        assert c.ws.status() == -7
+        # the other request is not touched by it
+        k, v, q = c.rows(1, 0), c.rows(1, 1), bf16_to_f64(c.q)[1]
+        out, absolute, size = attention64(q, k, v, c.scale)
+        tol = decode_bound(out, absolute, size, c.scale, c.d, 60, np.abs(v).max())
+        assert (np.abs(bf16_to_f64(c.out)[1] - out) <= tol).all()
+        pkv.workspace_init(c.ws.tensor)
     c.block_table = i32(c.bt, cuda_device)
     width = c.bt.shape[1]
     c.seq_lens = i32([100, width * 16 + 1], cuda_device)  # clamped to the table
@@ -417,6 +465,38 @@ def test_expand_is_exact(cuda_device, geom, lens):
             j = np.arange(n)
             wn[out_bt[b, j // 16], :, j % 16] = x
         assert np.array_equal(bits(got), bits(wn))
+    assert c.ws.status() == 0
+
+
+@pytest.mark.gpu
+def test_binding_refuses_bad_tensors(cuda_device):
+    c = Cache(37, GEOMS["16q8kv128"], [40, 20], cuda_device)
+    ok = dict(q=c.q, k_pages=c.k, v_pages=c.v, kv_scales=c.s, block_table=c.block_table, seq_lens=c.seq_lens, out=c.out,
+              scale=c.scale, workspace=c.ws)
+    pkv.decode_attn_fp8(**ok)
+    for bad, error in ((dict(q=c.q.float()), TypeError), (dict(k_pages=c.k.view(torch.uint8)), TypeError),
+                       (dict(kv_scales=c.s.view(torch.uint8)), TypeError), (dict(v_pages=c.v[:-1]), ValueError),
+                       (dict(kv_scales=c.s[:, :, :, :8].contiguous()), ValueError), (dict(out=c.out[:1]), ValueError),
+                       (dict(q=c.q[:, :, :64].contiguous()), ValueError), (dict(q=c.q.transpose(0, 1)), ValueError),
+                       (dict(seq_lens=c.seq_lens[:1]), ValueError), (dict(seq_lens=c.seq_lens.long()), TypeError),
+                       (dict(block_table=c.block_table[:1]), ValueError), (dict(block_table=c.block_table[0]), ValueError),
+                       (dict(q=c.q.cpu()), ValueError), (dict(out=None), ValueError),
+                       (dict(workspace=pkv.Workspace(256, cuda_device)), pkv.PkvError),
+                       (dict(workspace=None), pkv.PkvError)):
+        with pytest.raises(error):
+            pkv.decode_attn_fp8(**{**ok, **bad})
+    pages = c.bt.size
+    stage = torch.zeros(pages, 8, 16, 128, dtype=torch.bfloat16, device=cuda_device)
+    ident = i32(np.arange(pages).reshape(c.bt.shape), cuda_device)
+    ok = dict(k_pages=c.k, v_pages=c.v, kv_scales=c.s, block_table=c.block_table, seq_lens=c.seq_lens, k_out=stage,
+              v_out=stage.clone(), out_block_table=ident)
+    pkv.expand_fp8(**ok)
+    for bad, error in ((dict(k_out=stage.float()), TypeError), (dict(k_out=stage[:1]), ValueError),
+                       (dict(v_out=stage[:, :4].contiguous()), ValueError), (dict(out_block_table=ident[:1]), ValueError),
+                       (dict(out_block_table=ident.long()), TypeError), (dict(seq_lens=c.seq_lens[:1]), ValueError)):
+        with pytest.raises(error):
+            pkv.expand_fp8(**{**ok, **bad})
+    torch.cuda.synchronize()
     assert c.ws.status() == 0
 
 
