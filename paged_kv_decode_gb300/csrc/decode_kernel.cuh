@@ -53,6 +53,17 @@
 //    pages before its first new-row page are copied before the warp waits.
 //    Each piece's query rows are rotated the same way after they are staged
 //    (then rounded to bf16 as the MMA operand).
+//  * The 8-bit cache (DecGeo::kFp8; its format and its MMA step are in
+//    pkv_fp8.cuh) runs the same schedule over units of two pages, a unit's row
+//    scales copied beside its tiles. Measured on one GB300 (a CUDA graph of
+//    calls, each waiting for the one before): 16 requests of 300 to 3000 tokens
+//    13.4 us (50.5 MB; 7.5 us at the measured copy rate), one of 40k tokens
+//    19.2 us (82.6 MB; 12.3), 27 of 9 to 8000 at 32 query / 8 KV heads 37.3 us
+//    (212 MB; 31.7). Of the first, 1.8 us pass before the first copies go out
+//    (the wait, the length scan, the block table), 8.2 stream at 6.1 TB/s and
+//    1.5 end and merge the split pieces. There is no fused append (a row is
+//    quantised as a whole first); in early mode the requests' last units, which
+//    hold the new rows, wait for the predecessor.
 //  * The query rows of the next piece are copied into shared memory (cp.async)
 //    while the current piece streams, so a piece boundary costs no round trip.
 //  * At the end of a piece the warps merge through shared memory (at most four
