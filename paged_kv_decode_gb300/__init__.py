@@ -10,7 +10,8 @@ Layout (see include/pkv.h): pools bf16 [num_pages, Hkv, 16, D]; q / out bf16
 [rows, Hq, D]; block tables int32 [rows, max_pages]; lengths int32. The Qwen3
 decoder's 16/8/128 runs the tuned kernels; append, decode, the fused append +
 decode call and chunked prefill also take head_dim 64 or 128 with 1 to 8 query
-heads per KV head.
+heads per KV head. The 8-bit cache: pools float8_e4m3fn of the same shape and
+float8_e8m0fnu scales [num_pages, Hkv, 2, 16].
 """
 from __future__ import annotations
 
