@@ -27,7 +27,7 @@
 //    stage ring after it) and a split piece's merge waits on its other holders.
 //  * A CTA's share is cut into pieces, one per (request, KV head) it touches.
 //    Its consumer warps take the share's pages round-robin (page f of the share
-//    goes to consumer (f - lo) mod kCons, across piece boundaries). A producer warp
+//    goes to consumer (f - lo) mod kConsumers, across piece boundaries). A producer warp
 //    fills each consumer's ring of shared-memory stages with tiled TMA copies
 //    (cp.async.bulk.tensor, per page one copy of the K tile and one of the V
 //    tile, each head_dim / 64 swizzled 16-row x 64-dim halves, evict-first)
@@ -58,7 +58,7 @@
 //    scales copied beside its tiles. Measured on one GB300 (a CUDA graph of
 //    calls, each waiting for the one before): 16 requests of 300 to 3000 tokens
 //    13.4 us (50.5 MB; 7.5 us at the measured copy rate), one of 40k tokens
-//    19.2 us (82.6 MB; 12.3), 27 of 9 to 8000 at 32 query / 8 KV heads 37.3 us
+//    17.8 us (82.6 MB; 12.3), 27 of 9 to 8000 at 32 query / 8 KV heads 37.3 us
 //    (212 MB; 31.7). Of the first, 1.8 us pass before the first copies go out
 //    (the wait, the length scan, the block table), 8.2 stream at 6.1 TB/s and
 //    1.5 end and merge the split pieces. There is no fused append (a row is
@@ -181,13 +181,21 @@ struct DecGeo {
   static constexpr bool kFixed = kFixed_;
   static constexpr bool kWide = kWide_;
   static constexpr bool kFp8 = kFp8_;
+  // Consumer and producer warps. A producer feeds its own kFed consumers (unit f of the share goes to consumer
+  // (f - lo) mod kConsumers), so each half of an 8-bit wide CTA runs the schedule of a narrow CTA, and the halves
+  // meet only at piece boundaries.
+  static constexpr int kProducers = kFp8 && kWide ? 2 : 1;
+  static constexpr int kConsumers = kCons * kProducers;
+  static constexpr int kFed = kConsumers / kProducers;
+  static constexpr int kConsumerThreads = kConsumers * 32;
+  static constexpr int kThreads = kConsumerThreads + kProducers * 32;
   static constexpr int kCtasPerSm = kWide ? 1 : kDecCtasPerSm;
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
   static_assert(G == 1 || G == 2 || G == 4 || G == 8, "one 8-column MMA tile of heads");
   static_assert(!kFixed || (D == kHeadDim && G == kGroup), "the fixed geometry is 16 / 8 / 128");
   static constexpr int kKS = D / 16;                    // 16-dim steps of both MMA products
-  static constexpr int kRing = (D == 128 ? PKV_DEC_RING : 2 * PKV_DEC_RING) * (kWide ? 2 : 1);  // per consumer
-  static constexpr int kStages = kCons * kRing;
+  static constexpr int kRing = (D == 128 ? PKV_DEC_RING : 2 * PKV_DEC_RING) * (kWide && !kFp8 ? 2 : 1);  // per consumer
+  static constexpr int kStages = kConsumers * kRing;
   static constexpr int kUnitPages = kFp8 ? 2 : 1;       // pages per unit of work
   static constexpr int kUnit = kPageSize * kUnitPages;  // tokens per unit
   static constexpr int kPageTile = kPageSize * D * (kFp8 ? 1 : 2);  // K or V of a page and KV head
@@ -199,12 +207,13 @@ struct DecGeo {
   static constexpr int kPieceB = kPiece * 4;
   static constexpr int kSplitWords = G * D + 4 * G;     // polled record: o[G][D], then m_hi, m_lo, l_hi,
   static constexpr int kSplitB = kSplitWords * 4;       // l_lo of each head
-  static constexpr int kMH = G < 4 ? G : 4;             // heads per pass through the merge buffer
+  static constexpr int kMHMax = kConsumers > 4 ? 2 : 4;
+  static constexpr int kMH = G < kMHMax ? G : kMHMax;   // heads per pass through the merge buffer
   static constexpr int kQBuf = G * D * 2;               // query rows of one (request, KV head)
   static constexpr int kCsB = D * 4;                    // one cos/sin table row
   static constexpr int kSmemRing = kStages * kStage;
   static constexpr int kSmemBars = 2 * kStages * 8;     // full + empty barrier per stage
-  static constexpr int kMergeFloats = kCons * kMH * kRec;
+  static constexpr int kMergeFloats = kConsumers * kMH * kRec;
   static constexpr int kSmemMerge = kMergeFloats * 4;
   static constexpr int kSmemQ = 2 * kQBuf;              // this piece's rows and the next piece's
   static constexpr int kSmemCs = 2 * kCsB;              // rows for this piece's and the next piece's position
@@ -213,7 +222,7 @@ struct DecGeo {
       kSmemAlign + kSmemRing + kSmemBars + kSmemMerge + kSmemQ + kSmemCs + kSmemScales + kSmemMisc;
   // The 8-bit cache's shape, in units of two pages (16/8/128, us of a step's decode attention): a boundary costs 4 /
   // 8 / 12 / 16 / 32 units: bs16 14.1 / 13.4 / 14.0 / 14.2 / 16.8; 2 / 3 / 4 / 8 units a round: bs16 14.4 / 13.6 /
-  // 13.4 / 14.1, 40k 19.9 / 19.1 / 19.2 / 19.7; 2 or 3 stages a consumer: bs16 14.3 / 13.4. Shares of one unit: two
+  // 13.4 / 14.1, 40k (narrow) 19.9 / 19.1 / 19.2 / 19.7; 2 or 3 stages a consumer: bs16 14.3 / 13.4. Shares of one unit: two
   // requests of 37 and 200 tokens take 6.2 us, 6.7 and 8.4 with at least 2 and 8.
   static constexpr int kPieceCost = kFp8 ? 8 : PKV_DEC_PIECE_COST;
   static constexpr int kRound = kFp8 ? 4 : kRoundPages;
@@ -224,8 +233,8 @@ struct DecGeo {
   static constexpr int kGroups = G * D / 4;
   static constexpr int kLW = kGroups >= 32 ? kGroups / 32 : 1;
   static constexpr int kMergeBatch = 16 / kLW > 8 ? 8 : (16 / kLW < 1 ? 1 : 16 / kLW);  // polled records in flight
-  static constexpr int kItems = (kMH * D + kConsThreads - 1) / kConsThreads;  // (head, dim) per thread per pass
-  static_assert(kRound >= 1 && kRound <= kStages, "a page's previous stage use is in an earlier round");
+  static constexpr int kItems = (kMH * D + kConsumerThreads - 1) / kConsumerThreads;  // (head, dim) per thread per pass
+  static_assert(kRound >= 1 && kRound <= kFed * kRing, "a page's previous stage use is in an earlier round");
   static_assert(kSplitB % 16 == 0 && kPieceB % 16 == 0, "16-byte loads, copies and clears of a record");
   static_assert((kSmemRing + kSmemBars) % 16 == 0 && kSmemMerge % 16 == 0 && kQBuf % 16 == 0, "alignment");
   static_assert(kMergeCap >= 1, "a record fits the ring");
@@ -351,6 +360,23 @@ struct Shares {
   __device__ __forceinline__ int cta(long long f) const { return static_cast<int>(((cost(f) + 1) * n + Ctot - 1) / Ctot - 1); }
 };
 
+// CTAs that take a share of T pages in `pairs` non-empty (request, KV head) pairs: all that get kShareMin pages.
+// With the 8-bit cache's counted merge (few pairs, small shares) a pair has at most 2 sqrt(u) holders, u its units
+// on average: one CTA reads all their records, and a share's streaming shrinks with 1 / holders; and the number is a
+// multiple of the pairs, so that one request's shares end with its pairs (a CTA with two split pieces ends twice).
+// One request at 8/1/64, 4096 / 16384 / 40000 tokens: 15.9 / 29.2 / 29.6 us over all CTAs, 9.1 / 11.6 / 15.8 so
+// (1.5 sqrt(u): 9.1 / 12.2 / 16.4, 3 sqrt(u): 9.1 / 12.9 / 16.9); at 16/8/128, 1000 and 4096: 7.7 / 8.4, 7.2 / 8.5.
+template <class Geo, bool kPolled>
+__device__ __forceinline__ int share_count(long long T, int pairs) {
+  if (Geo::kFp8 && !kPolled && pairs > 0) {
+    const unsigned p = static_cast<unsigned>(pairs), u = static_cast<unsigned>(T) / p;  // u >= 1 units a pair
+    const unsigned h = min(min(static_cast<unsigned>(2.f * sqrtf(static_cast<float>(u))), u), gridDim.x / p);
+    return pairs * static_cast<int>(max(h, 1u));
+  }
+  const long long n = T / Geo::kShareMin > 0 ? T / Geo::kShareMin : 1;
+  return static_cast<int>(n < gridDim.x ? n : gridDim.x);
+}
+
 // Polled records are 32-bit words: an fp32 value rounded to nearest (even) at
 // 15 mantissa bits, with the tag in the freed low byte. Each word is one
 // single-copy-atomic access, so a reader that sees the tag sees the value,
@@ -384,8 +410,9 @@ __device__ __forceinline__ uint32_t ld_word(const uint32_t* p) {
 }
 __device__ __forceinline__ bool tagged(uint32_t w) { return (w & 0xffu) == kTag; }
 
+template <class Geo>
 __device__ __forceinline__ void consumer_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kConsThreads) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(Geo::kConsumerThreads) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -394,21 +421,21 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 // Combine the consumer warps' states of heads [h0, h0 + Geo::kMH) in the merge
 // buffer ([warp][head - h0][kRec]: m, l, pad, pad, o[D]) for this thread's
-// items: item e is (head h0 + x / D, dim x mod D) with x = tid + e * kConsThreads
+// items: item e is (head h0 + x / D, dim x mod D) with x = tid + e * Geo::kConsumerThreads
 // (valid when x < kMH * D). States of warps that folded nothing (m = -inf) weigh 0.
 template <class Geo>
 __device__ __forceinline__ void combine_items(const float* merge, int tid, float (&M)[Geo::kItems],
                                               float (&L)[Geo::kItems], float (&O)[Geo::kItems]) {
 #pragma unroll
   for (int e = 0; e < Geo::kItems; ++e) {
-    const int x = tid + e * kConsThreads;
+    const int x = tid + e * Geo::kConsumerThreads;
     const int hi = x / Geo::D < Geo::kMH ? x / Geo::D : Geo::kMH - 1, d = x % Geo::D;
     float m = -CUDART_INF_F;
 #pragma unroll
-    for (int w = 0; w < kCons; ++w) m = fmaxf(m, merge[(w * Geo::kMH + hi) * Geo::kRec]);
+    for (int w = 0; w < Geo::kConsumers; ++w) m = fmaxf(m, merge[(w * Geo::kMH + hi) * Geo::kRec]);
     float l = 0.f, o = 0.f;
 #pragma unroll
-    for (int w = 0; w < kCons; ++w) {
+    for (int w = 0; w < Geo::kConsumers; ++w) {
       const float* r = merge + (w * Geo::kMH + hi) * Geo::kRec;
       const float sc = r[0] == -CUDART_INF_F ? 0.f : ex2(r[0] - m);
       l += r[1] * sc;
@@ -444,7 +471,7 @@ __device__ __forceinline__ void store_lane_state(float* mw, int lane, int h0, co
 // kPolled: the polled merge, else the counted one. Each combination is its own
 // instantiation, so a path carries no code (and no registers) for the others.
 template <class Geo, bool kFused, bool kRope, bool kPolled>
-__global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(const __grid_constant__ CUtensorMap kmap,
+__global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                              const __grid_constant__ CUtensorMap vmap,
                                                                              const DecodeArgs a) {
   constexpr int D = Geo::D, G = Geo::G, kKS = Geo::kKS, kRing = Geo::kRing, kStages = Geo::kStages;
@@ -470,7 +497,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
   const int hkv = Geo::hkv(a);
   const int gq = Geo::gq(a);
   const int hq = hkv * gq;
-  if (tid == kConsThreads) {  // the producer's first lane: descriptors before its first copies
+  if (tid == Geo::kConsumerThreads) {  // the producer's first lane: descriptors before its first copies
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
   }
@@ -517,7 +544,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       }
       if (b < batch) pref[b] = carry + x - v;
       carry += __shfl_sync(kFull, x, 31);
-      const int w = kPolled && s > 0 ? hkv : 0;  // (the counted instantiation prices no boundary)
+      const int w = (kPolled || Geo::kFp8) && s > 0 ? hkv : 0;  // (the counted instantiation prices no boundary)
       int z = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -537,8 +564,8 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
     // and lo(c + 1) inside their requests.
     __syncwarp();
     const long long Tw = carry;
-    const long long gw = Tw / Geo::kShareMin > 0 ? Tw / Geo::kShareMin : 1;
-    const int nw = static_cast<int>(gw < gridDim.x ? gw : gridDim.x);
+    const int nw = share_count<Geo, kPolled>(Tw, pcarry);
+    if (Geo::kFp8 && lane == 0) flag[6] = nw;
     if (static_cast<int>(blockIdx.x) < nw) {
       Shares<kPolled ? Geo::kPieceCost : 0, Geo::kUnit> sw;
       sw.init(pref, pcp, sl, batch, hkv, nw, Tw, pcarry);
@@ -562,11 +589,10 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
 
   // Only min(gridDim.x, T / 8) CTAs (at least one) take a share, so that a share
   // holds 8 pages on average (a tiny step is not spread so thin that its merges
-  // dominate); the CTAs between the first and last holder of a (request, KV head)
-  // all hold a piece of it.
+  // dominate; share_count has the 8-bit cache's rule); the CTAs between the first
+  // and last holder of a (request, KV head) all hold a piece of it.
   const long long T = pref[batch];
-  const long long g_want = T / Geo::kShareMin > 0 ? T / Geo::kShareMin : 1;
-  const int nsh = static_cast<int>(g_want < gridDim.x ? g_want : gridDim.x);
+  const int nsh = Geo::kFp8 ? flag[6] : share_count<Geo, kPolled>(T, pcp[batch]);
   // zero output rows of empty requests (graph-bucket padding): CTA c clears rows
   // c, c + gridDim.x, ...; in early mode only after the grid dependency
   auto zero_empty_rows = [&](int first_thread, int nthreads) {
@@ -582,7 +608,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       grid_dependency_wait();
       allow_dependents();
     }
-    zero_empty_rows(0, kDecThreads);
+    zero_empty_rows(0, Geo::kThreads);
     return;
   }
   // the polled instantiation (batches, many short pairs) prices a pair boundary; the counted one
@@ -593,7 +619,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
   // ============================================================== producer warp
   // Walks the share 32 flattened indices at a time, one per lane: each lane
   // decodes its (request, KV head, page), loads the block-table entry, and works
-  // out which consumer reads the page ((f - lo) mod kCons) and which stage of
+  // out which consumer reads the page ((f - lo) mod Geo::kConsumers) and which stage of
   // that consumer's ring it fills (its running page count, from the lanes
   // before it with the same consumer). The lanes then issue their own tensor
   // copies in rounds of kRoundPages consecutive pages (round r of a chunk holds
@@ -606,16 +632,17 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
   // consumer, and a round could wait on a consumer held at a piece boundary by
   // a page of a later round (a deadlock). Smaller rounds land a CTA's first
   // pages sooner; one SIMT copy instruction per round amortises the issue.
-  if (warp == kCons) {
+  if (warp >= Geo::kConsumers) {
+    const int fed0 = (warp - Geo::kConsumers) * Geo::kFed;  // this producer's first consumer
     const uint64_t policy = policy_evict_first();
     const unsigned lt_mask = (1u << lane) - 1u;
-    int base[kCons];  // pages handed to each consumer before this chunk
+    int base[Geo::kConsumers];  // pages handed to each consumer before this chunk
 #pragma unroll
-    for (int c = 0; c < kCons; ++c) base[c] = 0;
+    for (int c = 0; c < Geo::kConsumers; ++c) base[c] = 0;
     bool pfail = false;
     bool waited = !a.early;
-    for (long long f0 = lo; f0 < hi && !pfail; f0 += 32) {
-      const long long f = f0 + lane;
+    for (long long f0 = lo + fed0; f0 < hi && !pfail; f0 += 32 * Geo::kProducers) {
+      const long long f = f0 + (lane / Geo::kFed) * Geo::kConsumers + lane % Geo::kFed;
       const bool valid = f < hi;
       int hh = 0, id = 0, c = 0, wslot = -1, bb = 0;
       int id2 = 0;       // (8-bit cache) the unit's second page,
@@ -627,7 +654,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
         const int off = static_cast<int>(f - pref[b]);
         hh = off / np;
         const int p = off % np;
-        c = static_cast<int>((f - lo) % kCons);
+        c = static_cast<int>((f - lo) % Geo::kConsumers);
         bb = b;
         const int* row = a.block_table + static_cast<size_t>(b) * a.max_pages + p * Geo::kUnitPages;
         id = __ldg(row);
@@ -642,7 +669,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       const int idx = __popc(same & lt_mask);  // earlier lanes of this chunk feeding the same consumer
       int my_base = 0;
 #pragma unroll
-      for (int cc = 0; cc < kCons; ++cc) {
+      for (int cc = 0; cc < Geo::kConsumers; ++cc) {
         if (cc == c) my_base = base[cc];
         base[cc] += __popc(__ballot_sync(kFull, valid && c == cc));
       }
@@ -838,10 +865,10 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
     grid_dependency_wait();
     allow_dependents();
   }
-  zero_empty_rows(0, kConsThreads);
+  zero_empty_rows(0, Geo::kConsumerThreads);
   if (have) stage_q(pc, 0);
   if (warp == 0) cp_async_wait_all();
-  consumer_sync();
+  consumer_sync<Geo>();
   for (int j = 0; have; ++j) {
     Piece nx;
     const bool have_next = find_piece<Geo::kUnit>(pc.fend, hi, pref, sl, batch, nx);
@@ -901,14 +928,14 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
     float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
     int vmax = 0;  // (8-bit cache) the largest value scale so far: o is 2^(kWeightShift + 127 - vmax) too large
 
-    const int w0 = static_cast<int>((pc.fstart - lo) % kCons);  // consumer of the piece's first page
-    const int p_first = pc.p0 + (warp - w0 + kCons) % kCons;    // this warp's first page of the piece
+    const int w0 = static_cast<int>((pc.fstart - lo) % Geo::kConsumers);  // consumer of the piece's first page
+    const int p_first = pc.p0 + (warp - w0 + Geo::kConsumers) % Geo::kConsumers;    // this warp's first page of the piece
     // Fused append without the rotary embedding: the warp that takes the request's last page loads
     // the new token's K and V rows for this head now (lane l: 16-byte chunk l of the K row, or of
     // the V row from lane D / 8 on) with that page's block-table entry. Once the page is staged it
     // writes them over the copied slot and into the pool.
     const bool takes_new =
-        kFused && !kRope && pc.p1 == pc.np && p_first <= pc.np - 1 && (pc.np - 1 - p_first) % kCons == 0;
+        kFused && !kRope && pc.p1 == pc.np && p_first <= pc.np - 1 && (pc.np - 1 - p_first) % Geo::kConsumers == 0;
     constexpr int kRowChunks = D / 8;
     uint4 nrow = make_uint4(0u, 0u, 0u, 0u);
     int nid = -1;
@@ -919,7 +946,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
                      lane % kRowChunks);
       nid = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pc.np - 1);
     }
-    for (int p = p_first; p < pc.p1; p += kCons) {
+    for (int p = p_first; p < pc.p1; p += Geo::kConsumers) {
       const int slot = warp * kRing + k % kRing;
       const uint32_t parity = static_cast<uint32_t>(k / kRing) & 1u;
       if (!failed) {
@@ -994,7 +1021,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
           }
         }
       }
-      consumer_sync();
+      consumer_sync<Geo>();
 
       // ---- CTA combine of the warp states for this thread's (head, dim) items
       float M[Geo::kItems], L[Geo::kItems], O[Geo::kItems];
@@ -1002,24 +1029,24 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       if (complete) {
 #pragma unroll
         for (int e = 0; e < Geo::kItems; ++e) {
-          const int x = tid + e * kConsThreads;
+          const int x = tid + e * Geo::kConsumerThreads;
           if (x < kMH * D && h0 + x / D < gq) orow[(h0 + x / D) * D + x % D] = __float2bfloat16_rn(O[e] / L[e]);
         }
       } else if constexpr (kPolled) {
         uint32_t* rec = a.tagged + static_cast<size_t>(my_slot) * Geo::kSplitWords;
 #pragma unroll
         for (int e = 0; e < Geo::kItems; ++e) {
-          const int x = tid + e * kConsThreads;
+          const int x = tid + e * Geo::kConsumerThreads;
           if (x < kMH * D) st_word(rec + h0 * D + x, tag_word(O[e]));
         }
         if (tid < 4 * kMH) {  // m_hi, m_lo, l_hi, l_lo of head h0 + tid / 4
           const int hi4 = tid >> 2;
           float m = -CUDART_INF_F;
 #pragma unroll
-          for (int w = 0; w < kCons; ++w) m = fmaxf(m, merge[(w * kMH + hi4) * kRec]);
+          for (int w = 0; w < Geo::kConsumers; ++w) m = fmaxf(m, merge[(w * kMH + hi4) * kRec]);
           float l = 0.f;
 #pragma unroll
-          for (int w = 0; w < kCons; ++w) {
+          for (int w = 0; w < Geo::kConsumers; ++w) {
             const float* rr = merge + (w * kMH + hi4) * kRec;
             l += rr[1] * (rr[0] == -CUDART_INF_F ? 0.f : ex2(rr[0] - m));
           }
@@ -1031,7 +1058,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
         float* rec = a.partials + static_cast<size_t>(my_slot) * Geo::kPiece;
 #pragma unroll
         for (int e = 0; e < Geo::kItems; ++e) {
-          const int x = tid + e * kConsThreads;
+          const int x = tid + e * Geo::kConsumerThreads;
           if (x < kMH * D) {
             rec[(h0 + x / D) * kRec + 4 + x % D] = O[e];
             if (x % D == 0) {
@@ -1041,7 +1068,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
           }
         }
       }
-      if (h0 + kMH < G) consumer_sync();  // the merge buffer is free for the next heads
+      if (h0 + kMH < G) consumer_sync<Geo>();  // the merge buffer is free for the next heads
     }
     if (!complete && !kPolled) {
       if (npend == 0) {
@@ -1052,7 +1079,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       ++npend;
     }
     if (warp == 0) cp_async_wait_all();  // the next piece's query rows have landed
-    consumer_sync();                     // merge buffer and qbuf[j & 1] free, qbuf[(j + 1) & 1] visible
+    consumer_sync<Geo>();                     // merge buffer and qbuf[j & 1] free, qbuf[(j + 1) & 1] visible
     pc = nx;
     have = have_next;
   }
@@ -1068,15 +1095,15 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
 #pragma unroll
     for (int h0 = 0; h0 < G; h0 += kMH) {
       store_lane_state<Geo>(merge + warp * kMH * kRec, lane, h0, fm, fl, fo);
-      consumer_sync();
+      consumer_sync<Geo>();
       float M[Geo::kItems], L[Geo::kItems], O[Geo::kItems];
       combine_items<Geo>(merge, tid, M, L, O);
 #pragma unroll
       for (int e = 0; e < Geo::kItems; ++e) {
-        const int x = tid + e * kConsThreads;
+        const int x = tid + e * Geo::kConsumerThreads;
         if (x < kMH * D && h0 + x / D < gq) orow[(h0 + x / D) * D + x % D] = __float2bfloat16_rn(O[e] / L[e]);
       }
-      consumer_sync();  // the merge buffer is free again
+      consumer_sync<Geo>();  // the merge buffer is free again
     }
   };
 
@@ -1084,7 +1111,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
     if (!merger || flag[2] != 0) return;  // (a failed wait: copies may still land, merge nothing)
 
     // Polled merge (log-sum-exp) of the pair of this CTA's first piece over the
-    // records of its n holders. Warp w folds records t = w, w + kCons, ... in that
+    // records of its n holders. Warp w folds records t = w, w + Geo::kConsumers, ... in that
     // order, with up to kMergeBatch of them loaded at a time (lanes 0 .. 4G - 1
     // also load the m/l words); a record is read again until every word carries
     // the tag. The order depends only on the pair, so the result is the same bits
@@ -1106,21 +1133,21 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
     constexpr int kMB = Geo::kMergeBatch;
     const uint4 tag4 = make_uint4(kTag, kTag, kTag, kTag);
     bool lost = false;  // a record never got its tags (a bounded wait ran out)
-    for (int t0 = warp; t0 < n && !lost; t0 += kMB * kCons) {
+    for (int t0 = warp; t0 < n && !lost; t0 += kMB * Geo::kConsumers) {
       uint4 R[kMB][kLW];  // o groups of this lane
       uint32_t W[kMB];    // lanes 0 .. 4G - 1: word lane of the m/l block
       auto load = [&](int rr) {
-        const uint32_t* rec = rec_of(t0 + rr * kCons);
+        const uint32_t* rec = rec_of(t0 + rr * Geo::kConsumers);
 #pragma unroll
         for (int j = 0; j < kLW; ++j) R[rr][j] = group_ok(j) ? ld_words4(rec + 4 * (lane + 32 * j)) : tag4;
         W[rr] = lane < 4 * G ? ld_word(rec + G * D + lane) : kTag;
       };
 #pragma unroll
       for (int rr = 0; rr < kMB; ++rr)
-        if (t0 + rr * kCons < n) load(rr);
+        if (t0 + rr * Geo::kConsumers < n) load(rr);
 #pragma unroll
       for (int rr = 0; rr < kMB; ++rr) {
-        if (t0 + rr * kCons >= n) break;
+        if (t0 + rr * Geo::kConsumers >= n) break;
         auto all_tagged = [&]() {
           bool ok = tagged(W[rr]);
 #pragma unroll
@@ -1163,11 +1190,11 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       set_status(a.status, PKV_ERR_DEVICE_TIMEOUT);
       flag[2] = 1;
     }
-    consumer_sync();
+    consumer_sync<Geo>();
     if (flag[2] != 0) return;
     finish_pair(mb, mh, fm, fl, fo);
     // clear the tags of the merged records for the next call (every read above has completed)
-    for (int i = tid; i < n * (Geo::kSplitB / 16); i += kConsThreads) {
+    for (int i = tid; i < n * (Geo::kSplitB / 16); i += Geo::kConsumerThreads) {
       const int t = i / (Geo::kSplitB / 16), c = i % (Geo::kSplitB / 16);
       reinterpret_cast<uint4*>(rec_of(t))[c] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -1184,7 +1211,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       flag[0] = old0 == pn0 - 1 ? 1 : 0;
       flag[1] = npend > 1 && old1 == pn1 - 1 ? 1 : 0;
     }
-    consumer_sync();
+    consumer_sync<Geo>();
     if (flag[2] != 0) {  // a wait failed: copies may still land in the ring, merge nothing
       if (tid == 0) {
         if (flag[0]) a.counters[pb0 * hkv + ph0] = 0;
@@ -1195,7 +1222,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
     // Final merges (log-sum-exp over the partial records) of the pairs whose count
     // this CTA completed, one pair after the other. A pair's records are staged in
     // the drained stage ring by 16-byte asynchronous copies (one round trip per
-    // batch of up to kMergeCap records); record t is folded by warp t % kCons in
+    // batch of up to kMergeCap records); record t is folded by warp t % Geo::kConsumers in
     // the lane layout above, and the warps' states are then combined through the
     // merge buffer. Which warp folds which record, and the batch boundaries,
     // depend only on the pair, so the result is the same whichever CTA merges.
@@ -1217,27 +1244,27 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
       }
       for (int t0 = 0; t0 < nm; t0 += Geo::kMergeCap) {
         const int t1 = t0 + Geo::kMergeCap < nm ? t0 + Geo::kMergeCap : nm;
-        for (int t = t0 + warp; t < t1; t += kCons) {
+        for (int t = t0 + warp; t < t1; t += Geo::kConsumers) {
           const size_t slot = 2 * static_cast<size_t>(cf + t) + ((t == 0 && two) ? 1 : 0);
           const unsigned char* src = reinterpret_cast<const unsigned char*>(a.partials + slot * Geo::kPiece);
           const uint32_t dst = ring_s + (t - t0) * Geo::kPieceB;
           for (int c = lane; c < kChunks; c += 32) cp_async16(dst + c * 16, src + c * 16);
         }
         cp_async_wait_all();
-        consumer_sync();
-        const int pfirst = ((warp - t0) % kCons + kCons) % kCons;  // this warp's first record position
+        consumer_sync<Geo>();
+        const int pfirst = ((warp - t0) % Geo::kConsumers + Geo::kConsumers) % Geo::kConsumers;  // this warp's first record position
 #pragma unroll
         for (int j = 0; j < kLW; ++j) {
           if (!group_ok(j)) continue;
           const int hd = group_head(j), d = (4 * (lane + 32 * j)) % D;
           float m = fm[j];
-          for (int p = pfirst; p < t1 - t0; p += kCons) m = fmaxf(m, Rs[p * Geo::kPiece + hd * kRec]);
+          for (int p = pfirst; p < t1 - t0; p += Geo::kConsumers) m = fmaxf(m, Rs[p * Geo::kPiece + hd * kRec]);
           const float keep = fm[j] == -CUDART_INF_F ? 0.f : ex2(fm[j] - m);
           float l = fl[j] * keep;
           float4 ov = fo[j];
           ov.x *= keep, ov.y *= keep, ov.z *= keep, ov.w *= keep;
 #pragma unroll 4
-          for (int p = pfirst; p < t1 - t0; p += kCons) {
+          for (int p = pfirst; p < t1 - t0; p += Geo::kConsumers) {
             const float* rr = Rs + p * Geo::kPiece + hd * kRec;
             const float sc = ex2(rr[0] - m);
             l += rr[1] * sc;
@@ -1248,7 +1275,7 @@ __global__ void __launch_bounds__(kDecThreads, Geo::kCtasPerSm) decode_kernel(co
           fl[j] = l;
           fo[j] = ov;
         }
-        consumer_sync();  // the ring is free for the next batch
+        consumer_sync<Geo>();  // the ring is free for the next batch
       }
       const int b = i ? pb1 : pb0, h = i ? ph1 : ph0;
       finish_pair(b, h, fm, fl, fo);
@@ -1320,15 +1347,18 @@ int launch_decode_geo(const DecodeLaunch& c) {
   const int grid = decode_grid(c.num_sms);
   const long long pairs = static_cast<long long>(c.batch) * c.hkv;
   // (head_dim 64 stays narrow: with one CTA per SM its consumers, four per SM, page too slowly -- one
-  // 40k-token request at 16/8/64 measured 19.0 us per layer wide against 17.8 narrow)
-  // (nor does the 8-bit cache: one 40k request 24.6 us wide, its one producer per SM short of copies, 19.2 narrow)
-  const bool wide = Geo::D == 128 && !Geo::kFp8 && grid > kPollMax * pairs && pairs * c.max_pages >= kWideMinPages;
+  // 40k-token request at 16/8/64 measured 19.0 us per layer wide against 17.8 narrow. The 8-bit cache's
+  // wide shape has two producers and eight consumers per CTA, so half the records to merge and no fewer
+  // warps: one 40k request 19.4 us narrow, 17.8 wide at 16/8/128, 13.0 and 12.0 at 16/4/64; 16k 11.9 and
+  // 10.6; as its own rule for larger batches it lost, bs16 13.4 narrow and 14.2 wide.)
+  const bool wide = (Geo::D == 128 || Geo::kFp8) && grid > kPollMax * pairs && pairs * c.max_pages >= kWideMinPages;
   const int grid_used = wide ? (c.num_sms < kMaxGrid ? c.num_sms : kMaxGrid) : grid;
   const bool polled = grid_used <= kPollMax * pairs;
   const size_t smem = wide ? GeoW::smem_bytes(c.batch) : Geo::smem_bytes(c.batch);
-  // (the wide rows are never taken at head_dim 64; they name the narrow kernels there so that
-  // no wide head_dim-64 instantiation is built)
-  using GW = typename std::conditional<Geo::D == 128 && !Geo::kFp8, GeoW, Geo>::type;
+  const int threads = wide ? GeoW::kThreads : Geo::kThreads;
+  // (the wide rows are never taken at head_dim 64 with bf16 pages; they name the narrow kernels there so
+  // that no such instantiation is built)
+  using GW = typename std::conditional<Geo::D == 128 || Geo::kFp8, GeoW, Geo>::type;
   static const DecodeKern kKerns[4][3] = {
       {decode_instance<Geo, false, false, false>(), decode_instance<Geo, true, false, false>(),
        decode_instance<Geo, true, true, false>()},
@@ -1353,7 +1383,7 @@ int launch_decode_geo(const DecodeLaunch& c) {
     attr_set[dev][shape][variant] = true;
   }
   int occ = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, kDecThreads, smem) != cudaSuccess)
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, smem) != cudaSuccess)
     return PKV_ERR_CUDA;
   if (occ < 1) return PKV_ERR_UNSUPPORTED;
   const int occ_cap = wide ? GeoW::kCtasPerSm : Geo::kCtasPerSm;
@@ -1389,7 +1419,7 @@ int launch_decode_geo(const DecodeLaunch& c) {
                            : encode_page_maps(c.k_pages, c.v_pages, Geo::D, c.num_pages, c.hkv, &kmap, &vmap);
   if (rc != PKV_OK) return rc;
   const int launch_grid = c.num_sms * occ < kMaxGrid ? c.num_sms * occ : kMaxGrid;
-  return launch_pdl(kern, dim3(launch_grid), dim3(kDecThreads), smem, c.stream, kmap, vmap, a) == cudaSuccess
+  return launch_pdl(kern, dim3(launch_grid), dim3(threads), smem, c.stream, kmap, vmap, a) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }

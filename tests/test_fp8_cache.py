@@ -16,7 +16,7 @@ from paged_kv_decode_gb300 import _lib
 from paged_kv_decode_gb300 import workloads as W
 from paged_kv_decode_gb300.build import build_library
 from parity import bf16_to_f64
-from test_schedule import ShareMap, assign_share, simulate
+from test_schedule import ShareMap, assign_share, piece_index, simulate
 
 
 # ---------------------------------------------------------------------------------------------- CPU
@@ -88,27 +88,75 @@ def test_expand_host_argument_checks(lib):
 
 
 class Units(ShareMap):
-    """The share map of the 8-bit decode kernel: units of 32 tokens, shares of at least one unit."""
+    """The share map of the 8-bit decode kernel: units of 32 tokens; shares of at least one unit, or (the counted merge,
+    lam 0) at most 2 sqrt(units of a pair) holders per pair and as many CTAs as a multiple of the pairs."""
 
     def __init__(self, seq_lens, grid, lam, hkv=8):
         super().__init__([(int(s) + 31) // 32 * 16 for s in seq_lens], grid, lam, hkv)  # as many pages as units
         self.n = min(grid, max(1, self.T))
+        if lam == 0 and self.pcp[-1]:
+            u = self.T // self.pcp[-1]
+            self.n = self.pcp[-1] * max(1, min(int(2 * np.sqrt(np.float32(u))), u, grid // self.pcp[-1]))
 
 
 UNIT_MIXES = [[37, 200], [1], [33], [32] * 7, [9000], [0, 700, 0, 33, 1, 2900, 0], list(range(1, 65)),
               [3, 8000, 5, 900], [1, 2, 3, 4, 5, 6, 7, 8, 4000], list(W.config_seq_lens(2))[:6]]
 
 
+def _halves_finish(lo, hi, starts, halves, round_units, ring=3):
+    """One CTA of `halves` producers with 4 consumers each: unit f of the share goes to consumer (f - lo) % (4 halves),
+    a producer walks its own units 32 at a time in rounds, consumers meet at piece boundaries. True if all is read; a
+    stage's previous use must lie in an earlier round (one barrier phase)."""
+    cons = 4 * halves
+    n = hi - lo
+    piece = piece_index(lo, hi, starts) if n else []
+    own = [[i for i in range(n) if i % cons // 4 == h] for h in range(halves)]
+    rounds, round_of = [], {}
+    for h in range(halves):
+        rs = {}
+        for o, i in enumerate(own[h]):
+            rs.setdefault((o // 32, o % 32 // round_units), []).append(i)
+        rounds.append([rs[k] for k in sorted(rs)])
+        for r, lst in enumerate(rounds[h]):
+            round_of.update({i: r for i in lst})
+    back = cons * ring
+    assert all(round_of[i - back] < round_of[i] for i in range(back, n))
+    issued, done = [False] * n, [False] * n
+    at, nxt, now = [0] * halves, [c for c in range(cons)], 0
+    while not all(done):
+        moved = False
+        for h in range(halves):
+            # a round goes out as a whole once all its stages are free
+            while at[h] < len(rounds[h]) and all(i < back or done[i - back] for i in rounds[h][at[h]]):
+                for i in rounds[h][at[h]]:
+                    issued[i] = True
+                at[h] += 1
+                moved = True
+        for c in range(cons):
+            while nxt[c] < n and issued[nxt[c]] and piece[nxt[c]] == now:
+                done[nxt[c]] = moved = True
+                nxt[c] += cons
+        if now < (piece[-1] if n else 0) and all(done[i] for i in range(n) if piece[i] == now):
+            now += 1
+            moved = True
+        if not moved:
+            return False
+    return True
+
+
 @pytest.mark.parametrize("lam", [0, 8])
 @pytest.mark.parametrize("grid", [7, 152, 304])
 def test_decode_shares_tile_the_units_and_cannot_deadlock(lam, grid):
     """Every unit in one share, the holders of a (request, KV head) consecutive and non-empty, and the copy schedule
-    (rounds of 4 units) of every share finishes."""
+    (rounds of 4 units) of every share finishes, with one producer and with two."""
     for lens in UNIT_MIXES:
         for hkv in (1, 8):
+            pairs = sum(1 for s in lens if s) * hkv
+            if lam == 0 and pairs > grid:
+                continue  # the counted merge is for few pairs
             sm = Units(lens, grid, lam, hkv)
             lo = [sm.lo(c) for c in range(sm.n + 1)]
-            assert lo[0] == 0 and lo[-1] == sm.T and all(a <= b for a, b in zip(lo, lo[1:]))
+            assert sm.n <= grid and lo[0] == 0 and lo[-1] == sm.T and all(a <= b for a, b in zip(lo, lo[1:]))
             starts = []
             for b, p in enumerate(sm.pages):
                 for h in range(hkv if p else 0):
@@ -120,6 +168,17 @@ def test_decode_shares_tile_the_units_and_cannot_deadlock(lam, grid):
                 assert lo[sm.cta(f)] <= f < lo[sm.cta(f) + 1]
             for c in range(sm.n):
                 assert simulate(lo[c], lo[c + 1], starts, assign_share, 4)
+            for c in range(0, sm.n, 1 + sm.n // 40):
+                assert _halves_finish(lo[c], lo[c + 1], starts, 2, 4)
+
+
+def test_two_producers_finish_on_one_share():
+    """One CTA holding everything: runs of one-unit pieces, long pieces, and a mix."""
+    for pieces in ([1] * 90, [200], [1, 1, 150, 1, 2, 3, 70, 1] * 2, list(range(1, 30))):
+        starts = list(np.cumsum([0] + pieces[:-1]))
+        assert _halves_finish(0, sum(pieces), starts, 2, 4) and _halves_finish(0, sum(pieces), starts, 1, 4)
+    with pytest.raises(AssertionError):  # a round larger than a half's stages would wait on itself
+        _halves_finish(0, 200, [0], 2, 16)
 
 
 # ---------------------------------------------------------------------------------------------- GPU
@@ -202,7 +261,11 @@ def test_decode(cuda_device, geom, lens):
 @pytest.mark.gpu
 @pytest.mark.parametrize("geom,lens,width", [("16q8kv128", W.config_seq_lens(2), None), ("16q8kv64", [3000] * 16, None),
                                              ("16q8kv128", [20000], None), ("16q8kv128", [900], 4096),
-                                             ("8q1kv64", [9001], None), ("32q32kv64", W.config_seq_lens(5)[:12], 600)])
+                                             ("8q1kv64", [9001], None), ("32q32kv64", W.config_seq_lens(5)[:12], 600),
+                                             ("16q8kv64", [20000], None), ("8q1kv64", [9001], 9000),
+                                             ("28q4kv128", [7000], 2100), ("28q4kv128", [5000, 40], None),
+                                             ("12q4kv128", [3, 0, 2500], 4000), ("64q8kv128", [17000], None),
+                                             ("8q1kv64", [1], 9000)])
 def test_decode_long_and_split(cuda_device, geom, lens, width):
     """Contexts split over many CTAs, by both merges and both launch shapes (a wide table takes the one-CTA shape)."""
     c = Cache(22, GEOMS[geom], lens, cuda_device, width=width)
