@@ -74,7 +74,7 @@
  *    it not so, the wait would run out after about one second and report
  *    PKV_ERR_DEVICE_TIMEOUT; it never hangs.
  *  - A workspace serves one kind of attention call: decode calls
- *    (pkv_decode_attn, pkv_decode_append_attn, pkv_decode_attn_fp8) or prefill calls
+ *    (pkv_decode_attn, pkv_decode_append_attn, and the 8-bit cache's) or prefill calls
  *    (pkv_prefill_chunk_attn), not both: each kind relies on its own split
  *    scratch (counters, and for decode tagged records) having been left
  *    cleared by the previous call of that kind. The appends and pkv_expand_fp8
@@ -397,6 +397,32 @@ int pkv_decode_attn_fp8(const void* q, const void* k_pages, const void* v_pages,
                         const int32_t* block_table, const int32_t* seq_lens, void* out, float scale,
                         pkv_stream_t stream, const pkv_cache_desc* desc, int32_t batch, int32_t max_pages_per_seq,
                         void* workspace, size_t workspace_bytes, uint32_t flags);
+
+/*
+ * pkv_decode_append_attn_fp8 -- one decode step of one layer over the 8-bit
+ * cache in one launch: pkv_append_rope_fp8 of each request's new token at
+ * position seq_lens[b] - 1, then pkv_decode_attn_fp8 over seq_lens[b]
+ * positions with the query rows normalised, rotated and rounded to bf16 as that
+ * append would (nothing is written to q). The rows written and the outputs are
+ * those of the two calls, bit for bit.
+ *
+ *  q, k_new, v_new: bf16 [batch][num_q_heads][head_dim] and
+ *                [batch][num_kv_heads][head_dim], contiguous; requests of
+ *                length 0 write nothing
+ *  rope_cos_sin, q_weight, k_weight: each may be NULL, as for
+ *                pkv_append_rope. A position >= rope_max_pos is clamped to the
+ *                table's last row and sets PKV_ERR_OUT_OF_BOUNDS
+ *  flags:        0 or PKV_DECODE_EARLY_PREFETCH, with the promise that the
+ *                previous kernel writes neither the cache (scales included)
+ *                nor block_table, seq_lens, rope_cos_sin or the weights
+ *  other arguments and the workspace: as for pkv_decode_attn_fp8
+ */
+int pkv_decode_append_attn_fp8(const void* q, const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                               void* kv_scales, const int32_t* block_table, const int32_t* seq_lens,
+                               const float* rope_cos_sin, int32_t rope_max_pos, const void* q_weight,
+                               const void* k_weight, float eps, void* out, float scale, pkv_stream_t stream,
+                               const pkv_cache_desc* desc, int32_t batch, int32_t max_pages_per_seq, void* workspace,
+                               size_t workspace_bytes, uint32_t flags);
 
 /*
  * pkv_expand_fp8 -- pages of the 8-bit cache as bf16 pages, exactly: the

@@ -38,7 +38,7 @@ __all__ = [
     "PkvError", "desc", "Workspace", "append", "decode_attn", "prefill_chunk_attn",
     "decode_workspace_bytes", "prefill_workspace_bytes", "workspace_init", "read_status", "status_string",
     "decode_attn_noalloc", "decode_append_attn", "mixed_step_attn", "mixed_workspace_bytes", "rope_cos_sin",
-    "append_rope", "append_rope_fp8", "decode_attn_fp8", "expand_fp8",
+    "append_rope", "append_rope_fp8", "decode_attn_fp8", "decode_append_attn_fp8", "expand_fp8",
 ]
 
 
@@ -309,6 +309,21 @@ def decode_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, 
     be read while it finishes (PKV_DECODE_EARLY_PREFETCH)."""
     _check(_lib.binding().decode_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, scale, workspace,
                                           stream, EARLY_PREFETCH if early_prefetch else 0), "pkv_decode_attn_fp8")
+
+
+def decode_append_attn_fp8(q, k_new, v_new, k_pages, v_pages, kv_scales, block_table, seq_lens, cos_sin, out,
+                           scale: float, workspace: Workspace, q_weight=None, k_weight=None, eps: float = 1e-6,
+                           stream=None, early_prefetch: bool = False):
+    """One decode step of one layer over the 8-bit cache in one launch: append_rope_fp8 of k_new / v_new [B, Hkv, D] at
+    positions seq_lens - 1, then decode_attn_fp8 with the rows of q [B, Hq, D] normalised and rotated alike (cos_sin,
+    q_weight and k_weight may be None). Bit for bit the two calls' rows and outputs.
+
+    early_prefetch: the previous kernel on the stream writes neither the cache nor the block table, the lengths, cos_sin
+    or the weights (PKV_DECODE_EARLY_PREFETCH)."""
+    _check(_lib.binding().decode_append_attn_fp8(q, k_new, v_new, k_pages, v_pages, kv_scales, block_table, seq_lens,
+                                                 cos_sin, out, scale, workspace, q_weight, k_weight, eps, stream,
+                                                 EARLY_PREFETCH if early_prefetch else 0),
+           "pkv_decode_append_attn_fp8")
 
 
 def expand_fp8(k_pages, v_pages, kv_scales, block_table, seq_lens, k_out, v_out, out_block_table,

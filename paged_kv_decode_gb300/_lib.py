@@ -48,6 +48,8 @@ PROTOTYPES = {
                                            _vp, _vp, _vp, _vp, _dp, _vp, _vp, _sz]),
     "pkv_decode_attn_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _dp, _i32, _i32, _vp, _sz,
                                            ctypes.c_uint32]),
+    "pkv_decode_append_attn_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _f32,
+                                                  _vp, _f32, _vp, _dp, _i32, _i32, _vp, _sz, ctypes.c_uint32]),
     "pkv_expand_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _dp, _vp, _vp, _sz]),
     "pkv_prefill_workspace_bytes": (_sz, [_dp, _i32, _i32]),
     "pkv_prefill_chunk_attn": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _f32, _vp, _dp, _i32,

@@ -37,6 +37,7 @@
 #include "pkv_device.cuh"
 #include "pkv_fp8.cuh"
 #include "pkv_kernels.h"
+#include "pkv_rows.cuh"
 
 namespace pkv {
 namespace {
@@ -49,51 +50,6 @@ constexpr int kBlocksPerSm = 4;
 constexpr int kDepth = 4;                // batches on the way per warp
 constexpr int kTables = kDepth / 2 + 2;  // tokens that kDepth + 1 batches touch (a token has at least 2)
 constexpr int kBatchBytes = 1024;        // 32 lanes x 16 values
-
-// A lane's 16 values: pairs 0 .. 3 are dims 8l .. 8l + 7, pairs 4 .. 7 dims D/2 + 8l .. D/2 + 8l + 7.
-struct Row {
-  float2 y[8];
-};
-__device__ __forceinline__ Row unpack(const uint4& lo, const uint4& hi) {
-  return {{bf2_to_f2(lo.x), bf2_to_f2(lo.y), bf2_to_f2(lo.z), bf2_to_f2(lo.w), bf2_to_f2(hi.x), bf2_to_f2(hi.y),
-           bf2_to_f2(hi.z), bf2_to_f2(hi.w)}};
-}
-__device__ __forceinline__ uint4 pack4(const float2* y) {
-  return make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y), pack_bf16x2(y[2].x, y[2].y),
-                    pack_bf16x2(y[3].x, y[3].y));
-}
-__device__ __forceinline__ uint32_t quant4(const float2& a, const float2& b, float f) {
-  const float2 f2 = make_float2(f, f);
-  const float2 x = __fmul2_rn(a, f2), y = __fmul2_rn(b, f2);
-  return static_cast<uint32_t>(to_e4m3x2(x.x, x.y)) | static_cast<uint32_t>(to_e4m3x2(y.x, y.y)) << 16;
-}
-
-// Largest finite magnitude of the row's values (over its lanes).
-template <int L>
-__device__ __forceinline__ float row_max(const Row& x) {
-  float most = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) most = fmaxf(most, fmaxf(fabsf(x.y[i].x), fabsf(x.y[i].y)));  // (drops NaN)
-#pragma unroll
-  for (int m = 1; m < L; m <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
-  if (__any_sync(0xffffffffu, most == CUDART_INF_F)) {  // rare: again without the infinities
-    float fin = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = fabsf(x.y[i].x), b = fabsf(x.y[i].y);
-      fin = fmaxf(fin, fmaxf(a < CUDART_INF_F ? a : 0.f, b < CUDART_INF_F ? b : 0.f));
-    }
-#pragma unroll
-    for (int m = 1; m < L; m <<= 1) fin = fmaxf(fin, __shfl_xor_sync(0xffffffffu, fin, m));
-    most = fin;
-  }
-  return most;
-}
-
-// The token's table row: c, s and -s of the lane's 8 pairs.
-struct Turn {
-  float2 c[4], s[4], n[4];
-};
 
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) append_rope_kernel(const AppendRopeArgs a) {
@@ -228,13 +184,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) append_rope_kernel(
 #pragma unroll 1
     for (; n > 0; --n, h += R) {
       landed();
-      uint4 xl, xh;
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(xl.x), "=r"(xl.y), "=r"(xl.z), "=r"(xl.w)
-                   : "r"(rring));
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(xh.x), "=r"(xh.y), "=r"(xh.z), "=r"(xh.w)
-                   : "r"(rring + kBatchBytes / 2));
+      const uint4 xl = lds128(rring), xh = lds128(rring + kBatchBytes / 2);
       rring += kBatchBytes;
       if (rring == ring_end) rring = ring;
       const bool writes = h < heads && (K == 0 || in_page >= 0);
@@ -246,44 +196,17 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) append_rope_kernel(
         }
       } else {
         Row x = unpack(xl, xh);
-        float norm = 1.f;
-        if (norms) {
-          float2 sq = __fmul2_rn(x.y[0], x.y[0]), sr = __fmul2_rn(x.y[1], x.y[1]);
-#pragma unroll
-          for (int j = 2; j < 8; j += 2) {
-            sq = __ffma2_rn(x.y[j], x.y[j], sq);
-            sr = __ffma2_rn(x.y[j + 1], x.y[j + 1], sr);
-          }
-          float sum = (sq.x + sq.y) + (sr.x + sr.y);
-#pragma unroll
-          for (int m = 1; m < L; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-          norm = __frsqrt_rn(sum * (1.f / D) + a.eps);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x.y[j] = __fmul2_rn(x.y[j], w.y[j]);
-        }
-        if (turns) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 x1 = x.y[j], x2 = x.y[4 + j];
-            x.y[j] = __ffma2_rn(x1, cs.c[j], __fmul2_rn(x2, cs.n[j]));
-            x.y[4 + j] = __ffma2_rn(x2, cs.c[j], __fmul2_rn(x1, cs.s[j]));
-          }
-        }
+        const float norm = turn_row<D>(x, norms, w, a.eps, turns, cs);
         if constexpr (kQuant) {
-          // rounding is monotonic: the largest of the rounded products by norm is the largest value's
-          const int e = row_exponent(row_max<L>(x) * norm);
-          const float f8 = norm * pow2i(-e);
+          uint2 q0, q1;
+          const int e = quantise_row<D>(x, norm, q0, q1);
           if (writes) {
-            reinterpret_cast<uint2*>(to)[0] = make_uint2(quant4(x.y[0], x.y[1], f8), quant4(x.y[2], x.y[3], f8));
-            reinterpret_cast<uint2*>(to)[L] = make_uint2(quant4(x.y[4], x.y[5], f8), quant4(x.y[6], x.y[7], f8));
-            if (l == 0) a.scales[(tile0 + h) * kScaleBytes + (K - 1) * kPageSize + in_page] = static_cast<uint8_t>(e + 127);
+            reinterpret_cast<uint2*>(to)[0] = q0;
+            reinterpret_cast<uint2*>(to)[L] = q1;
+            if (l == 0) a.scales[(tile0 + h) * kScaleBytes + (K - 1) * kPageSize + in_page] = static_cast<uint8_t>(e);
           }
         } else {
-          if (norms) {
-            const float2 n2 = make_float2(norm, norm);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x.y[j] = __fmul2_rn(x.y[j], n2);
-          }
+          if (norms) scale_row(x, norm);
           if (writes) {
             reinterpret_cast<uint4*>(to)[0] = pack4(x.y);
             reinterpret_cast<uint4*>(to)[L] = pack4(x.y + 4);
@@ -308,19 +231,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) append_rope_kernel(
       if (turn && (p < 0 || p >= a.rope_max_pos) && (a.hq > 0 || inside)) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
       in_page = inside ? slot % kPageSize : -1;
       tile0 = static_cast<size_t>(inside ? slot / kPageSize : 0) * a.hkv;
-      if (turn) {
-        const float4* row = reinterpret_cast<const float4*>(table_s[warp]) + rtable * (D / 4) + 2 * l;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 c = row[j], s = row[D / 8 + j];
-          cs.c[2 * j] = make_float2(c.x, c.y);
-          cs.c[2 * j + 1] = make_float2(c.z, c.w);
-          cs.s[2 * j] = make_float2(s.x, s.y);
-          cs.s[2 * j + 1] = make_float2(s.z, s.w);
-          cs.n[2 * j] = make_float2(-s.x, -s.y);
-          cs.n[2 * j + 1] = make_float2(-s.z, -s.w);
-        }
-      }
+      if (turn) load_turn<D>(reinterpret_cast<const float*>(table_s[warp]) + rtable * D, l, cs);
       enter = false;
     }
     const unsigned n = min(batches_of(kind) - before, hi - f);

@@ -1,7 +1,7 @@
 /*
  * binding.c -- CPython side of the calls whose kernels take a few
- * microseconds: pkv_append_rope, pkv_append_rope_fp8, pkv_decode_attn_fp8 and
- * pkv_expand_fp8. It reads the torch tensors' attributes, checks them and makes
+ * microseconds: pkv_append_rope, pkv_append_rope_fp8, pkv_decode_attn_fp8,
+ * pkv_decode_append_attn_fp8 and pkv_expand_fp8. It reads the torch tensors' attributes, checks them and makes
  * the C call. Written against the CPython API alone (no torch headers): a
  * tensor is asked for its dtype, device, strides and address like any object.
  * In Python, with ctypes, the same checks and call take 8.7 us
@@ -256,12 +256,39 @@ static int count_args(const char* name, Py_ssize_t have, Py_ssize_t want) {
   return -1;
 }
 
+/* A table [max_pos, hd] or None: its pointer and rows. */
+static int get_table(PyObject* t, long* dev, long long hd, void** ptr, long long* max_pos) {
+  *ptr = NULL;
+  *max_pos = 0;
+  if (t == Py_None) return 0;
+  Tensor table;
+  if (get_tensor(t, "cos_sin", t_f32, dev, 2, &table) != 0) return -1;
+  if (table.shape[1] != hd || table.shape[0] < 1) return bad_shape("cos_sin must be [max_pos, head_dim], not empty");
+  *ptr = table.ptr;
+  *max_pos = table.shape[0];
+  return fits_i32(*max_pos, 0, 0);
+}
+
+/* Norm weights [hd] or None. */
+static int get_weight(PyObject* t, const char* name, long* dev, long long hd, void** ptr) {
+  *ptr = NULL;
+  if (t == Py_None) return 0;
+  Tensor w;
+  if (get_tensor(t, name, t_bf16, dev, 1, &w) != 0) return -1;
+  if (w.shape[0] != hd) {
+    PyErr_Format(PyExc_ValueError, "%s must be [head_dim]", name);
+    return -1;
+  }
+  *ptr = w.ptr;
+  return 0;
+}
+
 /* (k_new, v_new, positions, slot_mapping, cos_sin, k_pages, v_pages, kv_scales or None, workspace, q, q_out, q_weight,
  * k_weight, eps, stream); an 8-bit append where fp8 */
 static PyObject* append_any(PyObject* const* a, Py_ssize_t n_args, int fp8) {
   if (count_args("append_rope", n_args, 15) != 0) return NULL;
   long dev = -1, back;
-  Tensor kp, vp, sc, slots, k, v, q, q_out, table, pos, w;
+  Tensor kp, vp, sc, slots, k, v, q, q_out, pos;
   pkv_cache_desc d;
   if (get_cache(a[5], a[6], fp8 ? a[7] : NULL, &dev, &kp, &vp, &sc, &d) != 0) return NULL;
   if (get_tensor(a[3], "slot_mapping", t_i32, &dev, -1, &slots) != 0) return NULL;
@@ -283,23 +310,15 @@ static PyObject* append_any(PyObject* const* a, Py_ssize_t n_args, int fp8) {
   } else if (a[10] != Py_None || a[11] != Py_None) {
     return bad_shape("q_out and q_weight come with q"), NULL;
   }
-  table.ptr = pos.ptr = NULL;
-  long long max_pos = 0;
-  if (a[4] != Py_None) {
-    if (get_tensor(a[4], "cos_sin", t_f32, &dev, 2, &table) != 0) return NULL;
-    if (table.shape[1] != hd) return bad_shape("cos_sin must be [max_pos, head_dim]"), NULL;
+  void *table, *qw, *kw;
+  long long max_pos;
+  if (get_table(a[4], &dev, hd, &table, &max_pos) != 0) return NULL;
+  pos.ptr = NULL;
+  if (table != NULL) {
     if (get_tensor(a[2], "positions", t_i32, &dev, -1, &pos) != 0) return NULL;
     if (numel(&pos) != n) return bad_shape("positions and slot_mapping differ in length"), NULL;
-    max_pos = table.shape[0];
-    if (fits_i32(max_pos, 0, 0) != 0) return NULL;
   }
-  void* weight[2] = {NULL, NULL};
-  for (int i = 0; i < 2; ++i) {
-    if (a[11 + i] == Py_None) continue;
-    if (get_tensor(a[11 + i], i ? "k_weight" : "q_weight", t_bf16, &dev, 1, &w) != 0) return NULL;
-    if (w.shape[0] != hd) return bad_shape(i ? "k_weight must be [head_dim]" : "q_weight must be [head_dim]"), NULL;
-    weight[i] = w.ptr;
-  }
+  if (get_weight(a[11], "q_weight", &dev, hd, &qw) != 0 || get_weight(a[12], "k_weight", &dev, hd, &kw) != 0) return NULL;
   const double eps = PyFloat_AsDouble(a[13]);
   if (eps == -1.0 && PyErr_Occurred()) return NULL;
   void* ws;
@@ -309,11 +328,11 @@ static PyObject* append_any(PyObject* const* a, Py_ssize_t n_args, int fp8) {
   if (enter_device(dev, &back) != 0) return NULL;
   int rc;
   Py_BEGIN_ALLOW_THREADS;
-  rc = fp8 ? pkv_append_rope_fp8(q.ptr, qs, k.ptr, ks, v.ptr, vs, pos.ptr, slots.ptr, (int32_t)n, table.ptr,
-                                 (int32_t)max_pos, weight[0], weight[1], (float)eps, q_out.ptr, kp.ptr, vp.ptr, sc.ptr,
+  rc = fp8 ? pkv_append_rope_fp8(q.ptr, qs, k.ptr, ks, v.ptr, vs, pos.ptr, slots.ptr, (int32_t)n, table,
+                                 (int32_t)max_pos, qw, kw, (float)eps, q_out.ptr, kp.ptr, vp.ptr, sc.ptr,
                                  &d, stream, ws, ws_bytes)
-           : pkv_append_rope(q.ptr, qs, k.ptr, ks, v.ptr, vs, pos.ptr, slots.ptr, (int32_t)n, table.ptr,
-                             (int32_t)max_pos, weight[0], weight[1], (float)eps, q_out.ptr, kp.ptr, vp.ptr, &d, stream,
+           : pkv_append_rope(q.ptr, qs, k.ptr, ks, v.ptr, vs, pos.ptr, slots.ptr, (int32_t)n, table,
+                             (int32_t)max_pos, qw, kw, (float)eps, q_out.ptr, kp.ptr, vp.ptr, &d, stream,
                              ws, ws_bytes);
   Py_END_ALLOW_THREADS;
   return leave_device(back, rc);
@@ -329,6 +348,26 @@ static PyObject* append_rope_fp8(PyObject* self, PyObject* const* a, Py_ssize_t 
   return append_any(a, n, 1);
 }
 
+/* What a decode call takes besides its cache: q, out, block table and lengths, checked against each other. */
+static int get_step(PyObject* q, PyObject* out, PyObject* table, PyObject* lens, long* dev, pkv_cache_desc* d, Tensor* tq,
+                    Tensor* to, Tensor* bt, Tensor* sl) {
+  if (get_tensor(q, "q", t_bf16, dev, 3, tq) != 0 || get_tensor(out, "out", t_bf16, dev, 3, to) != 0 ||
+      get_tensor(table, "block_table", t_i32, dev, 2, bt) != 0 || get_tensor(lens, "seq_lens", t_i32, dev, -1, sl) != 0)
+    return -1;
+  if (tq->shape[2] != d->head_dim || !same_shape(tq, to) || bt->shape[0] != tq->shape[0] || numel(sl) != tq->shape[0])
+    return bad_shape("shape mismatch");
+  if (fits_i32(tq->shape[0], tq->shape[1], bt->shape[1]) != 0) return -1;
+  d->num_q_heads = (int32_t)tq->shape[1];
+  return 0;
+}
+
+static int get_flags(PyObject* o, uint32_t* flags) {
+  const unsigned long f = PyLong_AsUnsignedLong(o);
+  if (f == (unsigned long)-1 && PyErr_Occurred()) return -1;
+  *flags = (uint32_t)f;
+  return 0;
+}
+
 /* (q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, scale, workspace, stream, flags) */
 static PyObject* decode_attn_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
   (void)self;
@@ -336,19 +375,11 @@ static PyObject* decode_attn_fp8(PyObject* self, PyObject* const* a, Py_ssize_t 
   long dev = -1, back;
   Tensor kp, vp, sc, q, bt, sl, out;
   pkv_cache_desc d;
+  uint32_t flags;
   if (get_cache(a[1], a[2], a[3], &dev, &kp, &vp, &sc, &d) != 0) return NULL;
-  if (get_tensor(a[0], "q", t_bf16, &dev, 3, &q) != 0 || get_tensor(a[6], "out", t_bf16, &dev, 3, &out) != 0 ||
-      get_tensor(a[4], "block_table", t_i32, &dev, 2, &bt) != 0 ||
-      get_tensor(a[5], "seq_lens", t_i32, &dev, -1, &sl) != 0)
-    return NULL;
-  if (q.shape[2] != d.head_dim || !same_shape(&q, &out) || bt.shape[0] != q.shape[0] || numel(&sl) != q.shape[0])
-    return bad_shape("shape mismatch"), NULL;
-  if (fits_i32(q.shape[0], q.shape[1], bt.shape[1]) != 0) return NULL;
-  d.num_q_heads = (int32_t)q.shape[1];
+  if (get_step(a[0], a[6], a[4], a[5], &dev, &d, &q, &out, &bt, &sl) != 0) return NULL;
   const double scale = PyFloat_AsDouble(a[7]);
-  if (scale == -1.0 && PyErr_Occurred()) return NULL;
-  const unsigned long flags = PyLong_AsUnsignedLong(a[10]);
-  if (flags == (unsigned long)-1 && PyErr_Occurred()) return NULL;
+  if ((scale == -1.0 && PyErr_Occurred()) || get_flags(a[10], &flags) != 0) return NULL;
   void* ws;
   size_t ws_bytes;
   pkv_stream_t stream;
@@ -357,7 +388,44 @@ static PyObject* decode_attn_fp8(PyObject* self, PyObject* const* a, Py_ssize_t 
   int rc;
   Py_BEGIN_ALLOW_THREADS;
   rc = pkv_decode_attn_fp8(q.ptr, kp.ptr, vp.ptr, sc.ptr, bt.ptr, sl.ptr, out.ptr, (float)scale, stream, &d,
-                           (int32_t)q.shape[0], (int32_t)bt.shape[1], ws, ws_bytes, (uint32_t)flags);
+                           (int32_t)q.shape[0], (int32_t)bt.shape[1], ws, ws_bytes, flags);
+  Py_END_ALLOW_THREADS;
+  return leave_device(back, rc);
+}
+
+/* (q, k_new, v_new, k_pages, v_pages, kv_scales, block_table, seq_lens, cos_sin, out, scale, workspace, q_weight,
+ * k_weight, eps, stream, flags) */
+static PyObject* decode_append_attn_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  (void)self;
+  if (count_args("decode_append_attn_fp8", n_args, 17) != 0) return NULL;
+  long dev = -1, back;
+  Tensor kp, vp, sc, q, k, v, bt, sl, out;
+  pkv_cache_desc d;
+  uint32_t flags;
+  if (get_cache(a[3], a[4], a[5], &dev, &kp, &vp, &sc, &d) != 0) return NULL;
+  if (get_step(a[0], a[9], a[6], a[7], &dev, &d, &q, &out, &bt, &sl) != 0) return NULL;
+  if (get_tensor(a[1], "k_new", t_bf16, &dev, 3, &k) != 0 || get_tensor(a[2], "v_new", t_bf16, &dev, 3, &v) != 0)
+    return NULL;
+  if (!same_shape(&k, &v) || k.shape[0] != q.shape[0] || k.shape[1] != d.num_kv_heads || k.shape[2] != d.head_dim)
+    return bad_shape("k_new and v_new are [batch, num_kv_heads, head_dim]"), NULL;
+  void *table, *qw, *kw, *ws;
+  long long max_pos;
+  if (get_table(a[8], &dev, d.head_dim, &table, &max_pos) != 0 ||
+      get_weight(a[12], "q_weight", &dev, d.head_dim, &qw) != 0 || get_weight(a[13], "k_weight", &dev, d.head_dim, &kw) != 0)
+    return NULL;
+  const double scale = PyFloat_AsDouble(a[10]);
+  if (scale == -1.0 && PyErr_Occurred()) return NULL;
+  const double eps = PyFloat_AsDouble(a[14]);
+  if ((eps == -1.0 && PyErr_Occurred()) || get_flags(a[16], &flags) != 0) return NULL;
+  size_t ws_bytes;
+  pkv_stream_t stream;
+  if (get_workspace(a[11], dev, &ws, &ws_bytes) != 0 || get_stream(a[15], dev, &stream) != 0) return NULL;
+  if (enter_device(dev, &back) != 0) return NULL;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = pkv_decode_append_attn_fp8(q.ptr, k.ptr, v.ptr, kp.ptr, vp.ptr, sc.ptr, bt.ptr, sl.ptr, table, (int32_t)max_pos, qw,
+                                  kw, (float)eps, out.ptr, (float)scale, stream, &d, (int32_t)q.shape[0],
+                                  (int32_t)bt.shape[1], ws, ws_bytes, flags);
   Py_END_ALLOW_THREADS;
   return leave_device(back, rc);
 }
@@ -396,6 +464,7 @@ static PyMethodDef methods[] = {
     {"append_rope", (PyCFunction)(void (*)(void))append_rope, METH_FASTCALL, NULL},
     {"append_rope_fp8", (PyCFunction)(void (*)(void))append_rope_fp8, METH_FASTCALL, NULL},
     {"decode_attn_fp8", (PyCFunction)(void (*)(void))decode_attn_fp8, METH_FASTCALL, NULL},
+    {"decode_append_attn_fp8", (PyCFunction)(void (*)(void))decode_append_attn_fp8, METH_FASTCALL, NULL},
     {"expand_fp8", (PyCFunction)(void (*)(void))expand_fp8, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 

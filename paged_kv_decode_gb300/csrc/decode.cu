@@ -97,20 +97,26 @@ size_t decode_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, i
   return off;
 }
 
-int launch_decode_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
-                      const int32_t* block_table, const int32_t* seq_lens, void* out, float scale, int num_q_heads,
-                      int num_kv_heads, int head_dim, int32_t batch, int32_t max_pages, int32_t num_pages,
-                      void* workspace, int num_sms, cudaStream_t stream, uint32_t flags) {
+int launch_decode_fp8(const DecodeFp8& f, int num_q_heads, int num_kv_heads, int head_dim, int32_t batch,
+                      int32_t max_pages, int32_t num_pages, void* workspace, int num_sms, cudaStream_t stream,
+                      uint32_t flags) {
   if (!decode_supported(num_q_heads, num_kv_heads, head_dim, kPageSize)) return PKV_ERR_UNSUPPORTED;
   DecodeLaunch c = {};
-  c.q = q;
-  c.k_pages = k_pages;
-  c.v_pages = v_pages;
-  c.scales = kv_scales;
-  c.block_table = block_table;
-  c.seq_lens = seq_lens;
-  c.out = out;
-  c.scale = scale;
+  c.q = f.q;
+  c.k_new = f.k_new;
+  c.v_new = f.v_new;
+  c.k_pages = f.k_pages;
+  c.v_pages = f.v_pages;
+  c.scales = f.kv_scales;
+  c.block_table = f.block_table;
+  c.seq_lens = f.seq_lens;
+  c.rope = f.rope;
+  c.rope_max_pos = f.rope_max_pos;
+  c.q_weight = f.q_weight;
+  c.k_weight = f.k_weight;
+  c.eps = f.eps;
+  c.out = f.out;
+  c.scale = f.scale;
   c.hq = num_q_heads;
   c.hkv = num_kv_heads;
   c.head_dim = head_dim;
@@ -131,13 +137,12 @@ int launch_decode(const void* q, const void* k_new, const void* v_new, const voi
                   int32_t max_pages, int32_t num_pages, void* workspace, int num_sms, cudaStream_t stream,
                   uint32_t flags) {
   if (!decode_supported(num_q_heads, num_kv_heads, head_dim, kPageSize)) return PKV_ERR_UNSUPPORTED;
-  DecodeLaunch c;
+  DecodeLaunch c = {};
   c.q = q;
   c.k_new = k_new;
   c.v_new = v_new;
   c.k_pages = k_pages;
   c.v_pages = v_pages;
-  c.scales = nullptr;
   c.block_table = block_table;
   c.seq_lens = seq_lens;
   c.rope = rope;

@@ -61,9 +61,12 @@
 //    17.8 us (82.6 MB; 12.3), 27 of 9 to 8000 at 32 query / 8 KV heads 37.3 us
 //    (212 MB; 31.7). Of the first, 1.8 us pass before the first copies go out
 //    (the wait, the length scan, the block table), 8.2 stream at 6.1 TB/s and
-//    1.5 end and merge the split pieces. There is no fused append (a row is
-//    quantised as a whole first); in early mode the requests' last units, which
-//    hold the new rows, wait for the predecessor.
+//    1.5 end and merge the split pieces. In the fused step a row warp
+//    turns (norm, rotation) each piece's query rows and turns and quantises its
+//    new row while the piece before streams; the consumer that takes the request's
+//    last unit writes the row over the staged slot and into the pool; the producer never waits
+//    for the predecessor in early mode. Attention alone, in early mode, waits
+//    with the requests' last units, which hold rows that the predecessor wrote.
 //  * The query rows of the next piece are copied into shared memory (cp.async)
 //    while the current piece streams, so a piece boundary costs no round trip.
 //  * At the end of a piece the warps merge through shared memory (at most four
@@ -98,6 +101,7 @@
 #include "pkv_fp8.cuh"
 #include "pkv_kernels.h"
 #include "pkv_mma.cuh"
+#include "pkv_rows.cuh"
 #include "pkv_tc.cuh"
 
 namespace pkv {
@@ -150,6 +154,9 @@ struct DecodeArgs {
   __nv_bfloat16* out;  // [batch][hq][D]
   const float* rope;  // optional cos/sin table [rope_max_pos][D] fp32 (cos[D/2], sin[D/2]), nullptr = none
   int rope_max_pos;
+  const __nv_bfloat16* q_weight;  // fused 8-bit step: optional [D] weights of the rows' RMS norm, and its eps
+  const __nv_bfloat16* k_weight;
+  float eps;
   float qscale;  // scale * log2(e)
   int early;     // prefetch before the grid dependency (caller guarantees the predecessor leaves
                  // pools, block table and lengths alone)
@@ -218,8 +225,10 @@ struct DecGeo {
   static constexpr int kSmemQ = 2 * kQBuf;              // this piece's rows and the next piece's
   static constexpr int kSmemCs = 2 * kCsB;              // rows for this piece's and the next piece's position
   static constexpr int kSmemScales = kFp8 ? kStages * kUnitPages * kScaleBytes : 0;  // the stages' row scales
+  static constexpr int kNewB = 4 * D + 16;              // a new token's K and V rows of one head (bf16, then codes)
+  static constexpr int kSmemNew = kFp8 ? 2 * kNewB : 0;  // of this piece's request and the next piece's
   static constexpr int kSmemFixed =
-      kSmemAlign + kSmemRing + kSmemBars + kSmemMerge + kSmemQ + kSmemCs + kSmemScales + kSmemMisc;
+      kSmemAlign + kSmemRing + kSmemBars + kSmemMerge + kSmemQ + kSmemCs + kSmemScales + kSmemNew + kSmemMisc;
   // The 8-bit cache's shape, in units of two pages (16/8/128, us of a step's decode attention): a boundary costs 4 /
   // 8 / 12 / 16 / 32 units: bs16 14.1 / 13.4 / 14.0 / 14.2 / 16.8; 2 / 3 / 4 / 8 units a round: bs16 14.4 / 13.6 /
   // 13.4 / 14.1, 40k (narrow) 19.9 / 19.1 / 19.2 / 19.7; 2 or 3 stages a consumer: bs16 14.3 / 13.4. Shares of one unit: two
@@ -467,15 +476,27 @@ __device__ __forceinline__ void store_lane_state(float* mw, int lane, int h0, co
   }
 }
 
+// Threads of a CTA: the fused step of the 8-bit cache has a row warp behind the producers.
+template <class Geo, bool kFused>
+struct DecThreads {
+  static constexpr int n = Geo::kThreads + (Geo::kFp8 && kFused ? 32 : 0);
+};
+// Barrier of the consumers and the row warp: a piece's rows are ready, the buffers of the piece before it free.
+template <class Geo>
+__device__ __forceinline__ void row_sync() {
+  asm volatile("bar.sync 2, %0;" ::"n"(Geo::kConsumerThreads + 32) : "memory");
+}
+
 // kFused: a.k_new / a.v_new are given (fused append); kRope: a.rope is given too;
 // kPolled: the polled merge, else the counted one. Each combination is its own
 // instantiation, so a path carries no code (and no registers) for the others.
 template <class Geo, bool kFused, bool kRope, bool kPolled>
-__global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(const __grid_constant__ CUtensorMap kmap,
+__global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm) decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                              const __grid_constant__ CUtensorMap vmap,
                                                                              const DecodeArgs a) {
   constexpr int D = Geo::D, G = Geo::G, kKS = Geo::kKS, kRing = Geo::kRing, kStages = Geo::kStages;
   constexpr int kRec = Geo::kRec, kMH = Geo::kMH, kLW = Geo::kLW;
+  constexpr bool kRowWarp = Geo::kFp8 && kFused;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((kSmemAlign - (smem_u32(smem_raw) & (kSmemAlign - 1))) & (kSmemAlign - 1));
   unsigned char* ring = smem;
@@ -485,7 +506,8 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
   unsigned char* qbuf = reinterpret_cast<unsigned char*>(merge + Geo::kMergeFloats);
   unsigned char* csbuf = qbuf + Geo::kSmemQ;
   unsigned char* scbuf = csbuf + Geo::kSmemCs;  // (8-bit cache) kScaleBytes per stage
-  int* flag = reinterpret_cast<int*>(scbuf + Geo::kSmemScales);  // [0..1] merge flags, [2] a wait failed, [4..5] share
+  unsigned char* newbuf = scbuf + Geo::kSmemScales;  // (8-bit cache, fused step) kNewB per piece
+  int* flag = reinterpret_cast<int*>(newbuf + Geo::kSmemNew);  // [0..1] merge flags, [2] a wait failed, [4..5] share
   int* pref = flag + kSmemMisc / 4;
   int* sl = pref + a.batch + 1;
   int* pcp = sl + a.batch;  // [batch + 1] non-empty (request, KV head) pairs before each request
@@ -608,7 +630,7 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
       grid_dependency_wait();
       allow_dependents();
     }
-    zero_empty_rows(0, Geo::kThreads);
+    zero_empty_rows(0, DecThreads<Geo, kFused>::n);
     return;
   }
   // the polled instantiation (batches, many short pairs) prices a pair boundary; the counted one
@@ -632,7 +654,7 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
   // consumer, and a round could wait on a consumer held at a piece boundary by
   // a page of a later round (a deadlock). Smaller rounds land a CTA's first
   // pages sooner; one SIMT copy instruction per round amortises the issue.
-  if (warp >= Geo::kConsumers) {
+  if (warp >= Geo::kConsumers && warp < Geo::kConsumers + Geo::kProducers) {
     const int fed0 = (warp - Geo::kConsumers) * Geo::kFed;  // this producer's first consumer
     const uint64_t policy = policy_evict_first();
     const unsigned lt_mask = (1u << lane) - 1u;
@@ -663,7 +685,7 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
           two = true;
         }
         last = p == np - 1;
-        if (kRope && p == np - 1) wslot = (sl[b] - 1) % kPageSize;  // the new token's slot (rotated append)
+        if (kRope && !Geo::kFp8 && p == np - 1) wslot = (sl[b] - 1) % kPageSize;  // the new token's slot (rotated append)
       }
       const unsigned same = __match_any_sync(kFull, valid ? c : -1);
       const int idx = __popc(same & lt_mask);  // earlier lanes of this chunk feeding the same consumer
@@ -723,7 +745,7 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
       // New rows come from the predecessor. Without the rotary embedding the consumer that takes
       // a request's last page writes the new row into the staged page and into the pool, so
       // every page goes out at once, whatever the slot of the new row holds now.
-      if constexpr (Geo::kFp8) {
+      if constexpr (Geo::kFp8 && !kFused) {
         // In early mode the predecessor may write the rows at seq_len - 1: the requests' last units wait for it.
         const unsigned nmask = __ballot_sync(kFull, valid && last);
         int from = 0;  // lanes already issued
@@ -735,7 +757,7 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
           waited = true;
         }
         issue_rounds(from, 32);
-      } else if (!kRope) {
+      } else if (!kRope || Geo::kFp8) {
         issue_rounds(0, 32);
       } else {
         // With it the whole warp writes the rows: every page of this chunk that holds its
@@ -791,11 +813,96 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
       }
       pfail = __any_sync(kFull, pfail);
     }
-    if (!(kRope || Geo::kFp8) || !waited) {
+    if (!(Geo::kFp8 ? !kFused : kRope) || !waited) {
       grid_dependency_wait();
       allow_dependents();
     }
     return;
+  }
+
+  // ============================================================== row warp (fused step of the 8-bit cache)
+  // For each piece, while the one before it streams: its query rows normalised and rotated as the append would, into
+  // qbuf in bf16, and (where the piece holds the request's last unit) the new token's K and V rows turned and
+  // quantised into newbuf, K codes at byte 0, V codes at 2 D, their scale bytes at 4 D. D / 16 lanes take a row: the
+  // group's query rows first, then K, then V. The weights and, for the first piece, the table row are loaded before
+  // the wait for the predecessor in early mode, so that one round trip for the rows is left behind it.
+  if constexpr (kRowWarp) {
+    if (warp == Geo::kConsumers + Geo::kProducers) {
+      constexpr int L = D / 16, kRows = 32 / L;
+      const int l = lane % L;
+      const bool turns = a.rope != nullptr, q_norms = a.q_weight != nullptr, k_norms = a.k_weight != nullptr;
+      Row wq, wk;
+      if (q_norms) {
+        const uint4* wp = reinterpret_cast<const uint4*>(a.q_weight) + l;
+        wq = unpack(__ldg(wp), __ldg(wp + L));
+      }
+      if (k_norms) {
+        const uint4* wp = reinterpret_cast<const uint4*>(a.k_weight) + l;
+        wk = unpack(__ldg(wp), __ldg(wp + L));
+      }
+      Piece p;
+      bool any = find_piece<Geo::kUnit>(lo, hi, pref, sl, batch, p), waited = !a.early;
+#pragma unroll 1
+      for (int buf = 0; any; buf ^= 1) {
+        Turn t;
+        if (turns) {
+          const int last = a.rope_max_pos - 1;
+          if (sl[p.b] - 1 > last && lane == 0) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
+          load_turn<D>(a.rope + static_cast<size_t>(min(sl[p.b] - 1, last)) * D, l, t);
+        }
+        if (!waited) {
+          grid_dependency_wait();
+          allow_dependents();
+          waited = true;
+        }
+        const int rows = gq + (p.p1 == p.np ? 2 : 0);
+        const __nv_bfloat16* q = a.q + (static_cast<size_t>(p.b) * hq + p.h * gq) * D;
+        const size_t kv = (static_cast<size_t>(p.b) * hkv + p.h) * D;
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += kRows) {
+          const int r = min(r0 + lane / L, rows - 1);
+          const bool mine = r0 + lane / L < rows, is_q = r < gq, is_v = r == gq + 1;
+          const uint4* src =
+              reinterpret_cast<const uint4*>(is_q ? q + r * D : (is_v ? a.v_new : a.k_new) + kv) + l;
+          const Row raw = unpack(__ldg(src), __ldg(src + L));
+          Row x = raw;
+          float norm = 1.f;
+          if (q_norms || k_norms || turns) {  // (every lane takes part; a row keeps what applies to it)
+            Row w;
+            const bool norms = is_q ? q_norms : k_norms && !is_v;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w.y[i] = norms ? (is_q ? wq.y[i] : wk.y[i]) : make_float2(1.f, 1.f);
+            norm = turn_row<D>(x, q_norms || k_norms, w, a.eps, turns, t);
+            if (is_v) x = raw;
+            if (!norms) norm = 1.f;
+          }
+          uint2 lo8, hi8;
+          const int scale = quantise_row<D>(x, norm, lo8, hi8);
+          if (is_q) {
+            scale_row(x, norm);
+            if (mine) {
+              unsigned char* to = qbuf + buf * Geo::kQBuf + r * Geo::kRowB + l * 16;
+              *reinterpret_cast<uint4*>(to) = pack4(x.y);
+              *reinterpret_cast<uint4*>(to + D) = pack4(x.y + 4);
+            }
+          } else if (mine) {
+            unsigned char* to = newbuf + buf * Geo::kNewB;
+            unsigned char* row = to + (is_v ? 2 * D : 0) + l * 8;
+            *reinterpret_cast<uint2*>(row) = lo8;
+            *reinterpret_cast<uint2*>(row + D / 2) = hi8;
+            if (l == 0) to[4 * D + (is_v ? 1 : 0)] = static_cast<unsigned char>(scale);
+          }
+        }
+        row_sync<Geo>();
+        any = find_piece<Geo::kUnit>(p.fend, hi, pref, sl, batch, p);
+      }
+      if (!waited) {
+        grid_dependency_wait();
+        allow_dependents();
+      }
+      return;
+    }
   }
 
   // ============================================================== consumer warps
@@ -866,13 +973,16 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
     allow_dependents();
   }
   zero_empty_rows(0, Geo::kConsumerThreads);
-  if (have) stage_q(pc, 0);
+  if (!kRowWarp && have) stage_q(pc, 0);
   if (warp == 0) cp_async_wait_all();
-  consumer_sync<Geo>();
+  if (kRowWarp && have)
+    row_sync<Geo>();
+  else
+    consumer_sync<Geo>();
   for (int j = 0; have; ++j) {
     Piece nx;
     const bool have_next = find_piece<Geo::kUnit>(pc.fend, hi, pref, sl, batch, nx);
-    if (have_next) stage_q(nx, (j + 1) & 1);
+    if (!kRowWarp && have_next) stage_q(nx, (j + 1) & 1);
     const int b = pc.b;
     const int h = pc.h;
     const bool complete = (pc.p0 == 0 && pc.p1 == pc.np);
@@ -935,16 +1045,18 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
     // the V row from lane D / 8 on) with that page's block-table entry. Once the page is staged it
     // writes them over the copied slot and into the pool.
     const bool takes_new =
-        kFused && !kRope && pc.p1 == pc.np && p_first <= pc.np - 1 && (pc.np - 1 - p_first) % Geo::kConsumers == 0;
+        kFused && (!kRope || Geo::kFp8) && pc.p1 == pc.np && p_first <= pc.np - 1 && (pc.np - 1 - p_first) % Geo::kConsumers == 0;
+    // (8-bit cache: the rows are in newbuf, turned and quantised by the row warp.)
     constexpr int kRowChunks = D / 8;
     uint4 nrow = make_uint4(0u, 0u, 0u, 0u);
     int nid = -1;
     if (takes_new) {
-      if (lane < 2 * kRowChunks)
+      if (!Geo::kFp8 && lane < 2 * kRowChunks)
         nrow = __ldg(reinterpret_cast<const uint4*>((lane < kRowChunks ? a.k_new : a.v_new) +
                                                     (static_cast<size_t>(b) * hkv + h) * D) +
                      lane % kRowChunks);
-      nid = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages + pc.np - 1);
+      nid = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages +
+                  (Geo::kFp8 ? (sl[b] - 1) / kPageSize : pc.np - 1));
     }
     for (int p = p_first; p < pc.p1; p += Geo::kConsumers) {
       const int slot = warp * kRing + k % kRing;
@@ -961,7 +1073,30 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
         const int rem = sl[b] - p * Geo::kUnit;
         const int n_valid = rem < Geo::kUnit ? rem : Geo::kUnit;
         const uint32_t kt = smem_u32(ring + slot * Geo::kStage);
-        if (takes_new && p == pc.np - 1) {
+        if (Geo::kFp8 && takes_new && p == pc.np - 1) {
+          // lanes 0 .. D / 16 - 1 take 16 bytes of the K row's codes each, the next D / 16 the V row's
+          constexpr int L = D / 16;
+          const int t = (sl[b] - 1) % kPageSize, page = (sl[b] - 1) % Geo::kUnit / kPageSize;
+          if (lane < 2 * L) {
+            const int l = lane % L;
+            const bool v = lane >= L;
+            const uint32_t nb = smem_u32(newbuf) + (j & 1) * Geo::kNewB;
+            const uint4 codes = lds128(nb + (v ? 2 * D : 0) + l * 16);
+            const int scale = static_cast<int>(lds8(nb + 4 * D + (v ? 1 : 0))), sc = (v ? kPageSize : 0) + t;
+            sts128(kt + (v ? Geo::kTile : 0) + page * Geo::kPageTile + swz8<D>(t, l), codes);
+            if (l == 0) sts8(smem_u32(scbuf + (slot * Geo::kUnitPages + page) * kScaleBytes) + sc, scale);
+            if (nid >= 0 && nid < a.num_pages) {  // (the producer reports a page id out of the pool)
+              const size_t z = static_cast<size_t>(nid) * hkv + h;
+              unsigned char* pool = reinterpret_cast<unsigned char*>(
+                  const_cast<__nv_bfloat16*>(v ? a.v_pages : a.k_pages));
+              reinterpret_cast<uint4*>(pool + (z * kPageSize + t) * D)[l] = codes;
+              if (l == 0) const_cast<uint8_t*>(a.scales)[z * kScaleBytes + sc] = static_cast<uint8_t>(scale);
+            }
+          }
+          fence_proxy_async_smem();  // the row stores before the stage's next tensor copy
+          __syncwarp();
+        }
+        if (!Geo::kFp8 && takes_new && p == pc.np - 1) {
           const int t = (sl[b] - 1) % kPageSize;  // the new token's slot
           if (lane < 2 * kRowChunks) {
             const int c = lane % kRowChunks;
@@ -1079,7 +1214,11 @@ __global__ void __launch_bounds__(Geo::kThreads, Geo::kCtasPerSm) decode_kernel(
       ++npend;
     }
     if (warp == 0) cp_async_wait_all();  // the next piece's query rows have landed
-    consumer_sync<Geo>();                     // merge buffer and qbuf[j & 1] free, qbuf[(j + 1) & 1] visible
+    // merge buffer and qbuf[j & 1] free, qbuf[(j + 1) & 1] visible
+    if (kRowWarp && have_next)
+      row_sync<Geo>();
+    else
+      consumer_sync<Geo>();
     pc = nx;
     have = have_next;
   }
@@ -1296,6 +1435,9 @@ struct DecodeLaunch {
   const int32_t* seq_lens;
   const float* rope;
   int32_t rope_max_pos;
+  const void* q_weight;  // 8-bit cache only
+  const void* k_weight;
+  float eps;
   void* out;
   float scale;
   int hq, hkv, head_dim;
@@ -1314,11 +1456,11 @@ int launch_decode_d128(const DecodeLaunch& c, int G);
 int launch_decode_fp8_d64(const DecodeLaunch& c, int G);
 int launch_decode_fp8_d128(const DecodeLaunch& c, int G);
 
-// One instantiation (the 8-bit cache has no fused append: its append quantises whole rows first).
+// One instantiation (the 8-bit cache's fused step has one form, with or without table and weights).
 using DecodeKern = void (*)(const CUtensorMap, const CUtensorMap, const DecodeArgs);
 template <class Geo, bool kFused, bool kRope, bool kPolled>
 constexpr DecodeKern decode_instance() {
-  if constexpr (Geo::kFp8 && kFused)
+  if constexpr (Geo::kFp8 && kFused && !kRope)
     return nullptr;
   else
     return decode_kernel<Geo, kFused, kRope, kPolled>;
@@ -1355,7 +1497,9 @@ int launch_decode_geo(const DecodeLaunch& c) {
   const int grid_used = wide ? (c.num_sms < kMaxGrid ? c.num_sms : kMaxGrid) : grid;
   const bool polled = grid_used <= kPollMax * pairs;
   const size_t smem = wide ? GeoW::smem_bytes(c.batch) : Geo::smem_bytes(c.batch);
-  const int threads = wide ? GeoW::kThreads : Geo::kThreads;
+  const bool fused = c.k_new != nullptr;
+  const int threads = wide ? (fused ? DecThreads<GeoW, true>::n : GeoW::kThreads)
+                           : (fused ? DecThreads<Geo, true>::n : Geo::kThreads);
   // (the wide rows are never taken at head_dim 64 with bf16 pages; they name the narrow kernels there so
   // that no such instantiation is built)
   using GW = typename std::conditional<Geo::D == 128 || Geo::kFp8, GeoW, Geo>::type;
@@ -1368,7 +1512,7 @@ int launch_decode_geo(const DecodeLaunch& c) {
        decode_instance<GW, true, true, false>()},
       {decode_instance<GW, false, false, true>(), decode_instance<GW, true, false, true>(),
        decode_instance<GW, true, true, true>()}};
-  const int variant = c.k_new == nullptr ? 0 : c.rope == nullptr ? 1 : 2;
+  const int variant = c.k_new == nullptr ? 0 : c.rope == nullptr && !Geo::kFp8 ? 1 : 2;
   const int shape = (wide ? 2 : 0) + (polled ? 1 : 0);
   const DecodeKern kern = kKerns[shape][variant];
   if (kern == nullptr) return PKV_ERR_UNSUPPORTED;
@@ -1401,6 +1545,9 @@ int launch_decode_geo(const DecodeLaunch& c) {
   a.out = static_cast<__nv_bfloat16*>(c.out);
   a.rope = c.rope;
   a.rope_max_pos = c.rope_max_pos;
+  a.q_weight = static_cast<const __nv_bfloat16*>(c.q_weight);
+  a.k_weight = static_cast<const __nv_bfloat16*>(c.k_weight);
+  a.eps = c.eps;
   a.qscale = c.scale * kLog2e;
   a.early = (c.flags & PKV_DECODE_EARLY_PREFETCH) ? 1 : 0;
   a.batch = c.batch;

@@ -387,29 +387,73 @@ int pkv_append_rope_fp8(const void* q, int64_t q_stride, const void* k_new, int6
                      workspace, workspace_bytes);
 }
 
-int pkv_decode_attn_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
-                        const int32_t* block_table, const int32_t* seq_lens, void* out, float scale,
-                        pkv_stream_t stream, const pkv_cache_desc* desc, int32_t batch, int32_t max_pages_per_seq,
-                        void* workspace, size_t workspace_bytes, uint32_t flags) {
+// Shared by the 8-bit cache's attention alone and its fused step.
+static int decode_fp8(const pkv::DecodeFp8& f, bool fused, pkv_stream_t stream, const pkv_cache_desc* desc,
+                      int32_t batch, int32_t max_pages_per_seq, void* workspace, size_t workspace_bytes,
+                      uint32_t flags) {
   int rc = check_desc_decode(desc);
   if (rc != PKV_OK) return rc;
   if (batch < 0 || max_pages_per_seq < 1 || max_pages_per_seq > kMaxTablePages) return PKV_ERR_BAD_SHAPE;
   if (batch > pkv::decode_max_batch()) return PKV_ERR_UNSUPPORTED;
   if (!table_fits(batch, max_pages_per_seq, desc->num_kv_heads)) return PKV_ERR_BAD_SHAPE;
+  if (fused && (!(f.eps >= 0.f) || (f.rope != nullptr && f.rope_max_pos < 1))) return PKV_ERR_BAD_SHAPE;
   if (workspace == nullptr) return PKV_ERR_NULL_ARG;
   if (batch == 0) return PKV_OK;
-  if (!q || !k_pages || !v_pages || !kv_scales || !block_table || !seq_lens || !out) return PKV_ERR_NULL_ARG;
-  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(kv_scales) || !aligned16(out) ||
-      !aligned16(workspace))
+  if (!f.q || !f.k_pages || !f.v_pages || !f.kv_scales || !f.block_table || !f.seq_lens || !f.out)
+    return PKV_ERR_NULL_ARG;
+  if (fused && (!f.k_new || !f.v_new)) return PKV_ERR_NULL_ARG;
+  if (!aligned16(f.q) || !aligned16(f.k_new) || !aligned16(f.v_new) || !aligned16(f.k_pages) ||
+      !aligned16(f.v_pages) || !aligned16(f.kv_scales) || !aligned16(f.rope) || !aligned16(f.q_weight) ||
+      !aligned16(f.k_weight) || !aligned16(f.out) || !aligned16(workspace))
     return PKV_ERR_MISALIGNED;
   int sms = 0;
   rc = current_device(&sms);
   if (rc != PKV_OK) return rc;
   if (workspace_bytes < decode_ws(desc, batch, sms)) return PKV_ERR_WORKSPACE_TOO_SMALL;
   if ((flags & ~static_cast<uint32_t>(PKV_DECODE_EARLY_PREFETCH)) != 0) return PKV_ERR_UNSUPPORTED;
-  return pkv::launch_decode_fp8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, out, scale, desc->num_q_heads,
-                                desc->num_kv_heads, desc->head_dim, batch, max_pages_per_seq, desc->num_pages,
-                                workspace, sms, reinterpret_cast<cudaStream_t>(stream), flags);
+  return pkv::launch_decode_fp8(f, desc->num_q_heads, desc->num_kv_heads, desc->head_dim, batch, max_pages_per_seq,
+                                desc->num_pages, workspace, sms, reinterpret_cast<cudaStream_t>(stream), flags);
+}
+
+int pkv_decode_attn_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
+                        const int32_t* block_table, const int32_t* seq_lens, void* out, float scale,
+                        pkv_stream_t stream, const pkv_cache_desc* desc, int32_t batch, int32_t max_pages_per_seq,
+                        void* workspace, size_t workspace_bytes, uint32_t flags) {
+  pkv::DecodeFp8 f = {};
+  f.q = q;
+  f.k_pages = k_pages;
+  f.v_pages = v_pages;
+  f.kv_scales = kv_scales;
+  f.block_table = block_table;
+  f.seq_lens = seq_lens;
+  f.out = out;
+  f.scale = scale;
+  return decode_fp8(f, false, stream, desc, batch, max_pages_per_seq, workspace, workspace_bytes, flags);
+}
+
+int pkv_decode_append_attn_fp8(const void* q, const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                               void* kv_scales, const int32_t* block_table, const int32_t* seq_lens,
+                               const float* rope_cos_sin, int32_t rope_max_pos, const void* q_weight,
+                               const void* k_weight, float eps, void* out, float scale, pkv_stream_t stream,
+                               const pkv_cache_desc* desc, int32_t batch, int32_t max_pages_per_seq, void* workspace,
+                               size_t workspace_bytes, uint32_t flags) {
+  pkv::DecodeFp8 f = {};
+  f.q = q;
+  f.k_new = k_new;
+  f.v_new = v_new;
+  f.k_pages = k_pages;
+  f.v_pages = v_pages;
+  f.kv_scales = kv_scales;
+  f.block_table = block_table;
+  f.seq_lens = seq_lens;
+  f.rope = rope_cos_sin;
+  f.rope_max_pos = rope_max_pos;
+  f.q_weight = q_weight;
+  f.k_weight = k_weight;
+  f.eps = eps;
+  f.out = out;
+  f.scale = scale;
+  return decode_fp8(f, true, stream, desc, batch, max_pages_per_seq, workspace, workspace_bytes, flags);
 }
 
 int pkv_expand_fp8(const void* k_pages, const void* v_pages, const void* kv_scales, const int32_t* block_table,

@@ -179,7 +179,7 @@ __device__ __forceinline__ void mma_unit_fp8(uint32_t kt, uint32_t vt, uint32_t 
                                              float (&o)[KS][4], float& m0, float& m1, float& l0, float& l1,
                                              int& vmax) {
   constexpr int kTile = kPageSize * KS * 16;  // bytes of a page's K or V
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int lane = threadIdx.x & 31, r = lane >> 2;
   if (nv < kPageSize * NP) {
     // the request's last unit: value rows behind it become zeros (0 times a stale NaN would be NaN)
     for (int i = nv * KS + lane; i < kPageSize * NP * KS; i += 32)

@@ -26,10 +26,26 @@ int launch_decode(const void* q, const void* k_new, const void* v_new, const voi
                   int32_t max_pages, int32_t num_pages, void* workspace, int num_sms, cudaStream_t stream,
                   uint32_t flags);
 // The 8-bit cache (decode_fp8_d64.cu, decode_fp8_d128.cu): the same geometries and workspace.
-int launch_decode_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
-                      const int32_t* block_table, const int32_t* seq_lens, void* out, float scale, int num_q_heads,
-                      int num_kv_heads, int head_dim, int32_t batch, int32_t max_pages, int32_t num_pages,
-                      void* workspace, int num_sms, cudaStream_t stream, uint32_t flags);
+struct DecodeFp8 {
+  const void* q;
+  const void* k_new;  // fused step: the new rows, written at seq_lens - 1; nullptr: attention alone
+  const void* v_new;
+  const void* k_pages;
+  const void* v_pages;
+  const void* kv_scales;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const float* rope;  // fused step: optional table, and norm weights
+  int32_t rope_max_pos;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  void* out;
+  float scale;
+};
+int launch_decode_fp8(const DecodeFp8& f, int num_q_heads, int num_kv_heads, int head_dim, int32_t batch,
+                      int32_t max_pages, int32_t num_pages, void* workspace, int num_sms, cudaStream_t stream,
+                      uint32_t flags);
 int decode_max_batch();
 
 // Append with the rotary embedding and per-head norm (append_rope.cu): head_dim 64 or 128, page size 16.

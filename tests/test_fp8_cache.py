@@ -69,6 +69,29 @@ def test_decode_host_argument_checks(lib):
     assert call(batch=0) == 0
 
 
+def test_decode_append_host_argument_checks(lib):
+    buf = ctypes.create_string_buffer(1024)
+    p = (ctypes.addressof(buf) + 255) // 256 * 256
+
+    def call(desc=_desc(), q=p, k=p, v=p, kp=p, vp=p, sc=p, bt=p, sl=p, table=p, max_pos=8, qw=p, kw=p, eps=1e-6, out=p,
+             batch=2, width=4, ws=p, nb=64):
+        return lib.pkv_decode_append_attn_fp8(q, k, v, kp, vp, sc, bt, sl, table, max_pos, qw, kw, eps, out, 1.0, None,
+                                              None if desc is None else ctypes.byref(desc), batch, width, ws, nb, 0)
+
+    assert call(desc=None) == -1
+    for bad in (_desc(head_dim=96), _desc(page_size=32), _desc(num_q_heads=36, num_kv_heads=4)):
+        assert call(desc=bad) == -3
+    assert call(batch=-1) == -2 and call(width=0) == -2 and call(width=1 << 27, batch=1) == -2
+    assert call(batch=1025) == -3 and call(batch=1024, width=1 << 18) == -2
+    assert call(max_pos=0) == -2 and call(eps=-1.0) == -2 and call(eps=float("nan")) == -2
+    assert call(ws=None) == -1
+    for name in ("q", "k", "v", "kp", "vp", "sc", "bt", "sl", "out"):
+        assert call(**{name: None}) == -1, name
+    for name in ("q", "k", "v", "kp", "vp", "sc", "table", "qw", "kw", "out", "ws"):
+        assert call(**{name: p + 8}) == -8, name
+    assert call(batch=0) == 0
+
+
 def test_expand_host_argument_checks(lib):
     buf = ctypes.create_string_buffer(1024)
     p = (ctypes.addressof(buf) + 255) // 256 * 256
@@ -505,6 +528,144 @@ def test_decode_early_prefetch_behind_the_append(cuda_device, geom, lens):
     assert torch.isfinite(got.float()).all() and torch.equal(got.view(torch.int16), want.view(torch.int16))
     for a, b in zip(got_caches, want_caches):
         assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
+class Step:
+    """Layers of new rows for a cache's requests, each layer with its own copy of the cache: the fused step, or the
+    append and the attention as two calls."""
+
+    def __init__(self, c, layers, seed, dev, *, rope, norm):
+        self.c, self.layers = c, layers
+        n, (hq, hkv, d) = len(c.lens), (c.hq, c.hkv, c.d)
+        gen = torch.Generator().manual_seed(seed)
+        draw = lambda heads: torch.randn(layers, n, heads, d, generator=gen).to(torch.bfloat16).to(dev)  # noqa: E731
+        self.q, self.k, self.v = draw(hq), draw(hkv), draw(hkv)
+        j = np.maximum(c.lens, 1) - 1
+        slots = np.where(c.lens > 0, c.bt[np.arange(n), j // 16] * 16 + j % 16, -1)
+        for b in range(n):  # the new rows' slots hold NaN until a call has written them
+            if slots[b] >= 0:
+                c.k.view(torch.uint8)[slots[b] // 16, :, slots[b] % 16] = NAN_CODE
+                c.v.view(torch.uint8)[slots[b] // 16, :, slots[b] % 16] = NAN_CODE
+                c.s.view(torch.uint8)[slots[b] // 16, :, :, slots[b] % 16] = 0xFF
+        self.pos, self.slots = i32(j, dev), i32(slots, dev)
+        self.table = pkv.rope_cos_sin(1e6, max(1, int(c.lens.max())), d, dev) if rope else None
+        w = (1 + 0.2 * torch.randn(2, d, generator=gen)).to(torch.bfloat16).to(dev)
+        self.qw, self.kw = (w[0].contiguous() if "q" in norm else None), (w[1].contiguous() if "k" in norm else None)
+        self.caches = lambda: [(c.k.clone(), c.v.clone(), c.s.clone()) for _ in range(layers)]
+
+    def two_calls(self, caches, outs):
+        c = self.c
+        q = torch.empty_like(self.q[0])
+        for i in range(self.layers):
+            pkv.append_rope_fp8(self.k[i], self.v[i], self.pos, self.slots, self.table, *caches[i], c.ws, q=self.q[i],
+                                q_out=q, q_weight=self.qw, k_weight=self.kw)
+            pkv.decode_attn_fp8(q, *caches[i], c.block_table, c.seq_lens, outs[i], c.scale, c.ws)
+
+    def fused(self, caches, outs, early):
+        c = self.c
+        for i in range(self.layers):
+            pkv.decode_append_attn_fp8(self.q[i], self.k[i], self.v[i], *caches[i], c.block_table, c.seq_lens, self.table,
+                                       outs[i], c.scale, c.ws, q_weight=self.qw, k_weight=self.kw, early_prefetch=early)
+
+
+STEP_LENS = [[1, 16, 17, 32, 33], [500, 0, 1777, 48, 64], [9000], [3, 700, 31, 32, 1999, 15, 1, 310, 5, 6, 7, 8, 40, 900]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rope,norm", [(True, "qk"), (True, ""), (False, "k"), (False, "")])
+@pytest.mark.parametrize("lens", STEP_LENS, ids=str)
+@pytest.mark.parametrize("geom", ["16q8kv128", "14q2kv64", "28q4kv128", "64q8kv128", "8q1kv64"])
+def test_fused_step_has_the_two_calls_bits(cuda_device, geom, lens, rope, norm):
+    """Outputs, rows and scales of the fused step, eager and as a replayed chain of layers with early prefetch."""
+    c = Cache(40, GEOMS[geom], lens, cuda_device, width=2500 if lens == [9000] else None)
+    st = Step(c, 3, 41, cuda_device, rope=rope, norm=norm)
+    want, want_caches = torch.full_like(st.q, float("nan")), st.caches()
+    st.two_calls(want_caches, want)
+    got, got_caches = torch.full_like(st.q, float("nan")), st.caches()
+    st.fused(got_caches, got, False)
+    chain, chain_caches = torch.full_like(st.q, float("nan")), st.caches()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.fused(chain_caches, chain, True)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert c.ws.status() == 0
+    assert torch.isfinite(want.float()).all()
+    for out, caches in ((got, got_caches), (chain, chain_caches)):
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        for a, b in zip(caches, want_caches):
+            assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
+def test_fused_step_against_float64(cuda_device):
+    """The fused step's outputs against float64 over the rows that it left in the cache."""
+    c = Cache(42, GEOMS["16q8kv128"], [333, 1, 90, 0, 1600], cuda_device)
+    st = Step(c, 1, 43, cuda_device, rope=True, norm="qk")
+    caches = st.caches()
+    out = torch.full_like(st.q, float("nan"))
+    st.fused(caches, out, False)
+    torch.cuda.synchronize()
+    c.kc, c.vc, c.sc = (codes_of(x) for x in caches[0])
+    table = bf16_to_f64(st.table)
+    got = bf16_to_f64(out)[0]
+    for b, n in enumerate(c.lens):
+        if n == 0:
+            assert (got[b] == 0).all()
+            continue
+        cs = table[n - 1:n]
+        y, size = rotate64(bf16_to_f64(st.q[0, b:b + 1]), bf16_to_f64(st.qw), cs, 1e-6)
+        k, v = c.rows(b, 0), c.rows(b, 1)
+        yk, _ = rotate64(bf16_to_f64(st.k[0, b:b + 1]), bf16_to_f64(st.kw), cs, 1e-6)
+        top = np.abs(yk).max(axis=-1, keepdims=True)
+        # half an e4m3 step (2^-4, or 2^-10 of a scale of at most top / 224), with room for fp32
+        assert (np.abs(k[n - 1] - yk[0]) <= np.maximum(2.0 ** -4 * np.abs(yk[0]), 2.0 ** -10 / 224 * top[0]) * 1.001).all()
+        out64, absolute, qk = attention64(y[0], k, v, c.scale)
+        # the query's rounding to bf16 moves a score by at most 2^-8 of scale * sum |q||k|
+        tol = decode_bound(out64, absolute, qk, c.scale, c.d, int(n), np.abs(v).max())
+        tol += 2 * 2.0 ** -8 * c.scale * qk[:, None] * absolute
+        assert (np.abs(got[b] - out64) <= tol).all(), b
+
+
+@pytest.mark.gpu
+def test_fused_step_reports_and_refuses(cuda_device):
+    c = Cache(44, GEOMS["16q8kv128"], [40, 100, 7], cuda_device)
+    st = Step(c, 1, 45, cuda_device, rope=True, norm="qk")
+    caches, out = st.caches(), torch.empty_like(st.q)
+    # a table that is too short: reported, clamped to its last row
+    short = st.table[:60].contiguous()
+    call = lambda **kw: pkv.decode_append_attn_fp8(  # noqa: E731
+        **{**dict(q=st.q[0], k_new=st.k[0], v_new=st.v[0], k_pages=caches[0][0], v_pages=caches[0][1],
+                  kv_scales=caches[0][2], block_table=c.block_table, seq_lens=c.seq_lens, cos_sin=st.table, out=out[0],
+                  scale=c.scale, workspace=c.ws, q_weight=st.qw, k_weight=st.kw), **kw})
+    call(cos_sin=short)
+    torch.cuda.synchronize()
+    assert c.ws.status() == -7
+    pkv.workspace_init(c.ws.tensor)
+    # the new row's page outside the pool: nothing is written there, the others are served
+    caches = st.caches()
+    before = [x.clone() for x in caches[0]]
+    bt = c.bt.copy()
+    bt[1, 6] = c.kc.shape[0]  # request 1's last page (100 tokens)
+    call(k_pages=caches[0][0], v_pages=caches[0][1], kv_scales=caches[0][2], block_table=i32(bt, cuda_device))
+    torch.cuda.synchronize()
+    assert c.ws.status() == -7
+    page = c.bt[1, 6]
+    for x, y in zip(caches[0], before):
+        assert torch.equal(x.view(torch.uint8)[page], y.view(torch.uint8)[page])
+        assert not torch.equal(x.view(torch.uint8)[c.bt[0, 2]], y.view(torch.uint8)[c.bt[0, 2]])
+    pkv.workspace_init(c.ws.tensor)
+    for bad, error in ((dict(k_new=st.k[0].float()), TypeError), (dict(k_new=st.k[0][:2]), ValueError),
+                       (dict(v_new=st.v[0][:, :4].contiguous()), ValueError), (dict(q=st.q[0][:2]), ValueError),
+                       (dict(cos_sin=st.table[:, :64].contiguous()), ValueError), (dict(cos_sin=st.table[:0]), ValueError),
+                       (dict(k_weight=st.kw[:64].contiguous()), ValueError), (dict(k_new=None), ValueError),
+                       (dict(workspace=pkv.Workspace(256, cuda_device)), pkv.PkvError), (dict(eps=-1.0), pkv.PkvError)):
+        with pytest.raises(error):
+            call(**bad)
+    call()
+    torch.cuda.synchronize()
+    assert c.ws.status() == 0
 
 
 @pytest.mark.gpu
