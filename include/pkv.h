@@ -361,7 +361,7 @@ int pkv_append_rope(const void* q, int64_t q_stride, const void* k_new, int64_t 
  *    (infinities saturate too; NaN stays NaN). 2^e v is exact in bf16.
  *  - Layout, block tables, slots and geometry as for the bf16 pools: page_size
  *    16, head_dim 64 or 128, 1 to 8 query heads per KV head.
- *  - max_pages_per_seq < 2^27 in these calls.
+ *  - max_pages_per_seq <= 2^27 - 2 in the calls that take it.
  */
 
 /*

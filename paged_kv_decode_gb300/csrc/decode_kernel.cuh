@@ -61,12 +61,14 @@
 //    17.8 us (82.6 MB; 12.3), 27 of 9 to 8000 at 32 query / 8 KV heads 37.3 us
 //    (212 MB; 31.7). Of the first, 1.8 us pass before the first copies go out
 //    (the wait, the length scan, the block table), 8.2 stream at 6.1 TB/s and
-//    1.5 end and merge the split pieces. In the fused step a row warp
-//    turns (norm, rotation) each piece's query rows and turns and quantises its
-//    new row while the piece before streams; the consumer that takes the request's
-//    last unit writes the row over the staged slot and into the pool; the producer never waits
-//    for the predecessor in early mode. Attention alone, in early mode, waits
-//    with the requests' last units, which hold rows that the predecessor wrote.
+//    1.5 end and merge the split pieces. In the fused step a row warp turns (norm,
+//    rotation) each piece's query rows and turns and quantises its new row while
+//    the piece before streams; the consumer that takes the request's last unit
+//    writes the row over the staged slot and into the pool; the producer never
+//    waits for the predecessor in early mode (12.8 us per layer for the 16
+//    requests, norms and rotation included; bf16 pages, rotation alone: 18.0).
+//    Attention alone, in early mode, waits with the requests' last units, which
+//    hold rows that the predecessor wrote.
 //  * The query rows of the next piece are copied into shared memory (cp.async)
 //    while the current piece streams, so a piece boundary costs no round trip.
 //  * At the end of a piece the warps merge through shared memory (at most four
@@ -176,8 +178,9 @@ struct DecodeArgs {
 // (1, 2, 4 or 8), whether the head counts are the Qwen3 decoder's 16 / 8 fixed
 // at compile time (otherwise DecodeArgs::hkv / gq), and the launch shape: two
 // CTAs per SM with kRing stages per consumer, or (kWide, for a few long requests)
-// one CTA per SM with twice the stages, so each (request, KV head) has half as
-// many holders to merge and each CTA twice the bytes in flight. kFp8: the 8-bit
+// one CTA per SM with twice the stages (8-bit cache: twice the consumers, and two
+// producers), so each (request, KV head) has half as many holders to merge and
+// each CTA twice the bytes in flight. kFp8: the 8-bit
 // cache (pkv_fp8.cuh); its pages are half as large, so the kernel works in units
 // of two pages (a stage holds both, "page" below then means such a unit): a warp's
 // step of 32 tokens pays the softmax's chain of shuffles and the barriers once.
@@ -214,7 +217,7 @@ struct DecGeo {
   static constexpr int kPieceB = kPiece * 4;
   static constexpr int kSplitWords = G * D + 4 * G;     // polled record: o[G][D], then m_hi, m_lo, l_hi,
   static constexpr int kSplitB = kSplitWords * 4;       // l_lo of each head
-  static constexpr int kMHMax = kConsumers > 4 ? 2 : 4;
+  static constexpr int kMHMax = kConsumers > 4 ? 2 : 4;  // (shared memory for eight warps' states at 1024 requests)
   static constexpr int kMH = G < kMHMax ? G : kMHMax;   // heads per pass through the merge buffer
   static constexpr int kQBuf = G * D * 2;               // query rows of one (request, KV head)
   static constexpr int kCsB = D * 4;                    // one cos/sin table row
@@ -223,16 +226,16 @@ struct DecGeo {
   static constexpr int kMergeFloats = kConsumers * kMH * kRec;
   static constexpr int kSmemMerge = kMergeFloats * 4;
   static constexpr int kSmemQ = 2 * kQBuf;              // this piece's rows and the next piece's
-  static constexpr int kSmemCs = 2 * kCsB;              // rows for this piece's and the next piece's position
+  static constexpr int kSmemCs = kFp8 ? 0 : 2 * kCsB;   // rows for this piece's and the next piece's position
   static constexpr int kSmemScales = kFp8 ? kStages * kUnitPages * kScaleBytes : 0;  // the stages' row scales
-  static constexpr int kNewB = 4 * D + 16;              // a new token's K and V rows of one head (bf16, then codes)
+  static constexpr int kNewB = 2 * D + 16;              // codes of a new token's K and V row of one head, their scales
   static constexpr int kSmemNew = kFp8 ? 2 * kNewB : 0;  // of this piece's request and the next piece's
   static constexpr int kSmemFixed =
       kSmemAlign + kSmemRing + kSmemBars + kSmemMerge + kSmemQ + kSmemCs + kSmemScales + kSmemNew + kSmemMisc;
-  // The 8-bit cache's shape, in units of two pages (16/8/128, us of a step's decode attention): a boundary costs 4 /
+  // The 8-bit cache's shape, in units of two pages (16/8/128, us a call): a boundary costs 4 /
   // 8 / 12 / 16 / 32 units: bs16 14.1 / 13.4 / 14.0 / 14.2 / 16.8; 2 / 3 / 4 / 8 units a round: bs16 14.4 / 13.6 /
-  // 13.4 / 14.1, 40k (narrow) 19.9 / 19.1 / 19.2 / 19.7; 2 or 3 stages a consumer: bs16 14.3 / 13.4. Shares of one unit: two
-  // requests of 37 and 200 tokens take 6.2 us, 6.7 and 8.4 with at least 2 and 8.
+  // 13.4 / 14.1, 40k (narrow) 19.9 / 19.1 / 19.2 / 19.7; 2 or 3 stages a consumer: bs16 14.3 / 13.4. Shares of
+  // one unit: two requests of 37 and 200 tokens take 6.2 us, 6.7 and 8.4 with at least 2 and 8.
   static constexpr int kPieceCost = kFp8 ? 8 : PKV_DEC_PIECE_COST;
   static constexpr int kRound = kFp8 ? 4 : kRoundPages;
   static constexpr int kShareMin = kFp8 ? 1 : kMinShare;
@@ -823,7 +826,7 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm) d
   // ============================================================== row warp (fused step of the 8-bit cache)
   // For each piece, while the one before it streams: its query rows normalised and rotated as the append would, into
   // qbuf in bf16, and (where the piece holds the request's last unit) the new token's K and V rows turned and
-  // quantised into newbuf, K codes at byte 0, V codes at 2 D, their scale bytes at 4 D. D / 16 lanes take a row: the
+  // quantised into newbuf, K codes at byte 0, V codes at D, their scale bytes at 2 D. D / 16 lanes take a row: the
   // group's query rows first, then K, then V. The weights and, for the first piece, the table row are loaded before
   // the wait for the predecessor in early mode, so that one round trip for the rows is left behind it.
   if constexpr (kRowWarp) {
@@ -888,10 +891,10 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm) d
             }
           } else if (mine) {
             unsigned char* to = newbuf + buf * Geo::kNewB;
-            unsigned char* row = to + (is_v ? 2 * D : 0) + l * 8;
+            unsigned char* row = to + (is_v ? D : 0) + l * 8;
             *reinterpret_cast<uint2*>(row) = lo8;
             *reinterpret_cast<uint2*>(row + D / 2) = hi8;
-            if (l == 0) to[4 * D + (is_v ? 1 : 0)] = static_cast<unsigned char>(scale);
+            if (l == 0) to[2 * D + (is_v ? 1 : 0)] = static_cast<unsigned char>(scale);
           }
         }
         row_sync<Geo>();
@@ -1081,8 +1084,8 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm) d
             const int l = lane % L;
             const bool v = lane >= L;
             const uint32_t nb = smem_u32(newbuf) + (j & 1) * Geo::kNewB;
-            const uint4 codes = lds128(nb + (v ? 2 * D : 0) + l * 16);
-            const int scale = static_cast<int>(lds8(nb + 4 * D + (v ? 1 : 0))), sc = (v ? kPageSize : 0) + t;
+            const uint4 codes = lds128(nb + (v ? D : 0) + l * 16);
+            const int scale = static_cast<int>(lds8(nb + 2 * D + (v ? 1 : 0))), sc = (v ? kPageSize : 0) + t;
             sts128(kt + (v ? Geo::kTile : 0) + page * Geo::kPageTile + swz8<D>(t, l), codes);
             if (l == 0) sts8(smem_u32(scbuf + (slot * Geo::kUnitPages + page) * kScaleBytes) + sc, scale);
             if (nid >= 0 && nid < a.num_pages) {  // (the producer reports a page id out of the pool)

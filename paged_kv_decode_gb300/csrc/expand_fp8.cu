@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_fp8_kernel(const Expand
       if (lane == 0) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
       len = len < 0 ? 0 : a.max_pages * kPageSize;
     }
-    const int rows = min(len - p * kPageSize, kPageSize);  // of this page (max_pages is below 2^27: host check)
+    const int rows = min(len - p * kPageSize, kPageSize);  // of this page (max_pages is below 2^27 - 1: host check)
     if (rows <= 0) continue;
     const int src = __ldg(a.block_table + sp), dst = __ldg(a.out_block_table + sp);
     if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.out_pages) {

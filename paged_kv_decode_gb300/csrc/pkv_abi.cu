@@ -309,8 +309,8 @@ int pkv_mixed_step_attn(const void* q, const void* k_pages, const void* v_pages,
                              dec_batch > 0 ? &dec : nullptr);
 }
 
-// Longest block table of the 8-bit calls: its positions fit 32 bits.
-constexpr int32_t kMaxTablePages = (1 << 27) - 1;
+// Longest block table of the 8-bit calls: its positions, rounded up to whole units of 32, fit 32 bits.
+constexpr int32_t kMaxTablePages = (1 << 27) - 2;
 
 // Shared by the bf16 and the 8-bit append with rotation (kv_scales is nullptr for the bf16 one).
 static int append_rope(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,

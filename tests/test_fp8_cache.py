@@ -58,7 +58,7 @@ def test_decode_host_argument_checks(lib):
     assert call(desc=None) == -1
     for bad in (_desc(head_dim=96), _desc(page_size=32), _desc(num_q_heads=36, num_kv_heads=4)):
         assert call(desc=bad) == -3
-    assert call(batch=-1) == -2 and call(width=0) == -2 and call(width=1 << 27, batch=1) == -2
+    assert call(batch=-1) == -2 and call(width=0) == -2 and call(width=(1 << 27) - 1, batch=1) == -2
     assert call(batch=1025) == -3
     assert call(batch=1024, width=1 << 18) == -2
     assert call(ws=None) == -1
@@ -81,7 +81,7 @@ def test_decode_append_host_argument_checks(lib):
     assert call(desc=None) == -1
     for bad in (_desc(head_dim=96), _desc(page_size=32), _desc(num_q_heads=36, num_kv_heads=4)):
         assert call(desc=bad) == -3
-    assert call(batch=-1) == -2 and call(width=0) == -2 and call(width=1 << 27, batch=1) == -2
+    assert call(batch=-1) == -2 and call(width=0) == -2 and call(width=(1 << 27) - 1, batch=1) == -2
     assert call(batch=1025) == -3 and call(batch=1024, width=1 << 18) == -2
     assert call(max_pos=0) == -2 and call(eps=-1.0) == -2 and call(eps=float("nan")) == -2
     assert call(ws=None) == -1
@@ -101,7 +101,7 @@ def test_expand_host_argument_checks(lib):
                                   None if desc is None else ctypes.byref(desc), None, ws, nb)
 
     assert call(desc=None) == -1 and call(desc=_desc(head_dim=32)) == -3
-    assert call(seqs=-1) == -2 and call(width=0) == -2 and call(out_pages=0) == -2 and call(width=1 << 27, seqs=1) == -2
+    assert call(seqs=-1) == -2 and call(width=0) == -2 and call(out_pages=0) == -2 and call(width=(1 << 27) - 1, seqs=1) == -2
     for name in ("kp", "vp", "sc", "bt", "sl", "ko", "vo", "ot"):
         assert call(**{name: None}) == -1, name
     for name in ("kp", "vp", "sc", "ko", "vo"):
