@@ -373,20 +373,25 @@ struct Shares {
 };
 
 // CTAs that take a share of T pages in `pairs` non-empty (request, KV head) pairs: all that get kShareMin pages.
-// With the 8-bit cache's counted merge (few pairs, small shares) a pair has at most 2 sqrt(u) holders, u its units
-// on average: one CTA reads all their records, and a share's streaming shrinks with 1 / holders; and the number is a
-// multiple of the pairs, so that one request's shares end with its pairs (a CTA with two split pieces ends twice).
+// With the 8-bit cache a pair has at most 2 sqrt(u) holders, u its units on average: one CTA reads all their
+// records, and a share's streaming shrinks with 1 / holders. For one request (the counted merge) the number is a
+// multiple of the pairs, so that shares end with the pairs: a CTA with two split pieces ends twice.
 // One request at 8/1/64, 4096 / 16384 / 40000 tokens: 15.9 / 29.2 / 29.6 us over all CTAs, 9.1 / 11.6 / 15.8 so
 // (1.5 sqrt(u): 9.1 / 12.2 / 16.4, 3 sqrt(u): 9.1 / 12.9 / 16.9); at 16/8/128, 1000 and 4096: 7.7 / 8.4, 7.2 / 8.5.
 template <class Geo, bool kPolled>
 __device__ __forceinline__ int share_count(long long T, int pairs) {
-  if (Geo::kFp8 && !kPolled && pairs > 0) {
-    const unsigned p = static_cast<unsigned>(pairs), u = static_cast<unsigned>(T) / p;  // u >= 1 units a pair
-    const unsigned h = min(min(static_cast<unsigned>(2.f * sqrtf(static_cast<float>(u))), u), gridDim.x / p);
-    return pairs * static_cast<int>(max(h, 1u));
-  }
   const long long n = T / Geo::kShareMin > 0 ? T / Geo::kShareMin : 1;
-  return static_cast<int>(n < gridDim.x ? n : gridDim.x);
+  const int all = static_cast<int>(n < gridDim.x ? n : gridDim.x);
+  // (64 pairs of more than 5 units reach 304 CTAs with 2 sqrt(u) holders each, and fewer units have few holders
+  // anyway: batches are spared the division and the root, 0.2 us before their first copies)
+  if (Geo::kFp8 && pairs > 0 && (!kPolled || pairs < 64)) {
+    const unsigned p = static_cast<unsigned>(pairs), u = static_cast<unsigned>(T) / p;  // u >= 1 units a pair
+    unsigned h = static_cast<unsigned>(2.f * sqrtf(static_cast<float>(u)));
+    if (!kPolled) h = min(min(h, u), gridDim.x / p);
+    const unsigned most = p * max(h, 1u);  // (below 2^32: p h <= 2 sqrt(p T))
+    return most < static_cast<unsigned>(all) || !kPolled ? static_cast<int>(most) : all;
+  }
+  return all;
 }
 
 // Polled records are 32-bit words: an fp32 value rounded to nearest (even) at
@@ -1498,7 +1503,10 @@ int launch_decode_geo(const DecodeLaunch& c) {
   // 10.6; as its own rule for larger batches it lost, bs16 13.4 narrow and 14.2 wide.)
   const bool wide = (Geo::D == 128 || Geo::kFp8) && grid > kPollMax * pairs && pairs * c.max_pages >= kWideMinPages;
   const int grid_used = wide ? (c.num_sms < kMaxGrid ? c.num_sms : kMaxGrid) : grid;
-  const bool polled = grid_used <= kPollMax * pairs;
+  // (the 8-bit cache counts for one request alone: with shares of unequal pairs a CTA ends up to three split pieces,
+  // and its bound on holders keeps polled merges short -- 10 requests of 120 to 1084 tokens at 8/1/64 12.1 us counted,
+  // 7.9 polled)
+  const bool polled = grid_used <= kPollMax * pairs || (Geo::kFp8 && c.batch > 1);
   const size_t smem = wide ? GeoW::smem_bytes(c.batch) : Geo::smem_bytes(c.batch);
   const bool fused = c.k_new != nullptr;
   const int threads = wide ? (fused ? DecThreads<GeoW, true>::n : GeoW::kThreads)

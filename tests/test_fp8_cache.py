@@ -111,15 +111,20 @@ def test_expand_host_argument_checks(lib):
 
 
 class Units(ShareMap):
-    """The share map of the 8-bit decode kernel: units of 32 tokens; shares of at least one unit, or (the counted merge,
-    lam 0) at most 2 sqrt(units of a pair) holders per pair and as many CTAs as a multiple of the pairs."""
+    """The share map of the 8-bit decode kernel: units of 32 tokens; shares of at least one unit and at most 2 sqrt(units
+    of a pair) holders per pair; with the counted merge (one request, lam 0) a multiple of the pairs."""
 
     def __init__(self, seq_lens, grid, lam, hkv=8):
         super().__init__([(int(s) + 31) // 32 * 16 for s in seq_lens], grid, lam, hkv)  # as many pages as units
         self.n = min(grid, max(1, self.T))
-        if lam == 0 and self.pcp[-1]:
-            u = self.T // self.pcp[-1]
-            self.n = self.pcp[-1] * max(1, min(int(2 * np.sqrt(np.float32(u))), u, grid // self.pcp[-1]))
+        pairs = sum(1 for p in self.pages if p) * hkv
+        if pairs:
+            u = self.T // pairs
+            h = int(2 * np.sqrt(np.float32(u)))
+            if lam == 0:
+                self.n = pairs * max(1, min(h, u, grid // pairs))
+            elif pairs < 64:
+                self.n = min(self.n, pairs * max(1, h))
 
 
 UNIT_MIXES = [[37, 200], [1], [33], [32] * 7, [9000], [0, 700, 0, 33, 1, 2900, 0], list(range(1, 65)),
@@ -174,9 +179,8 @@ def test_decode_shares_tile_the_units_and_cannot_deadlock(lam, grid):
     (rounds of 4 units) of every share finishes, with one producer and with two."""
     for lens in UNIT_MIXES:
         for hkv in (1, 8):
-            pairs = sum(1 for s in lens if s) * hkv
-            if lam == 0 and pairs > grid:
-                continue  # the counted merge is for few pairs
+            if lam == 0 and (len(lens) > 1 or hkv > grid):
+                continue  # the counted merge is for one request and few pairs
             sm = Units(lens, grid, lam, hkv)
             lo = [sm.lo(c) for c in range(sm.n + 1)]
             assert sm.n <= grid and lo[0] == 0 and lo[-1] == sm.T and all(a <= b for a, b in zip(lo, lo[1:]))
@@ -287,6 +291,7 @@ def test_decode(cuda_device, geom, lens):
                                              ("8q1kv64", [9001], None), ("32q32kv64", W.config_seq_lens(5)[:12], 600),
                                              ("16q8kv64", [20000], None), ("8q1kv64", [9001], 9000),
                                              ("28q4kv128", [7000], 2100), ("28q4kv128", [5000, 40], None),
+                                             ("8q1kv64", [9000, 15000], None), ("8q1kv64", [9000, 15000, 1], 3000),
                                              ("12q4kv128", [3, 0, 2500], 4000), ("64q8kv128", [17000], None),
                                              ("8q1kv64", [1], 9000)])
 def test_decode_long_and_split(cuda_device, geom, lens, width):
