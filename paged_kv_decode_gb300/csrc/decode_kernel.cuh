@@ -124,9 +124,7 @@ namespace pkv {
 #ifndef PKV_DEC_PIECE_COST  // pages a (request, KV head) boundary inside a share counts for (polled merge)
 #define PKV_DEC_PIECE_COST 32
 #endif
-constexpr int kCons = PKV_DEC_CONSUMERS;  // consumer warps; one more warp produces
-constexpr int kConsThreads = kCons * 32;
-constexpr int kDecThreads = kConsThreads + 32;
+constexpr int kCons = PKV_DEC_CONSUMERS;  // consumer warps per producer warp
 constexpr int kDecCtasPerSm = PKV_DEC_CTAS_PER_SM;
 constexpr int kRoundPages = PKV_DEC_ROUND_PAGES;
 constexpr int kMaxDecodeBatch = 1024;
@@ -499,9 +497,9 @@ __device__ __forceinline__ void row_sync() {
 // kPolled: the polled merge, else the counted one. Each combination is its own
 // instantiation, so a path carries no code (and no registers) for the others.
 template <class Geo, bool kFused, bool kRope, bool kPolled>
-__global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm) decode_kernel(const __grid_constant__ CUtensorMap kmap,
-                                                                             const __grid_constant__ CUtensorMap vmap,
-                                                                             const DecodeArgs a) {
+__global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
+    decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const DecodeArgs a) {
   constexpr int D = Geo::D, G = Geo::G, kKS = Geo::kKS, kRing = Geo::kRing, kStages = Geo::kStages;
   constexpr int kRec = Geo::kRec, kMH = Geo::kMH, kLW = Geo::kLW;
   constexpr bool kRowWarp = Geo::kFp8 && kFused;
@@ -693,7 +691,7 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm) d
           two = true;
         }
         last = p == np - 1;
-        if (kRope && !Geo::kFp8 && p == np - 1) wslot = (sl[b] - 1) % kPageSize;  // the new token's slot (rotated append)
+        if (kRope && !Geo::kFp8 && p == np - 1) wslot = (sl[b] - 1) % kPageSize;  // the new token's slot (rotated)
       }
       const unsigned same = __match_any_sync(kFull, valid ? c : -1);
       const int idx = __popc(same & lt_mask);  // earlier lanes of this chunk feeding the same consumer
@@ -1047,13 +1045,14 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm) d
     int vmax = 0;  // (8-bit cache) the largest value scale so far: o is 2^(kWeightShift + 127 - vmax) too large
 
     const int w0 = static_cast<int>((pc.fstart - lo) % Geo::kConsumers);  // consumer of the piece's first page
-    const int p_first = pc.p0 + (warp - w0 + Geo::kConsumers) % Geo::kConsumers;    // this warp's first page of the piece
+    const int p_first = pc.p0 + (warp - w0 + Geo::kConsumers) % Geo::kConsumers;  // this warp's first page
     // Fused append without the rotary embedding: the warp that takes the request's last page loads
     // the new token's K and V rows for this head now (lane l: 16-byte chunk l of the K row, or of
     // the V row from lane D / 8 on) with that page's block-table entry. Once the page is staged it
     // writes them over the copied slot and into the pool.
     const bool takes_new =
-        kFused && (!kRope || Geo::kFp8) && pc.p1 == pc.np && p_first <= pc.np - 1 && (pc.np - 1 - p_first) % Geo::kConsumers == 0;
+        kFused && (!kRope || Geo::kFp8) && pc.p1 == pc.np && p_first <= pc.np - 1 &&
+        (pc.np - 1 - p_first) % Geo::kConsumers == 0;
     // (8-bit cache: the rows are in newbuf, turned and quantised by the row warp.)
     constexpr int kRowChunks = D / 8;
     uint4 nrow = make_uint4(0u, 0u, 0u, 0u);
@@ -1399,7 +1398,8 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm) d
         }
         cp_async_wait_all();
         consumer_sync<Geo>();
-        const int pfirst = ((warp - t0) % Geo::kConsumers + Geo::kConsumers) % Geo::kConsumers;  // this warp's first record position
+        // this warp's first record position
+        const int pfirst = ((warp - t0) % Geo::kConsumers + Geo::kConsumers) % Geo::kConsumers;
 #pragma unroll
         for (int j = 0; j < kLW; ++j) {
           if (!group_ok(j)) continue;
