@@ -77,8 +77,10 @@
  *    (pkv_decode_attn, pkv_decode_append_attn, and the 8-bit cache's) or prefill calls
  *    (pkv_prefill_chunk_attn), not both: each kind relies on its own split
  *    scratch (counters, and for decode tagged records) having been left
- *    cleared by the previous call of that kind. The appends and pkv_expand_fp8
- *    use only the status word and may share either.
+ *    cleared by the previous call of that kind. Decode calls of any geometry,
+ *    batch and cache type may share a workspace that is large enough for each
+ *    of them. The appends and pkv_expand_fp8 use only the status word and may
+ *    share either kind's.
  */
 #ifndef PKV_H_
 #define PKV_H_

@@ -91,10 +91,8 @@ bool decode_supported(int num_q_heads, int num_kv_heads, int head_dim, int page_
 size_t decode_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int32_t batch, int num_sms) {
   const size_t G = static_cast<size_t>(group_pad(num_q_heads / num_kv_heads));
   const size_t grid = static_cast<size_t>(decode_grid(num_sms));
-  size_t off = PKV_STATUS_BYTES + decode_counter_bytes(batch, num_kv_heads);
-  off += 2 * grid * G * (head_dim + 4) * 4;      // counted records
-  off += 2 * grid * (G * head_dim + 4 * G) * 4;  // polled records
-  return off;
+  const size_t records = (2 * grid * G * (head_dim + 4) * 4 + kGrain - 1) / kGrain * kGrain;
+  return PKV_STATUS_BYTES + decode_counter_bytes(batch, num_kv_heads) + 2 * records;  // counted and polled
 }
 
 int launch_decode_fp8(const DecodeFp8& f, int num_q_heads, int num_kv_heads, int head_dim, int32_t batch,

@@ -135,6 +135,8 @@ constexpr int kSmemMisc = 32;                // flag words, then the CTA's share
 constexpr int kSmemAlign = 1024;             // the ring starts on a 1024-byte boundary (swizzle atoms)
 constexpr uint32_t kTag = 0xa5u;             // low byte of a word written by this call
 constexpr int kPollMax = 24;                 // polled merge up to this many holders per pair
+constexpr int kCountMax = 64;                // counted merge up to this many pairs (its block of counters)
+constexpr unsigned kGrain = 512;             // bytes of one kind of split records at a time in the workspace
 // A step with few (request, KV head) pairs for the two-CTA grid (the counted
 // merge) runs the wide launch shape when the block table can hold at least this
 // many (request, KV head, page) triples (batch x max_pages x KV heads); with half
@@ -167,9 +169,9 @@ struct DecodeArgs {
   int gq;   // query heads per KV head (run-time geometries; at most the kernel's group)
   const uint8_t* scales;  // 8-bit cache: [num_pages][hkv][2][16] e8m0 scales, else nullptr
   int* status;
-  int* counters;       // [batch * hkv], zero between calls (counted merge)
-  float* partials;     // [2 * gridDim.x][G * (D + 4)] (counted merge)
-  uint32_t* tagged;    // [2 * gridDim.x][G * D + 4 * G], no word tagged between calls (polled merge)
+  int* counters;       // [kCountMax], zero between calls (counted merge)
+  float* partials;     // [2 * gridDim.x][G * (D + 4)] at spread() (counted merge)
+  uint32_t* tagged;    // [2 * gridDim.x][G * D + 4 * G] at spread(), zero between calls (polled merge)
 };
 
 // Geometry of one instantiation: head_dim D, G query heads per KV head computed
@@ -246,6 +248,7 @@ struct DecGeo {
   static constexpr int kItems = (kMH * D + kConsumerThreads - 1) / kConsumerThreads;  // (head, dim) per thread per pass
   static_assert(kRound >= 1 && kRound <= kFed * kRing, "a page's previous stage use is in an earlier round");
   static_assert(kSplitB % 16 == 0 && kPieceB % 16 == 0, "16-byte loads, copies and clears of a record");
+  static_assert(kSplitB == kPieceB, "the two areas of records are of one size");
   static_assert((kSmemRing + kSmemBars) % 16 == 0 && kSmemMerge % 16 == 0 && kQBuf % 16 == 0, "alignment");
   static_assert(kMergeCap >= 1, "a record fits the ring");
   __device__ __forceinline__ static int hkv(const DecodeArgs& a) { return kFixed ? kKVHeads : a.hkv; }
@@ -391,6 +394,14 @@ __device__ __forceinline__ int share_count(long long T, int pairs) {
   }
   return all;
 }
+
+// Split records of both merges alternate in the workspace, kGrain bytes of the one area, kGrain of the other:
+// word i of an area lies at word spread(i) behind its start, and the polled area starts kGrain bytes behind
+// the counted one. Records differ in size between geometries, so in areas one behind the other the counted
+// records, which stay behind uncleared, would lie where another geometry's tagged words are looked for.
+// (One 9000-token request at 64/8/128 18.3 -> 18.6 us, 16 requests at 16/8/128 14.41 -> 14.44; grains of 64
+// bytes 18.9 and 14.65. Clearing the counted records cost the CTA that merges a pair 1 to 10 us a call.)
+__device__ __forceinline__ uint32_t spread(uint32_t i) { return i + (i & ~(kGrain / 4 - 1u)); }
 
 // Polled records are 32-bit words: an fp32 value rounded to nearest (even) at
 // 15 mantissa bits, with the tag in the freed low byte. Each word is one
@@ -1175,11 +1186,11 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
           if (x < kMH * D && h0 + x / D < gq) orow[(h0 + x / D) * D + x % D] = __float2bfloat16_rn(O[e] / L[e]);
         }
       } else if constexpr (kPolled) {
-        uint32_t* rec = a.tagged + static_cast<size_t>(my_slot) * Geo::kSplitWords;
+        const uint32_t rec = static_cast<uint32_t>(my_slot) * Geo::kSplitWords;
 #pragma unroll
         for (int e = 0; e < Geo::kItems; ++e) {
           const int x = tid + e * Geo::kConsumerThreads;
-          if (x < kMH * D) st_word(rec + h0 * D + x, tag_word(O[e]));
+          if (x < kMH * D) st_word(a.tagged + spread(rec + h0 * D + x), tag_word(O[e]));
         }
         if (tid < 4 * kMH) {  // m_hi, m_lo, l_hi, l_lo of head h0 + tid / 4
           const int hi4 = tid >> 2;
@@ -1194,19 +1205,17 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
           }
           uint32_t whi, wlo;
           tag_split((tid & 2) ? l : m, whi, wlo);
-          st_word(rec + G * D + 4 * h0 + tid, (tid & 1) ? wlo : whi);
+          st_word(a.tagged + spread(rec + G * D + 4 * h0 + tid), (tid & 1) ? wlo : whi);
         }
       } else {
-        float* rec = a.partials + static_cast<size_t>(my_slot) * Geo::kPiece;
+        const uint32_t rec = static_cast<uint32_t>(my_slot) * Geo::kPiece;
 #pragma unroll
         for (int e = 0; e < Geo::kItems; ++e) {
           const int x = tid + e * Geo::kConsumerThreads;
           if (x < kMH * D) {
-            rec[(h0 + x / D) * kRec + 4 + x % D] = O[e];
-            if (x % D == 0) {
-              rec[(h0 + x / D) * kRec] = M[e];
-              rec[(h0 + x / D) * kRec + 1] = L[e];
-            }
+            const uint32_t head = rec + (h0 + x / D) * kRec;
+            a.partials[spread(head + 4 + x % D)] = O[e];
+            if (x % D == 0) *reinterpret_cast<float2*>(a.partials + spread(head)) = make_float2(M[e], L[e]);
           }
         }
       }
@@ -1265,8 +1274,7 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
     const int cf = m_cf, n = m_n;
     const bool two = m_two;
     auto rec_of = [&](int t) {
-      const size_t slot = 2 * static_cast<size_t>(cf + t) + ((t == 0 && two) ? 1 : 0);
-      return a.tagged + slot * Geo::kSplitWords;
+      return static_cast<uint32_t>(2 * (cf + t) + ((t == 0 && two) ? 1 : 0)) * Geo::kSplitWords;
     };
     float fm[kLW], fl[kLW];
     float4 fo[kLW];
@@ -1283,10 +1291,11 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
       uint4 R[kMB][kLW];  // o groups of this lane
       uint32_t W[kMB];    // lanes 0 .. 4G - 1: word lane of the m/l block
       auto load = [&](int rr) {
-        const uint32_t* rec = rec_of(t0 + rr * Geo::kConsumers);
+        const uint32_t rec = rec_of(t0 + rr * Geo::kConsumers);
 #pragma unroll
-        for (int j = 0; j < kLW; ++j) R[rr][j] = group_ok(j) ? ld_words4(rec + 4 * (lane + 32 * j)) : tag4;
-        W[rr] = lane < 4 * G ? ld_word(rec + G * D + lane) : kTag;
+        for (int j = 0; j < kLW; ++j)
+          R[rr][j] = group_ok(j) ? ld_words4(a.tagged + spread(rec + 4 * (lane + 32 * j))) : tag4;
+        W[rr] = lane < 4 * G ? ld_word(a.tagged + spread(rec + G * D + lane)) : kTag;
       };
 #pragma unroll
       for (int rr = 0; rr < kMB; ++rr)
@@ -1342,7 +1351,7 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
     // clear the tags of the merged records for the next call (every read above has completed)
     for (int i = tid; i < n * (Geo::kSplitB / 16); i += Geo::kConsumerThreads) {
       const int t = i / (Geo::kSplitB / 16), c = i % (Geo::kSplitB / 16);
-      reinterpret_cast<uint4*>(rec_of(t))[c] = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(a.tagged + spread(rec_of(t) + 4 * c)) = make_uint4(0u, 0u, 0u, 0u);
     }
   } else {
     if (npend == 0) return;
@@ -1391,10 +1400,9 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
       for (int t0 = 0; t0 < nm; t0 += Geo::kMergeCap) {
         const int t1 = t0 + Geo::kMergeCap < nm ? t0 + Geo::kMergeCap : nm;
         for (int t = t0 + warp; t < t1; t += Geo::kConsumers) {
-          const size_t slot = 2 * static_cast<size_t>(cf + t) + ((t == 0 && two) ? 1 : 0);
-          const unsigned char* src = reinterpret_cast<const unsigned char*>(a.partials + slot * Geo::kPiece);
+          const uint32_t rec = static_cast<uint32_t>(2 * (cf + t) + ((t == 0 && two) ? 1 : 0)) * Geo::kPiece;
           const uint32_t dst = ring_s + (t - t0) * Geo::kPieceB;
-          for (int c = lane; c < kChunks; c += 32) cp_async16(dst + c * 16, src + c * 16);
+          for (int c = lane; c < kChunks; c += 32) cp_async16(dst + c * 16, a.partials + spread(rec + 4 * c));
         }
         cp_async_wait_all();
         consumer_sync<Geo>();
@@ -1474,12 +1482,15 @@ constexpr DecodeKern decode_instance() {
     return decode_kernel<Geo, kFused, kRope, kPolled>;
 }
 
-// Workspace layout of a decode call: status | counters [batch * hkv] (256-byte
-// padded) | counted records [2 * grid][G * (D + 4)] fp32 | polled records
-// [2 * grid][G * D + 4 G] words.
+// Workspace layout of a decode call: status | counters [kCountMax] | kGrain bytes of
+// the counted records [2 * grid][G * (D + 4)] fp32, kGrain of the polled records
+// [2 * grid][G * D + 4 G] words, and so on (spread()). Calls of any geometry and batch
+// may share a workspace: counters and polled words, which must be zero at a call's
+// start and are left zero, never lie where a call leaves counted records.
 inline int decode_grid(int num_sms) {
   return kDecCtasPerSm * num_sms < kMaxGrid ? kDecCtasPerSm * num_sms : kMaxGrid;
 }
+// (one counter per pair, although polled calls, the ones with many pairs, use none)
 inline size_t decode_counter_bytes(int32_t batch, int hkv) {
   return (static_cast<size_t>(batch) * hkv * 4 + 255) / 256 * 256;
 }
@@ -1506,7 +1517,7 @@ int launch_decode_geo(const DecodeLaunch& c) {
   // (the 8-bit cache counts for one request alone: with shares of unequal pairs a CTA ends up to three split pieces,
   // and its bound on holders keeps polled merges short -- 10 requests of 120 to 1084 tokens at 8/1/64 12.1 us counted,
   // 7.9 polled)
-  const bool polled = grid_used <= kPollMax * pairs || (Geo::kFp8 && c.batch > 1);
+  const bool polled = grid_used <= kPollMax * pairs || pairs > kCountMax || (Geo::kFp8 && c.batch > 1);
   const size_t smem = wide ? GeoW::smem_bytes(c.batch) : Geo::smem_bytes(c.batch);
   const bool fused = c.k_new != nullptr;
   const int threads = wide ? (fused ? DecThreads<GeoW, true>::n : GeoW::kThreads)
@@ -1569,9 +1580,9 @@ int launch_decode_geo(const DecodeLaunch& c) {
   a.scales = static_cast<const uint8_t*>(c.scales);
   a.status = reinterpret_cast<int*>(ws);
   a.counters = reinterpret_cast<int*>(ws + PKV_STATUS_BYTES);
-  a.partials = reinterpret_cast<float*>(ws + PKV_STATUS_BYTES + decode_counter_bytes(c.batch, c.hkv));
-  a.tagged = reinterpret_cast<uint32_t*>(reinterpret_cast<unsigned char*>(a.partials) +
-                                         static_cast<size_t>(2) * grid * Geo::kPieceB);
+  // (decode_counter_bytes() is at least kCountMax counters)
+  a.partials = reinterpret_cast<float*>(ws + PKV_STATUS_BYTES + kCountMax * 4);
+  a.tagged = reinterpret_cast<uint32_t*>(ws + PKV_STATUS_BYTES + kCountMax * 4 + kGrain);
   CUtensorMap kmap, vmap;
   const int rc = Geo::kFp8 ? encode_page_maps_fp8(c.k_pages, c.v_pages, Geo::D, c.num_pages, c.hkv, &kmap, &vmap)
                            : encode_page_maps(c.k_pages, c.v_pages, Geo::D, c.num_pages, c.hkv, &kmap, &vmap);
