@@ -1053,7 +1053,7 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
 #pragma unroll
     for (int ks = 0; ks < kKS; ++ks) o[ks][0] = o[ks][1] = o[ks][2] = o[ks][3] = 0.f;
     float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
-    int vmax = 0;  // (8-bit cache) the largest value scale so far: o is 2^(kWeightShift + 127 - vmax) too large
+    float vw0 = -CUDART_INF_F, vw1 = -CUDART_INF_F;  // (8-bit cache) the largest contributions (mma_unit_fp8)
 
     const int w0 = static_cast<int>((pc.fstart - lo) % Geo::kConsumers);  // consumer of the piece's first page
     const int p_first = pc.p0 + (warp - w0 + Geo::kConsumers) % Geo::kConsumers;  // this warp's first page
@@ -1131,7 +1131,7 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
         if constexpr (Geo::kFp8)
           mma_unit_fp8<kKS, Geo::kUnitPages>(kt, kt + Geo::kTile,
                                              smem_u32(scbuf + slot * (Geo::kUnitPages * kScaleBytes)), koff, qf,
-                                             n_valid, qs0, qs1, o, m0, m1, l0, l1, vmax);
+                                             n_valid, qs0, qs1, o, m0, m1, l0, l1, vw0, vw1);
         else
           mma_page<kKS>(kt, kt + Geo::kTile, koff, voff, qf, n_valid, a.qscale, o, m0, m1, l0, l1);
       }
@@ -1141,11 +1141,14 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
     }
 
     if constexpr (Geo::kFp8) {
-      const float up = field_pow2(vmax - kWeightShift);  // (a warp without pages: o is zero)
+      const float up0 = value_power(vw0, m0), up1 = value_power(vw1, m1);
 #pragma unroll
-      for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[ks][e] *= up;
+      for (int ks = 0; ks < kKS; ++ks) {
+        o[ks][0] *= up0;
+        o[ks][1] *= up1;
+        o[ks][2] *= up0;
+        o[ks][3] *= up1;
+      }
     }
     // ---- warp states: lane (r, cq) holds heads 2 cq, 2 cq + 1 (MMA columns); l summed over r
 #pragma unroll

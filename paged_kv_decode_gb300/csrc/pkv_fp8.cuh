@@ -141,12 +141,18 @@ __device__ __forceinline__ void fp8_query(uint32_t row, bool live, float qscale,
   qs1 = qscale * __shfl_sync(0xffffffffu, up, 8 * c + 4);  // lane (2c + 1, 0)
 }
 
-// Weights enter the value product 2^kWeightShift above their own size, so that fp16 holds them to 2^-38 of
-// the largest (its subnormals end at 2^-24) while the largest, 2^14, stays below fp16's 65504.
-constexpr int kWeightShift = 14;
+// Weights enter the value product 2^kWeightShift above their own size, so that fp16 holds them to 2^-39 of
+// the largest (half its subnormals' step, 2^-25) while the largest, 2^14, stays below fp16's 65504.
+constexpr float kWeightShift = 14.f;
 
-// 2^(e - 127) from an exponent field that may have fallen below the normal floats' (then 0)
-__device__ __forceinline__ float field_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(max(e, 0)) << 23); }
+// log2 of the scale that byte b stands for, b - 127, without a conversion (2^23 + b from its bits)
+__device__ __forceinline__ float scale_log2(uint32_t b) { return __uint_as_float(0x4b000000u | b) - 8388735.f; }
+
+// What a warp's o still has to be multiplied by: it is 2^(kWeightShift - w) sum_j 2^(s_j) v_j, to become
+// 2^(-m) times that sum (a warp without units: o is zero).
+__device__ __forceinline__ float value_power(float w, float m) {
+  return w == -CUDART_INF_F ? 0.f : ex2(w - m - kWeightShift);
+}
 
 // One unit of NP pages: the scores of its 16 NP tokens for the 8 head columns, the online-softmax update of
 // this lane's heads (2c, 2c + 1), and the value product. kt, vt: shared addresses of the pages' swizzled
@@ -155,12 +161,15 @@ __device__ __forceinline__ float field_pow2(int e) { return __uint_as_float(stat
 //
 // With k_j = 2^(ek_j) k8_j and v_j = 2^(ev_j) v8_j, s_j = qscale 2^(ek_j) <q, k8_j> (log2 domain), the sums
 // are l = sum_j 2^(s_j - m) in fp32, m the running maximum of s, and
-//   o = sum_j [2^(s_j - m) 2^(ev_j - E + kWeightShift)] v8_j
-// on the tensor cores, E the running maximum of ev over the warp's tokens (vmax holds its byte; when it grows
-// o is scaled down with the other rescaling). The key's power multiplies the fp32 score and the value's the
-// fp32 weight, so neither costs a rounding. The e4m3 operands become fp16 in registers (exact), so K and V
-// enter the products unrounded; the bracket is rounded to fp16 (2^-11 of it), tighter than the bf16
-// output's own rounding.
+//   o = sum_j [2^(s_j + ev_j - w + kWeightShift)] v8_j
+// on the tensor cores, w the running maximum of s + ev (of a token's contribution; value_power() takes w out
+// at the end). The key's power multiplies the fp32 score and the value's joins the exponent (one fp32 sum,
+// s_j + ev_j: 2^-17 of the weight while it is below 256, about the score's own last bits beyond). The e4m3 operands become fp16 in registers (exact), so K and V
+// enter the products unrounded; the bracket is rounded to fp16 (2^-11 of it), tighter than the bf16 output's
+// own rounding. Its largest value belongs to the token that contributes most, so a value row of any size that
+// the softmax gives nothing takes no precision from the others. With the maximum of ev alone in w's place
+// (one power for both heads, no second exponential), such a row 2^39 above the rest left nothing of them
+// (16 requests at 16/8/128 14.55 us that way, 14.59 this, 32 requests 30.4 and 30.7).
 //
 // ldmatrix moves 16-byte rows of 8 x 16-bit units. For K a lane's 32 bits are dims 4c .. 4c + 3 of token r:
 // as the pairs (k slots 2c, 2c + 1) and (8 + 2c, 9 + 2c) of the A operand, with the query's slots permuted
@@ -171,7 +180,7 @@ template <int KS, int NP>
 __device__ __forceinline__ void mma_unit_fp8(uint32_t kt, uint32_t vt, uint32_t st, const uint32_t (&off)[KS / 2],
                                              const uint32_t (&qf)[KS][2], int nv, float qs0, float qs1,
                                              float (&o)[KS][4], float& m0, float& m1, float& l0, float& l1,
-                                             int& vmax) {
+                                             float& w0, float& w1) {
   constexpr int kTile = kPageSize * KS * 16;  // bytes of a page's K or V
   const int lane = threadIdx.x & 31, r = lane >> 2;
   if (nv < kPageSize * NP) {
@@ -182,16 +191,15 @@ __device__ __forceinline__ void mma_unit_fp8(uint32_t kt, uint32_t vt, uint32_t 
     __syncwarp();
   }
   float s[NP][4];  // tokens r and r + 8 of each page x heads 2c, 2c + 1
-  int ev[NP][2];
-  float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F;
-  int top = 0;
+  float ev[NP][2];
+  float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F, y0 = -CUDART_INF_F, y1 = -CUDART_INF_F;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const uint32_t sp = st + p * kScaleBytes;
     const bool v0 = r < nv - p * kPageSize, v1 = r + 8 < nv - p * kPageSize;
     const uint32_t ek0 = lds8(sp + r), ek1 = lds8(sp + r + 8);
-    ev[p][0] = v0 ? static_cast<int>(lds8(sp + kPageSize + r)) : 0;
-    ev[p][1] = v1 ? static_cast<int>(lds8(sp + kPageSize + r + 8)) : 0;
+    ev[p][0] = scale_log2(lds8(sp + kPageSize + r));
+    ev[p][1] = scale_log2(lds8(sp + kPageSize + r + 8));
     float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < KS / 2; ++i) {
@@ -211,21 +219,21 @@ __device__ __forceinline__ void mma_unit_fp8(uint32_t kt, uint32_t vt, uint32_t 
     s[p][3] = v1 ? (sa[3] + sb[3]) * (k1 * qs1) : -CUDART_INF_F;
     x0 = fmaxf(x0, fmaxf(s[p][0], s[p][2]));
     x1 = fmaxf(x1, fmaxf(s[p][1], s[p][3]));
-    top = max(top, max(ev[p][0], ev[p][1]));
+    y0 = fmaxf(y0, fmaxf(s[p][0] + ev[p][0], s[p][2] + ev[p][1]));
+    y1 = fmaxf(y1, fmaxf(s[p][1] + ev[p][0], s[p][3] + ev[p][1]));
   }
 #pragma unroll
   for (int m = 4; m < 32; m <<= 1) {
     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, m));
     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, m));
+    y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, m));
+    y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, m));
   }
-  const int e_new = max(vmax, __reduce_max_sync(0xffffffffu, top));
-  const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-  if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1 || e_new != vmax)) {
-    const float al0 = ex2(m0 - n0), al1 = ex2(m1 - n1);  // 0 on the first unit
-    l0 *= al0;
-    l1 *= al1;
-    const float down = field_pow2(vmax - e_new + 127);
-    const float o0 = al0 * down, o1 = al1 * down;
+  const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1), u0 = fmaxf(w0, y0), u1 = fmaxf(w1, y1);
+  if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1 || u0 != w0 || u1 != w1)) {
+    l0 *= ex2(m0 - n0);  // 0 on the first unit
+    l1 *= ex2(m1 - n1);
+    const float o0 = ex2(w0 - u0), o1 = ex2(w1 - u1);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       o[ks][0] *= o0;
@@ -235,17 +243,18 @@ __device__ __forceinline__ void mma_unit_fp8(uint32_t kt, uint32_t vt, uint32_t 
     }
     m0 = n0;
     m1 = n1;
-    vmax = e_new;
+    w0 = u0;
+    w1 = u1;
   }
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const float p00 = ex2(s[p][0] - n0), p01 = ex2(s[p][1] - n1);  // token r
     const float p10 = ex2(s[p][2] - n0), p11 = ex2(s[p][3] - n1);  // token r + 8
-    const float f0 = field_pow2(ev[p][0] - e_new + kWeightShift + 127);
-    const float f1 = field_pow2(ev[p][1] - e_new + kWeightShift + 127);
     l0 += p00 + p10;
     l1 += p01 + p11;
-    const uint32_t pb0 = movm_t(pack_f16x2(p00 * f0, p01 * f0)), pb1 = movm_t(pack_f16x2(p10 * f1, p11 * f1));
+    const float c0 = kWeightShift - u0, c1 = kWeightShift - u1;
+    const uint32_t pb0 = movm_t(pack_f16x2(ex2(s[p][0] + ev[p][0] + c0), ex2(s[p][1] + ev[p][0] + c1)));
+    const uint32_t pb1 = movm_t(pack_f16x2(ex2(s[p][2] + ev[p][1] + c0), ex2(s[p][3] + ev[p][1] + c1)));
 #pragma unroll
     for (int i = 0; i < KS / 2; ++i) {
       uint32_t y[4], a0, a1, a2, a3;

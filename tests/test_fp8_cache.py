@@ -375,6 +375,47 @@ def test_decode_rows_of_very_different_scales(cuda_device):
     assert (bf16_to_f64(c.out)[2] == 0).all()
 
 
+def _check_weighted(c, extra=None):
+    """The outputs against float64, with fp16's smallest weight taken relative to the largest contribution of a row,
+    p_j max|v_j|: a weight is held to 2^-25 where the largest p_j 2^e_j is 2^14, and 448 * 2^e_j is at most twice the
+    row's largest value: n * 2^-38 * max_j p_j max|v_j|. extra(q, k): more error of the scores, [hq, 1]."""
+    got, q64 = bf16_to_f64(c.out), bf16_to_f64(c.q)
+    for b, n in enumerate(c.lens):
+        k, v = c.rows(b, 0), c.rows(b, 1)
+        out, absolute, size = attention64(q64[b], k, v, c.scale)
+        s = np.einsum("hgd,nhd->hgn", q64[b].reshape(c.hkv, -1, c.d), k) * c.scale
+        p = np.exp(s - s.max(axis=-1, keepdims=True))
+        p /= p.sum(axis=-1, keepdims=True)
+        top = (p * np.abs(v).max(axis=-1).T[:, None]).max(axis=-1).reshape(-1, 1)
+        tol = decode_bound(out, absolute, size, c.scale, c.d, int(n), top)
+        if extra is not None:
+            tol += 2 * extra(q64[b], k) * absolute
+        err = np.abs(got[b] - out)
+        assert (err <= tol).all(), f"request {b} of {n}: {err.max()} over by {(err - tol).max()}"
+    assert c.ws.status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("geom,lens", [("16q8kv128", [1000, 37, 64, 2900]), ("14q2kv64", [300, 20000]), ("8q1kv64", [9000])])
+@pytest.mark.parametrize("exponent,key", [(40, 4), (100, 4), (60, 2), (32, 0), (36, 1), (-60, 4)])
+def test_decode_value_rows_far_above_the_rest(cuda_device, geom, lens, exponent, key):
+    """One value row of a request 2^exponent above the others, at a key of -2^key in every dimension that the (positive)
+    queries score far below the others: it takes no precision from the rows that the softmax weighs."""
+
+    def edit(c):
+        for b, n in enumerate(c.lens):
+            j = int(n) // 3
+            page, slot = c.bt[b, j // 16], j % 16
+            c.kc[page, :, slot], c.sc[page, :, 0, slot] = 0xB8, 127 + key  # e4m3 -1
+            c.sc[page, :, 1, slot] = 127 + exponent - 8
+
+    c = Cache(51, GEOMS[geom], lens, cuda_device, edit=edit)
+    c.q = c.q.abs()
+    c.step()
+    torch.cuda.synchronize()
+    _check_weighted(c)
+
+
 @pytest.mark.gpu
 def test_decode_exact_cases(cuda_device):
     """A context of one token gives that value row; identical keys give the mean, here of equal rows."""
