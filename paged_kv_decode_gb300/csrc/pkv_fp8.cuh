@@ -110,8 +110,9 @@ __device__ __forceinline__ void fp8_offsets(uint32_t (&off)[D / 32]) {
 
 // The query rows as the B operand of the score product: lane (r, c) holds head r's dims 16 ks + 4c .. 4c + 3
 // (staged at `row`, bf16), as fp16 scaled by the power of two that brings the row's largest value into
-// [1, 2): bf16's 8 significant bits fit fp16's 11, and what falls below fp16's range is under 2^-24 of the
-// row's largest value. qs0, qs1: qscale times the powers taken out of heads 2c and 2c + 1.
+// [2^14, 2^15), the top of fp16's range: bf16's 8 significant bits are exact down to 2^-31 of the row's largest
+// value, below that they are held to 2^-39 of it. (With [1, 2) a row with one value 2^26 above the others lost
+// the others.) qs0, qs1: qscale times the powers taken out of heads 2c and 2c + 1.
 template <int KS>
 __device__ __forceinline__ void fp8_query(uint32_t row, bool live, float qscale, uint32_t (&qf)[KS][2], float& qs0,
                                           float& qs1) {
@@ -127,9 +128,9 @@ __device__ __forceinline__ void fp8_query(uint32_t row, bool live, float qscale,
     }
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-  // field E of the largest value; the factor 2^(127 - E) and its inverse stay normal floats
-  const uint32_t E = min(max(most >> 7, 1u), 253u);
-  const float down = __uint_as_float((254u - E) << 23), up = __uint_as_float(E << 23);
+  // field E of the largest value; the factor 2^(127 + 14 - E) and its inverse stay normal floats
+  const uint32_t E = min(max(most >> 7, 15u), 254u);
+  const float down = __uint_as_float((268u - E) << 23), up = __uint_as_float((E - 14u) << 23);
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks)
 #pragma unroll

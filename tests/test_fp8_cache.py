@@ -458,6 +458,30 @@ def test_decode_query_of_any_size(cuda_device):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("geom", ["16q8kv128", "14q2kv64"])
+@pytest.mark.parametrize("small", [-12, -20, -26])
+def test_decode_query_with_one_large_dimension(cuda_device, geom, small):
+    """Query rows of 2^small but for one dimension of 1, in which the keys are zero: the scores are the other dimensions'.
+    A query value keeps bf16's 8 bits down to 2^-31 of its row's largest and is held to 2^-39 of it below."""
+
+    def edit(c):
+        c.kc[..., 3] = 0
+        c.sc[:, :, 0] = c.sc[:, :, 0].astype(int) - small  # keys 2^-small larger
+
+    c = Cache(52, GEOMS[geom], [700, 33, 1, 90], cuda_device, edit=edit)
+    c.q = c.q * 2.0 ** small
+    c.q[..., 3] = 1.0
+    c.step()
+    torch.cuda.synchronize()
+
+    def lost(q, k):
+        most = np.abs(q).max(axis=-1, keepdims=True) * 2.0 ** -39
+        return c.scale * most * np.repeat(np.abs(k).sum(axis=-1).max(axis=0), c.hq // c.hkv)[:, None]
+
+    _check_weighted(c, lost)
+
+
+@pytest.mark.gpu
 def test_decode_page_order_does_not_matter(cuda_device):
     c = Cache(26, GEOMS["16q8kv128"], [500, 77, 1200], cuda_device)
     a = c.step().clone()
