@@ -457,12 +457,14 @@ int pkv_expand_fp8(const void* k_pages, const void* v_pages, const void* kv_scal
                    pkv_stream_t stream, void* workspace, size_t workspace_bytes);
 
 /*
- * Workspace bytes pkv_prefill_chunk_attn needs: the status header, split
- * counters (num_seqs x head pairs x ceil(max_q_len / 128) x 2 ints, with
- * num_kv_heads x ceil(G / 2) head pairs) and two partial records per SM of the
- * current device (for each of the 2 query heads of a pair: 128 rows x
- * head_dim dims of fp16 O / l, then fp32 max and sum per row: 67,584 bytes at
- * head_dim 128), for query tiles whose key range is cut between CTAs.
+ * Workspace bytes pkv_prefill_chunk_attn needs: the status header, two partial
+ * records per SM of the current device (for each of the 2 query heads of a
+ * pair: 128 rows x head_dim dims of fp16 O / l, then fp32 max and sum per row:
+ * 67,584 bytes at head_dim 128, and as much room at 64), for query tiles whose
+ * key range is cut between CTAs, and split counters (num_seqs x head pairs x
+ * ceil(max_q_len / 128) x 2 ints, with num_kv_heads x ceil(G / 2) head pairs).
+ * Calls of any geometry, num_seqs and max_q_len may share a workspace that is
+ * large enough for each of them.
  */
 size_t pkv_prefill_workspace_bytes(const pkv_cache_desc* desc, int32_t num_seqs, int32_t max_q_len);
 
@@ -548,7 +550,8 @@ size_t pkv_mixed_workspace_bytes(const pkv_cache_desc* desc, int32_t num_seqs, i
  *  workspace:       >= pkv_mixed_workspace_bytes(desc, num_seqs, max_q_len,
  *                   dec_batch, dec_max_pages_per_seq), zeroed once by
  *                   pkv_workspace_init (the call leaves its counters at zero);
- *                   serves mixed-step calls only
+ *                   serves mixed-step calls only, of any sizes it is large
+ *                   enough for
  * Geometry: 16 query / 8 KV heads, head_dim 128, page 16 (PKV_ERR_UNSUPPORTED
  * otherwise).
  */

@@ -228,8 +228,7 @@ size_t pkv_prefill_workspace_bytes(const pkv_cache_desc* desc, int32_t num_seqs,
   if (check_desc_prefill(desc) != PKV_OK || num_seqs < 0 || max_q_len < 0) return 0;
   int sms = 0;
   if (current_device(&sms) != PKV_OK) return 0;
-  return pkv::prefill_workspace_bytes(desc->num_q_heads, desc->num_kv_heads, desc->head_dim, num_seqs, max_q_len,
-                                      sms);
+  return pkv::prefill_workspace_bytes(desc->num_q_heads, desc->num_kv_heads, num_seqs, max_q_len, sms);
 }
 
 int pkv_prefill_chunk_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
@@ -252,8 +251,8 @@ int pkv_prefill_chunk_attn(const void* q, const void* k_pages, const void* v_pag
   int sms = 0;
   rc = current_device(&sms);
   if (rc != PKV_OK) return rc;
-  if (workspace_bytes < pkv::prefill_workspace_bytes(desc->num_q_heads, desc->num_kv_heads, desc->head_dim, num_seqs,
-                                                     max_q_len, sms))
+  if (workspace_bytes <
+      pkv::prefill_workspace_bytes(desc->num_q_heads, desc->num_kv_heads, num_seqs, max_q_len, sms))
     return PKV_ERR_WORKSPACE_TOO_SMALL;
   return pkv::launch_prefill(q, k_pages, v_pages, block_table, prefix_lens, cu_q_lens, num_seqs, total_q, out, scale,
                              desc->num_q_heads, desc->num_kv_heads, desc->head_dim, max_pages_per_seq, max_q_len,

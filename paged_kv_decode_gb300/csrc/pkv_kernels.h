@@ -90,8 +90,7 @@ int launch_rope_table(float* table, int32_t max_pos, int32_t head_dim, double th
 
 // Chunked prefill (prefill.cu): page size 16, head_dim 64 or 128, 1 to 8 query heads per KV head.
 bool prefill_supported(int num_q_heads, int num_kv_heads, int head_dim, int page_size);
-size_t prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int32_t num_seqs, int32_t max_q_len,
-                               int num_sms);
+size_t prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int32_t num_seqs, int32_t max_q_len, int num_sms);
 int prefill_max_seqs();
 // The decode half of a mixed step (16/8/128 only): decode requests attended in the prefill launch.
 struct MixedDecode {

@@ -594,6 +594,9 @@ __device__ __noinline__ void mixed_decode_cta(const PrefillArgs& a, const CUtens
     }
     orow[n * kHeadDim + d] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
   }
+  __syncthreads();  // the records are read: cleared, as the next call's counters may lie there
+  float4* spent = reinterpret_cast<float4*>(a.drec + (static_cast<size_t>(b) * kKVHeads + g) * a.dmaxc * (kGroup * kRec));
+  for (int x = tid; x < nc * (kGroup * kRec) / 4; x += blockDim.x) spent[x] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (tid == 0) *counter = 0;
 }
 
@@ -1472,14 +1475,16 @@ static EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Workspace: status header, split counters [num_seqs][head pairs][tmax][2], then
-// two partial records per CTA of the persistent grid (one CTA per SM).
+// Workspace: status header, two partial records per CTA of the persistent grid (one
+// CTA per SM), split counters [num_seqs][head pairs][tmax][2]. The records stay behind
+// as they are, so they come first, with the room of head_dim 128's at any head_dim:
+// a call's counters, which must be zero, never lie where another call left records.
 static int pf_pairs(int hq, int hkv) { return hkv * ((hq / hkv + 1) / 2); }
 static size_t pf_counter_bytes(int32_t num_seqs, int32_t max_q_len, int pairs) {
   const size_t tmax = (static_cast<size_t>(max_q_len) + kPfRows - 1) / kPfRows;
   return (static_cast<size_t>(num_seqs) * pairs * tmax * 2 * 4 + 255) / 256 * 256;
 }
-static size_t pf_rec_bytes(int hd) { return hd == 64 ? PfDim<64>::kRecBytes : PfDim<128>::kRecBytes; }
+static size_t pf_records_bytes(int num_sms) { return static_cast<size_t>(2) * num_sms * PfDim<128>::kRecBytes; }
 
 bool prefill_supported(int num_q_heads, int num_kv_heads, int head_dim, int page_size) {
   if (num_q_heads <= 0 || num_kv_heads <= 0 || page_size != kPageSize) return false;
@@ -1489,21 +1494,20 @@ bool prefill_supported(int num_q_heads, int num_kv_heads, int head_dim, int page
   return g >= 1 && g <= 8;
 }
 
-size_t prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int32_t num_seqs, int32_t max_q_len,
-                               int num_sms) {
-  return PKV_STATUS_BYTES + pf_counter_bytes(num_seqs, max_q_len, pf_pairs(num_q_heads, num_kv_heads)) +
-         static_cast<size_t>(2) * num_sms * pf_rec_bytes(head_dim);
+size_t prefill_workspace_bytes(int num_q_heads, int num_kv_heads, int32_t num_seqs, int32_t max_q_len, int num_sms) {
+  return PKV_STATUS_BYTES + pf_records_bytes(num_sms) +
+         pf_counter_bytes(num_seqs, max_q_len, pf_pairs(num_q_heads, num_kv_heads));
 }
 
 // The mixed step's decode part after the prefill workspace: chunk counters [dec_batch][8] (256-byte
-// padded), then the partial records [dec_batch][8][chunks][2][132] floats.
+// padded), then the partial records [dec_batch][8][chunks][2][132] floats, both zero between calls.
 static size_t mixed_counter_bytes(int32_t dec_batch) {
   return (static_cast<size_t>(dec_batch) * kKVHeads * 4 + 255) / 256 * 256;
 }
 size_t mixed_workspace_bytes(int32_t num_seqs, int32_t max_q_len, int32_t dec_batch, int32_t dec_max_pages,
                              int num_sms) {
   const int maxc = mixed_chunks_per_pair(dec_max_pages);
-  return prefill_workspace_bytes(kQHeads, kKVHeads, kHeadDim, num_seqs, max_q_len, num_sms) +
+  return prefill_workspace_bytes(kQHeads, kKVHeads, num_seqs, max_q_len, num_sms) +
          mixed_counter_bytes(dec_batch) +
          static_cast<size_t>(dec_batch) * kKVHeads * (maxc > 1 ? maxc : 0) * kGroup * kMixRec * 4;
 }
@@ -1600,8 +1604,8 @@ int launch_prefill(const void* q, const void* k_pages, const void* v_pages, cons
   a.pairs = num_kv_heads * a.npair;
   a.scale_log2 = scale * kLog2e;
   a.status = reinterpret_cast<int*>(ws);
-  a.counters = reinterpret_cast<int*>(ws + PKV_STATUS_BYTES);
-  a.records = ws + PKV_STATUS_BYTES + pf_counter_bytes(num_seqs, max_q_len, a.pairs);
+  a.records = ws + PKV_STATUS_BYTES;
+  a.counters = reinterpret_cast<int*>(ws + PKV_STATUS_BYTES + pf_records_bytes(num_sms));
   a.dq = mixed ? static_cast<const __nv_bfloat16*>(dec->q) : nullptr;
   a.dbt = mixed ? dec->block_table : nullptr;
   a.dlens = mixed ? dec->seq_lens : nullptr;
@@ -1610,7 +1614,7 @@ int launch_prefill(const void* q, const void* k_pages, const void* v_pages, cons
   a.dmax_pages = mixed ? dec->max_pages : 1;
   a.dmaxc = mixed_chunks_per_pair(a.dmax_pages);
   {
-    unsigned char* dws = ws + prefill_workspace_bytes(num_q_heads, num_kv_heads, head_dim, num_seqs, max_q_len, num_sms);
+    unsigned char* dws = ws + prefill_workspace_bytes(num_q_heads, num_kv_heads, num_seqs, max_q_len, num_sms);
     a.dcnt = mixed ? reinterpret_cast<int*>(dws) : nullptr;
     a.drec = mixed ? reinterpret_cast<float*>(dws + mixed_counter_bytes(a.dbatch)) : nullptr;
   }
