@@ -1141,7 +1141,7 @@ __global__ void __launch_bounds__(DecThreads<Geo, kFused>::n, Geo::kCtasPerSm)
     }
 
     if constexpr (Geo::kFp8) {
-      const float up0 = value_power(vw0, m0), up1 = value_power(vw1, m1);
+      const float up0 = value_power(vw0), up1 = value_power(vw1);
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         o[ks][0] *= up0;

@@ -149,11 +149,8 @@ constexpr float kWeightShift = 14.f;
 // log2 of the scale that byte b stands for, b - 127, without a conversion (2^23 + b from its bits)
 __device__ __forceinline__ float scale_log2(uint32_t b) { return __uint_as_float(0x4b000000u | b) - 8388735.f; }
 
-// What a warp's o still has to be multiplied by: it is 2^(kWeightShift - w) sum_j 2^(s_j) v_j, to become
-// 2^(-m) times that sum (a warp without units: o is zero).
-__device__ __forceinline__ float value_power(float w, float m) {
-  return w == -CUDART_INF_F ? 0.f : ex2(w - m - kWeightShift);
-}
+// What takes w (below) out of a warp's o at the end; a warp without units has w = -inf and o = 0.
+__device__ __forceinline__ float value_power(float w) { return ex2(w - kWeightShift); }
 
 // One unit of NP pages: the scores of its 16 NP tokens for the 8 head columns, the online-softmax update of
 // this lane's heads (2c, 2c + 1), and the value product. kt, vt: shared addresses of the pages' swizzled
@@ -162,15 +159,17 @@ __device__ __forceinline__ float value_power(float w, float m) {
 //
 // With k_j = 2^(ek_j) k8_j and v_j = 2^(ev_j) v8_j, s_j = qscale 2^(ek_j) <q, k8_j> (log2 domain), the sums
 // are l = sum_j 2^(s_j - m) in fp32, m the running maximum of s, and
-//   o = sum_j [2^(s_j + ev_j - w + kWeightShift)] v8_j
-// on the tensor cores, w the running maximum of s + ev (of a token's contribution; value_power() takes w out
-// at the end). The key's power multiplies the fp32 score and the value's joins the exponent (one fp32 sum,
-// s_j + ev_j: 2^-17 of the weight while it is below 256, about the score's own last bits beyond). The e4m3 operands become fp16 in registers (exact), so K and V
+//   o = sum_j [2^(s_j - m + ev_j - w + kWeightShift)] v8_j
+// on the tensor cores, w the running maximum of s - m + ev, a token's contribution (value_power() takes it out
+// at the end). The key's power multiplies the fp32 score and the value's joins the exponent, which is held
+// against m first: s + ev would lose ev where scores are large. The sum's rounding costs the weights that
+// count 2^-17 at most. The e4m3 operands become fp16 in registers (exact), so K and V
 // enter the products unrounded; the bracket is rounded to fp16 (2^-11 of it), tighter than the bf16 output's
 // own rounding. Its largest value belongs to the token that contributes most, so a value row of any size that
 // the softmax gives nothing takes no precision from the others. With the maximum of ev alone in w's place
 // (one power for both heads, no second exponential), such a row 2^39 above the rest left nothing of them
-// (16 requests at 16/8/128 14.55 us that way, 14.59 this, 32 requests 30.4 and 30.7).
+// (16 requests at 16/8/128 14.55 us that way, 14.78 this, 32 requests 30.4 and 30.7; finding w from s + ev
+// beside m, where scores are small enough, saved nothing).
 //
 // ldmatrix moves 16-byte rows of 8 x 16-bit units. For K a lane's 32 bits are dims 4c .. 4c + 3 of token r:
 // as the pairs (k slots 2c, 2c + 1) and (8 + 2c, 9 + 2c) of the A operand, with the query's slots permuted
@@ -193,7 +192,7 @@ __device__ __forceinline__ void mma_unit_fp8(uint32_t kt, uint32_t vt, uint32_t 
   }
   float s[NP][4];  // tokens r and r + 8 of each page x heads 2c, 2c + 1
   float ev[NP][2];
-  float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F, y0 = -CUDART_INF_F, y1 = -CUDART_INF_F;
+  float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const uint32_t sp = st + p * kScaleBytes;
@@ -220,21 +219,34 @@ __device__ __forceinline__ void mma_unit_fp8(uint32_t kt, uint32_t vt, uint32_t 
     s[p][3] = v1 ? (sa[3] + sb[3]) * (k1 * qs1) : -CUDART_INF_F;
     x0 = fmaxf(x0, fmaxf(s[p][0], s[p][2]));
     x1 = fmaxf(x1, fmaxf(s[p][1], s[p][3]));
-    y0 = fmaxf(y0, fmaxf(s[p][0] + ev[p][0], s[p][2] + ev[p][1]));
-    y1 = fmaxf(y1, fmaxf(s[p][1] + ev[p][0], s[p][3] + ev[p][1]));
   }
 #pragma unroll
   for (int m = 4; m < 32; m <<= 1) {
     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, m));
     x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, m));
+  }
+  const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+  float y0 = -CUDART_INF_F, y1 = -CUDART_INF_F;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    s[p][0] -= n0;
+    s[p][1] -= n1;
+    s[p][2] -= n0;
+    s[p][3] -= n1;
+    y0 = fmaxf(y0, fmaxf(s[p][0] + ev[p][0], s[p][2] + ev[p][1]));
+    y1 = fmaxf(y1, fmaxf(s[p][1] + ev[p][0], s[p][3] + ev[p][1]));
+  }
+#pragma unroll
+  for (int m = 4; m < 32; m <<= 1) {
     y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, m));
     y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, m));
   }
-  const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1), u0 = fmaxf(w0, y0), u1 = fmaxf(w1, y1);
-  if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1 || u0 != w0 || u1 != w1)) {
-    l0 *= ex2(m0 - n0);  // 0 on the first unit
-    l1 *= ex2(m1 - n1);
-    const float o0 = ex2(w0 - u0), o1 = ex2(w1 - u1);
+  const float g0 = m0 - n0, g1 = m1 - n1;  // -inf on the first unit
+  const float u0 = fmaxf(w0 + g0, y0), u1 = fmaxf(w1 + g1, y1);
+  if (__any_sync(0xffffffffu, g0 != 0.f || g1 != 0.f || u0 != w0 || u1 != w1)) {
+    l0 *= ex2(g0);
+    l1 *= ex2(g1);
+    const float o0 = ex2(w0 + g0 - u0), o1 = ex2(w1 + g1 - u1);  // 0 on the first unit
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       o[ks][0] *= o0;
@@ -249,10 +261,8 @@ __device__ __forceinline__ void mma_unit_fp8(uint32_t kt, uint32_t vt, uint32_t 
   }
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    const float p00 = ex2(s[p][0] - n0), p01 = ex2(s[p][1] - n1);  // token r
-    const float p10 = ex2(s[p][2] - n0), p11 = ex2(s[p][3] - n1);  // token r + 8
-    l0 += p00 + p10;
-    l1 += p01 + p11;
+    l0 += ex2(s[p][0]) + ex2(s[p][2]);  // tokens r and r + 8
+    l1 += ex2(s[p][1]) + ex2(s[p][3]);
     const float c0 = kWeightShift - u0, c1 = kWeightShift - u1;
     const uint32_t pb0 = movm_t(pack_f16x2(ex2(s[p][0] + ev[p][0] + c0), ex2(s[p][1] + ev[p][0] + c1)));
     const uint32_t pb1 = movm_t(pack_f16x2(ex2(s[p][2] + ev[p][1] + c0), ex2(s[p][3] + ev[p][1] + c1)));

@@ -458,6 +458,33 @@ def test_decode_query_of_any_size(cuda_device):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("power", [10, 20, 40, 80])
+@pytest.mark.parametrize("geom", ["16q8kv128", "14q2kv64"])
+def test_decode_huge_scores_give_one_row(cuda_device, geom, power):
+    """Scores so far apart that the largest takes everything: its value row, to bf16's 2^-8 and the weight's 2^-11, for
+    every head whose two largest scores differ by more than fp32's error in them and 64 (2^-92 in weight)."""
+    c = Cache(53, GEOMS[geom], [700, 33, 1, 9000], cuda_device)
+    c.q = c.q * 2.0 ** power
+    c.step()
+    torch.cuda.synchronize()
+    got, q64 = bf16_to_f64(c.out), bf16_to_f64(c.q)
+    clear = 0
+    for b, n in enumerate(c.lens):
+        k, v = c.rows(b, 0), c.rows(b, 1)
+        for h in range(c.hq):
+            g = h // (c.hq // c.hkv)
+            s = k[:, g] @ q64[b, h] * c.scale
+            at = np.argsort(s)
+            error = (c.d + 8) * 2.0 ** -24 * c.scale * (np.abs(k[:, g]) @ np.abs(q64[b, h])).max()
+            if n > 1 and s[at[-1]] - s[at[-2]] <= 64 + 2 * error:
+                continue
+            clear += 1
+            want = v[at[-1], g]
+            assert (np.abs(got[b, h] - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want)).all(), (b, h)
+    assert clear >= 2 * c.hq and c.ws.status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("geom", ["16q8kv128", "14q2kv64"])
 @pytest.mark.parametrize("small", [-12, -20, -26])
 def test_decode_query_with_one_large_dimension(cuda_device, geom, small):
