@@ -50,7 +50,7 @@ WORKLOAD = ("qwen3-0.6b decode step: 28 layers x bs16, 16q/8kv heads, d128, page
 # (dram__bytes_read.sum + dram__bytes_write.sum), valid only for the decode kernel source it was
 # measured on (sha256 prefix of csrc/decode_kernel.cuh followed by csrc/pkv_mma.cuh); any other source
 # reports null.
-NCU_DECODE_TRAFFIC = {"37aff601de101808": 107_554_816 + 3_372_288}
+NCU_DECODE_TRAFFIC = {"b3641a0951979114": 107_553_280 + 3_416_576}
 
 
 def _decode_traffic():

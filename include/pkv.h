@@ -381,14 +381,13 @@ int pkv_append_rope_fp8(const void* q, int64_t q_stride, const void* k_new, int6
 /*
  * pkv_decode_attn_fp8 -- pkv_decode_attn over the 8-bit cache: the same sums
  * over the rows that the cache stands for, in fp32, with the keys and values
- * unrounded and the softmax weights p_j rounded to fp16 before they multiply V:
- * p_j is off by at most 2^-11 of itself, or, where that is more, by what makes
- * 2^-39 of the largest p_i 2^(e_i) of the sum out of p_j 2^(e_j) (e: the scales
- * of the value rows). Weights below 2^-126 count as 0. Query values are exact
- * down to 2^-31 of their row's largest and held to 2^-39 of it below.
- * Arguments, lengths of zero, errors and the workspace
- * (pkv_decode_workspace_bytes) are pkv_decode_attn's; a workspace may serve
- * both in turn.
+ * unrounded and the softmax weights p_j rounded to fp16, with the scale 2^(e_j)
+ * of their value row, before they multiply V: p_j 2^(e_j) is off by at most
+ * 2^-11 of itself, or by 2^-39 of the largest of them where that is more.
+ * Weights below 2^-126 count as 0. Query values are exact down to 2^-31 of
+ * their row's largest and held to 2^-39 of it below. Arguments, lengths of
+ * zero, errors and the workspace (pkv_decode_workspace_bytes) are
+ * pkv_decode_attn's; a workspace may serve both in turn.
  *
  *  flags: 0 or PKV_DECODE_EARLY_PREFETCH. Here the caller promises that the
  *         previous kernel on the stream writes neither block_table nor

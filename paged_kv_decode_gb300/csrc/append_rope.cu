@@ -16,8 +16,9 @@
 // between); value rows are copied or quantised, never rotated.
 //
 // The op reads and writes every row once and is bound by memory; what stands in
-// the way is the arithmetic between, so it is kept to about 100 instructions per
-// warp and 4 rows. D / 16 lanes take a row, lane l dims 8l .. 8l + 7 and
+// the way is the arithmetic between, so it is kept down: 225 warp instructions
+// per 4 rows at D = 128, copies and bookkeeping included (a plain copy takes 118),
+// 253 in the 8-bit form. D / 16 lanes take a row, lane l dims 8l .. 8l + 7 and
 // D/2 + 8l .. D/2 + 8l + 7: both halves of a pair are in one lane (no exchange
 // for the rotation), every access is 16 bytes, and the row's sum of squares and
 // largest magnitude are 2 or 3 shuffles away. The rows that a warp's lanes hold

@@ -57,16 +57,17 @@
 //    pkv_fp8.cuh) runs the same schedule over units of two pages, a unit's row
 //    scales copied beside its tiles. Measured on one GB300 (a CUDA graph of
 //    calls, each waiting for the one before): 16 requests of 300 to 3000 tokens
-//    13.4 us (50.5 MB; 7.5 us at the measured copy rate), one of 40k tokens
-//    17.8 us (82.6 MB; 12.3), 27 of 9 to 8000 at 32 query / 8 KV heads 37.3 us
+//    13.8 us (50.5 MB; 7.5 us at the measured copy rate), one of 40k tokens
+//    18.2 us (82.6 MB; 12.3), 27 of 9 to 8000 at 32 query / 8 KV heads 37.9 us
 //    (212 MB; 31.7). Of the first, 1.8 us pass before the first copies go out
 //    (the wait, the length scan, the block table), 8.2 stream at 6.1 TB/s and
-//    1.5 end and merge the split pieces. In the fused step a row warp turns (norm,
+//    1.5 end and merge the split pieces (clock samples of a version that took
+//    13.4). In the fused step a row warp turns (norm,
 //    rotation) each piece's query rows and turns and quantises its new row while
 //    the piece before streams; the consumer that takes the request's last unit
 //    writes the row over the staged slot and into the pool; the producer never
-//    waits for the predecessor in early mode (12.8 us per layer for the 16
-//    requests, norms and rotation included; bf16 pages, rotation alone: 18.0).
+//    waits for the predecessor in early mode (13.0 us per layer for the 16
+//    requests, norms and rotation included; bf16 pages, rotation alone: 18.2).
 //    Attention alone, in early mode, waits with the requests' last units, which
 //    hold rows that the predecessor wrote.
 //  * The query rows of the next piece are copied into shared memory (cp.async)
@@ -78,7 +79,7 @@
 //    holders are consecutive CTAs. The records are merged (log-sum-exp, in an
 //    order fixed by the pair alone) in one of two ways, each its own
 //    instantiation, chosen by the expected number of holders per pair (grid
-//    size over batch x KV heads):
+//    size over batch x KV heads); batches over the 8-bit cache always poll:
 //     - Counted, for few pairs over many CTAs (one long request): fp32
 //       records; after its last piece a CTA bumps the pairs' counters (one
 //       fence, one round trip) and the CTA that completes a count stages the
@@ -370,21 +371,25 @@ struct Shares {
     return f < s_next ? f : s_next;
   }
   // the CTA whose share holds index f (< T)
-  __device__ __forceinline__ int cta(long long f) const { return static_cast<int>(((cost(f) + 1) * n + Ctot - 1) / Ctot - 1); }
+  __device__ __forceinline__ int cta(long long f) const {
+    return static_cast<int>(((cost(f) + 1) * n + Ctot - 1) / Ctot - 1);
+  }
 };
 
 // CTAs that take a share of T pages in `pairs` non-empty (request, KV head) pairs: all that get kShareMin pages.
-// With the 8-bit cache a pair has at most 2 sqrt(u) holders, u its units on average: one CTA reads all their
-// records, and a share's streaming shrinks with 1 / holders. For one request (the counted merge) the number is a
-// multiple of the pairs, so that shares end with the pairs: a CTA with two split pieces ends twice.
+// With the 8-bit cache and fewer than 64 pairs, at most 2 sqrt(u) times the pairs, u the units of a pair on
+// average: one CTA reads all of a pair's records, and a share's streaming shrinks with 1 / holders. That bounds the
+// holders of requests of about equal length; one far longer than the others still spreads over most of the CTAs.
+// For one request (the counted merge) the number is a multiple of the pairs, so that shares end with the pairs: a
+// CTA with two split pieces ends twice.
 // One request at 8/1/64, 4096 / 16384 / 40000 tokens: 15.9 / 29.2 / 29.6 us over all CTAs, 9.1 / 11.6 / 15.8 so
 // (1.5 sqrt(u): 9.1 / 12.2 / 16.4, 3 sqrt(u): 9.1 / 12.9 / 16.9); at 16/8/128, 1000 and 4096: 7.7 / 8.4, 7.2 / 8.5.
 template <class Geo, bool kPolled>
 __device__ __forceinline__ int share_count(long long T, int pairs) {
   const long long n = T / Geo::kShareMin > 0 ? T / Geo::kShareMin : 1;
   const int all = static_cast<int>(n < gridDim.x ? n : gridDim.x);
-  // (64 pairs of more than 5 units reach 304 CTAs with 2 sqrt(u) holders each, and fewer units have few holders
-  // anyway: batches are spared the division and the root, 0.2 us before their first copies)
+  // (at 64 pairs the bound is 256 CTAs or more from 4 units a pair on, most of a GB300's 304, and fewer units have
+  // few holders anyway: larger batches are spared the division and the root, 0.2 us before their first copies)
   if (Geo::kFp8 && pairs > 0 && (!kPolled || pairs < 64)) {
     const unsigned p = static_cast<unsigned>(pairs), u = static_cast<unsigned>(T) / p;  // u >= 1 units a pair
     unsigned h = static_cast<unsigned>(2.f * sqrtf(static_cast<float>(u)));
@@ -1517,9 +1522,9 @@ int launch_decode_geo(const DecodeLaunch& c) {
   // 10.6; as its own rule for larger batches it lost, bs16 13.4 narrow and 14.2 wide.)
   const bool wide = (Geo::D == 128 || Geo::kFp8) && grid > kPollMax * pairs && pairs * c.max_pages >= kWideMinPages;
   const int grid_used = wide ? (c.num_sms < kMaxGrid ? c.num_sms : kMaxGrid) : grid;
-  // (the 8-bit cache counts for one request alone: with shares of unequal pairs a CTA ends up to three split pieces,
-  // and its bound on holders keeps polled merges short -- 10 requests of 120 to 1084 tokens at 8/1/64 12.1 us counted,
-  // 7.9 polled)
+  // (the 8-bit cache counts for one request alone, whose shares end with its pairs; with pairs of unequal length a
+  // CTA may end two split pieces, and polling for them is quicker -- 10 requests of 120 to 1084 tokens at 8/1/64
+  // 12.1 us counted, 7.9 polled)
   const bool polled = grid_used <= kPollMax * pairs || pairs > kCountMax || (Geo::kFp8 && c.batch > 1);
   const size_t smem = wide ? GeoW::smem_bytes(c.batch) : Geo::smem_bytes(c.batch);
   const bool fused = c.k_new != nullptr;

@@ -161,15 +161,14 @@ __device__ __forceinline__ float value_power(float w) { return ex2(w - kWeightSh
 // are l = sum_j 2^(s_j - m) in fp32, m the running maximum of s, and
 //   o = sum_j [2^(s_j - m + ev_j - w + kWeightShift)] v8_j
 // on the tensor cores, w the running maximum of s - m + ev, a token's contribution (value_power() takes it out
-// at the end). The key's power multiplies the fp32 score and the value's joins the exponent, which is held
-// against m first: s + ev would lose ev where scores are large. The sum's rounding costs the weights that
-// count 2^-17 at most. The e4m3 operands become fp16 in registers (exact), so K and V
-// enter the products unrounded; the bracket is rounded to fp16 (2^-11 of it), tighter than the bf16 output's
-// own rounding. Its largest value belongs to the token that contributes most, so a value row of any size that
-// the softmax gives nothing takes no precision from the others. With the maximum of ev alone in w's place
-// (one power for both heads, no second exponential), such a row 2^39 above the rest left nothing of them
-// (16 requests at 16/8/128 14.55 us that way, 14.78 this, 32 requests 30.4 and 30.7; finding w from s + ev
-// beside m, where scores are small enough, saved nothing).
+// at the end). The key's power multiplies the fp32 score; the value's joins the exponent, which is held against
+// m first (s + ev would lose ev where scores are large; the sum's rounding costs the weights that count 2^-17 at
+// most). The e4m3 operands become fp16 in registers (exact), so K and V enter the products unrounded; the
+// bracket is rounded to fp16 (2^-11 of it), tighter than the bf16 output's own rounding. Its largest value
+// belongs to the token that contributes most, so a value row of any size that the softmax gives nothing takes
+// no precision from the others. With the maximum of ev alone in w's place (one power for both heads, no second
+// exponential), such a row 2^39 above the rest left nothing of them (16 requests at 16/8/128 14.55 us that way,
+// 14.78 this, 32 requests 30.4 and 30.7; finding w from s + ev beside m, where scores are small, saved nothing).
 //
 // ldmatrix moves 16-byte rows of 8 x 16-bit units. For K a lane's 32 bits are dims 4c .. 4c + 3 of token r:
 // as the pairs (k slots 2c, 2c + 1) and (8 + 2c, 9 + 2c) of the A operand, with the query's slots permuted

@@ -14,7 +14,7 @@ int launch_append(const void* k_new, const void* v_new, const int32_t* slot_mapp
                   cudaStream_t stream);
 
 // Decode (decode.cu, decode_kernel.cuh): page size 16, head_dim 64 or 128, num_q_heads / num_kv_heads
-// from 1 to 8. Workspace = [status header | counters (batch * kv heads) | records].
+// from 1 to 8. Workspace = [status header | counters | records], laid out in decode_kernel.cuh.
 bool decode_supported(int num_q_heads, int num_kv_heads, int head_dim, int page_size);
 size_t decode_workspace_bytes(int num_q_heads, int num_kv_heads, int head_dim, int32_t batch, int num_sms);
 // k_new / v_new (nullable): fused append of each request's new token at position seq_lens[b] - 1.

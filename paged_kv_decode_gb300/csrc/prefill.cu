@@ -595,7 +595,8 @@ __device__ __noinline__ void mixed_decode_cta(const PrefillArgs& a, const CUtens
     orow[n * kHeadDim + d] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
   }
   __syncthreads();  // the records are read: cleared, as the next call's counters may lie there
-  float4* spent = reinterpret_cast<float4*>(a.drec + (static_cast<size_t>(b) * kKVHeads + g) * a.dmaxc * (kGroup * kRec));
+  float* recs = a.drec + (static_cast<size_t>(b) * kKVHeads + g) * a.dmaxc * (kGroup * kRec);
+  float4* spent = reinterpret_cast<float4*>(recs);
   for (int x = tid; x < nc * (kGroup * kRec) / 4; x += blockDim.x) spent[x] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (tid == 0) *counter = 0;
 }
