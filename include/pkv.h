@@ -34,8 +34,9 @@
  *  - Every call: num_q_heads = 16, num_kv_heads = 8, head_dim = 128,
  *    page_size = 16 (the Qwen3 decoder; the tuned kernels).
  *  - pkv_append, pkv_decode_attn, pkv_decode_append_attn,
- *    pkv_decode_append_rope_attn, pkv_append_rope, pkv_prefill_chunk_attn and
- *    the calls of the 8-bit cache also take page_size = 16, head_dim 64 or 128,
+ *    pkv_decode_append_rope_attn, pkv_append_rope, pkv_prefill_chunk_attn,
+ *    pkv_tree_attn, pkv_keep_nodes, pkv_copy_pages and the calls of the 8-bit
+ *    cache also take page_size = 16, head_dim 64 or 128,
  *    any num_kv_heads and num_q_heads = G * num_kv_heads with G from 1 to 8
  *    (other decoder backbones; decode runs the same persistent split-KV
  *    kernel with the head counts read at run time, early prefetch included;
@@ -43,7 +44,8 @@
  *  - Anything else returns PKV_ERR_UNSUPPORTED.
  *
  * Conventions for every entry point:
- *  - Every pointer argument except `desc` is DEVICE memory owned by the
+ *  - Every pointer argument except `desc` (and the arrays of pools of
+ *    pkv_keep_nodes and pkv_copy_pages) is DEVICE memory owned by the
  *    caller; `desc` is a host pointer read during the call only. The library
  *    never allocates, frees or synchronises, and keeps no state between calls
  *    apart from a per-device cache of the SM count. The one exception is
@@ -79,8 +81,9 @@
  *    scratch (counters, and for decode tagged records) having been left
  *    cleared by the previous call of that kind. Decode calls of any geometry,
  *    batch and cache type may share a workspace that is large enough for each
- *    of them. The appends and pkv_expand_fp8 use only the status word and may
- *    share either kind's.
+ *    of them. The tree attention calls are a third kind. The appends,
+ *    pkv_expand_fp8, pkv_keep_nodes and pkv_copy_pages use only the status word
+ *    and may share any kind's.
  */
 #ifndef PKV_H_
 #define PKV_H_
@@ -560,6 +563,128 @@ int pkv_mixed_step_attn(const void* q, const void* k_pages, const void* v_pages,
                         const int32_t* dec_block_table, const int32_t* dec_seq_lens, void* dec_out, int32_t dec_batch,
                         int32_t dec_max_pages_per_seq, float scale, pkv_stream_t stream, const pkv_cache_desc* desc,
                         void* workspace, size_t workspace_bytes);
+
+/*
+ * Workspace bytes the tree attention calls need: the status header, a counter
+ * per SM of the current device and two partial records per SM (66,560 bytes
+ * each), for items whose keys are cut between CTAs. One size for all calls on a
+ * device: tree attention calls of any geometry, sizes and cache type may share a
+ * workspace (in stream order). Returns 0 for unsupported arguments.
+ */
+size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t num_seqs, int32_t max_nodes);
+
+/*
+ * pkv_tree_attn -- attention of drafted tokens over the paged cache: the
+ * verification step of speculative decoding.
+ *
+ * Source: the pages have no counterpart. Decode takes over 94% of the time on
+ * long audio ("Optimizing ASR for 90-minute multi-speaker audio", section "Time
+ * spent: profiling") and reads a request's whole cache for each new token; this
+ * call reads it once for all tokens that a draft proposes.
+ *
+ * Request n owns the nodes (rows of q) cu_nodes[n] .. cu_nodes[n+1]-1, T of
+ * them, in any order that the caller numbers them in (for pkv_keep_nodes:
+ * parents before children). Their key and value rows lie in the cache behind the
+ * request's P = prefix_lens[n] tokens, node i's at position P + i (append them
+ * first: pkv_append_rope with slots of positions P + i and rotary positions of
+ * the nodes' depths). Node i sees positions 0 .. P - 1 and the nodes j < T whose
+ * bit j of tree_mask[cu_nodes[n] + i] is set (its ancestors and, usually,
+ * itself). Without masks the nodes are a chain: node i sees nodes 0 .. i.
+ *   out[i][h] = sum_j softmax_j(scale * <q[i][h], k_j>) v_j over what it sees,
+ * zeros for a node that sees nothing. bf16 inputs, fp32 sums and statistics, the
+ * softmax weights rounded to bf16 before they multiply V, bf16 output. Rows that a
+ * node does not see have no influence, whatever they hold.
+ *
+ *  q, out:       bf16 [total_nodes][num_q_heads][head_dim]; rows past
+ *                cu_nodes[num_seqs] of out are left as they were
+ *  block_table:  int32 [num_seqs][max_pages_per_seq]; it covers the nodes too
+ *  prefix_lens:  int32 [num_seqs], >= 0; P + T <= max_pages_per_seq * page_size
+ *  cu_nodes:     int32 [num_seqs + 1], non-decreasing, cu_nodes[num_seqs] <=
+ *                total_nodes. A request without nodes (padding) costs nothing
+ *  tree_mask:    int64 [total_nodes], 8-byte aligned, or NULL. Bits at and
+ *                past T are ignored
+ *  max_nodes:    host-side upper bound on any request's nodes, 1 .. 64
+ *                (PKV_ERR_UNSUPPORTED beyond)
+ *  num_seqs:     0 .. 1024 (PKV_ERR_UNSUPPORTED beyond); num_seqs *
+ *                max_pages_per_seq * max(num_kv_heads, 8) < 2^31
+ *  workspace:    >= pkv_tree_workspace_bytes(...), zeroed once by
+ *                pkv_workspace_init (the call leaves its counters at zero). It
+ *                serves tree attention calls only
+ * A request whose lengths are out of bounds, or that has more than max_nodes
+ * nodes, sets PKV_ERR_OUT_OF_BOUNDS and its rows are not written. A page id
+ * outside the pool sets it too; the rows of that request are then undefined.
+ * Geometry: head_dim 64 or 128, 1 to 8 query heads per KV head, page_size 16.
+ */
+int pkv_tree_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
+                  const int32_t* prefix_lens, const int32_t* cu_nodes, const int64_t* tree_mask, int32_t num_seqs,
+                  int32_t total_nodes, int32_t max_nodes, void* out, float scale, pkv_stream_t stream,
+                  const pkv_cache_desc* desc, int32_t max_pages_per_seq, void* workspace, size_t workspace_bytes);
+
+/*
+ * pkv_tree_attn_fp8 -- pkv_tree_attn over the 8-bit cache. The rows that it
+ * stands for are exact in bf16: the outputs are those of pkv_expand_fp8 followed
+ * by pkv_tree_attn, bit for bit. max_pages_per_seq <= 2^27 - 2.
+ */
+int pkv_tree_attn_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
+                      const int32_t* block_table, const int32_t* prefix_lens, const int32_t* cu_nodes,
+                      const int64_t* tree_mask, int32_t num_seqs, int32_t total_nodes, int32_t max_nodes, void* out,
+                      float scale, pkv_stream_t stream, const pkv_cache_desc* desc, int32_t max_pages_per_seq,
+                      void* workspace, size_t workspace_bytes);
+
+/*
+ * pkv_keep_nodes -- after verification: the rows of the accepted nodes move up
+ * to consecutive positions behind the prefix, in all layers at once.
+ *
+ * Source: the pages have no counterpart (see pkv_tree_attn).
+ *
+ * For every request s, layer and i < path_lens[s], the K and V rows (and, of an
+ * 8-bit cache, their scale bytes) at position prefix_lens[s] + path[s][i] are
+ * written to position prefix_lens[s] + i, bit-exactly and as if all rows were
+ * read before any is written. The request's length is then prefix_lens[s] +
+ * path_lens[s]. Other rows are left as they were.
+ *
+ *  path:         int32 [num_seqs][max_path], the accepted nodes' numbers,
+ *                rising (0 <= path[s][0] < path[s][1] < ...); entries at and
+ *                past path_lens[s] are not read. An entry that does not rise, or
+ *                whose position or page lies outside the table or the pool, sets
+ *                PKV_ERR_OUT_OF_BOUNDS and its row is not moved
+ *  path_lens:    int32 [num_seqs], 0 .. max_path (clamped, with
+ *                PKV_ERR_OUT_OF_BOUNDS)
+ *  prefix_lens, block_table: as for pkv_tree_attn; no two requests may have
+ *                the same page among those that hold their nodes
+ *  num_seqs:     >= 0 (0 launches nothing); num_seqs * max_pages_per_seq *
+ *                max(num_kv_heads, 8) < 2^31
+ *  max_path:     1 .. 64 (PKV_ERR_UNSUPPORTED beyond)
+ *  k_pages, v_pages, kv_scales: HOST arrays of n_layers device pointers, one
+ *                pool per layer, read during the call only; all pools of the
+ *                geometry of `desc`. kv_scales NULL: bf16 pools; else 8-bit ones
+ *  n_layers:     >= 0 (0 launches nothing); one launch per 64 layers
+ *  workspace:    as for pkv_append (may be NULL)
+ */
+int pkv_keep_nodes(const int32_t* path, const int32_t* path_lens, const int32_t* prefix_lens,
+                   const int32_t* block_table, int32_t num_seqs, int32_t max_path, int32_t max_pages_per_seq,
+                   void* const* k_pages, void* const* v_pages, void* const* kv_scales, int32_t n_layers,
+                   const pkv_cache_desc* desc, pkv_stream_t stream, void* workspace, size_t workspace_bytes);
+
+/*
+ * pkv_copy_pages -- whole pages to other pages, in all layers at once: what a
+ * forked request (a companion prompt, another hypothesis) cannot share with its
+ * origin, usually the last page that both would append to.
+ *
+ * Source: the cache is allocated on demand, page by page ("FunASR vLLM Inference
+ * Engine Guide", section 2); the pages do not say how requests part.
+ *
+ *  src, dst:     int32 [n_pairs]; page dst[i] of every pool becomes page src[i]
+ *                of it (and, of an 8-bit cache, its scale bytes). A pair with a
+ *                negative page is skipped; one with a page >= num_pages sets
+ *                PKV_ERR_OUT_OF_BOUNDS and is skipped. No dst may be another
+ *                pair's src or dst (either row's bytes may end up there)
+ *  n_pairs:      >= 0 (0 launches nothing)
+ *  k_pages, v_pages, kv_scales, n_layers, workspace: as for pkv_keep_nodes
+ */
+int pkv_copy_pages(const int32_t* src, const int32_t* dst, int32_t n_pairs, void* const* k_pages, void* const* v_pages,
+                   void* const* kv_scales, int32_t n_layers, const pkv_cache_desc* desc, pkv_stream_t stream,
+                   void* workspace, size_t workspace_bytes);
 
 /*
  * pkv_decode_attn_noalloc -- pkv_decode_attn without a caller-provided workspace.

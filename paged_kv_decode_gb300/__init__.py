@@ -39,6 +39,7 @@ __all__ = [
     "decode_workspace_bytes", "prefill_workspace_bytes", "workspace_init", "read_status", "status_string",
     "decode_attn_noalloc", "decode_append_attn", "mixed_step_attn", "mixed_workspace_bytes", "rope_cos_sin",
     "append_rope", "append_rope_fp8", "decode_attn_fp8", "decode_append_attn_fp8", "expand_fp8",
+    "tree_attn", "tree_attn_fp8", "tree_workspace_bytes", "keep_nodes", "copy_pages",
 ]
 
 
@@ -332,6 +333,47 @@ def expand_fp8(k_pages, v_pages, kv_scales, block_table, seq_lens, k_out, v_out,
     out_block_table [S, max_pages] of k_out / v_out [P', Hkv, 16, D] (what prefill_chunk_attn then reads)."""
     _check(_lib.binding().expand_fp8(k_pages, v_pages, kv_scales, block_table, seq_lens, k_out, v_out, out_block_table,
                                      workspace, stream), "pkv_expand_fp8")
+
+
+# ---------------------------------------------------------------------------- speculative decoding, forks
+def tree_workspace_bytes(num_seqs: int, max_nodes: int, num_pages: int = 1, num_q_heads: int = 16,
+                         num_kv_heads: int = 8, head_dim: int = 128) -> int:
+    """Workspace bytes of a tree attention call (one size for all of them on a device; 0 for unsupported arguments)."""
+    d = desc(num_pages, num_q_heads, num_kv_heads, head_dim)
+    return int(_lib.load().pkv_tree_workspace_bytes(ctypes.byref(d), int(num_seqs), int(max_nodes)))
+
+
+def tree_attn(q, k_pages, v_pages, block_table, prefix_lens, cu_nodes, tree_mask, out, scale: float, max_nodes: int,
+              workspace: Workspace, stream=None):
+    """Attention of drafted tokens, the nodes of a tree per request (at most max_nodes <= 64): out [total, Hq, D] for
+    q [total, Hq, D] packed by cu_nodes [S + 1]. Node i's rows lie in the cache at position prefix_lens + i; it sees the
+    prefix and the nodes whose bits are set in its tree_mask [total] (int64), or, with tree_mask None (a chain), nodes
+    0 .. i. Geometries as for decode_attn."""
+    _check(_lib.binding().tree_attn(q, k_pages, v_pages, None, block_table, prefix_lens, cu_nodes, tree_mask, out, scale,
+                                    max_nodes, workspace, stream), "pkv_tree_attn")
+
+
+def tree_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, prefix_lens, cu_nodes, tree_mask, out, scale: float,
+                  max_nodes: int, workspace: Workspace, stream=None):
+    """tree_attn over the 8-bit cache (pools and kv_scales as for append_rope_fp8): the outputs of expand_fp8 followed by
+    tree_attn, bit for bit."""
+    _check(_lib.binding().tree_attn_fp8(q, k_pages, v_pages, kv_scales, block_table, prefix_lens, cu_nodes, tree_mask, out,
+                                        scale, max_nodes, workspace, stream), "pkv_tree_attn_fp8")
+
+
+def keep_nodes(path, path_lens, prefix_lens, block_table, k_pages, v_pages, kv_scales=None,
+               workspace: Optional[Workspace] = None, stream=None):
+    """The rows of the accepted nodes path [S, max_path] (rising numbers, path_lens [S] of them) move to the positions
+    straight behind prefix_lens [S], in the pools of all layers: one pool [P, Hkv, 16, D], all of them stacked
+    [L, P, Hkv, 16, D], or a list of pools; kv_scales likewise for an 8-bit cache."""
+    _check(_lib.binding().keep_nodes(path, path_lens, prefix_lens, block_table, k_pages, v_pages, kv_scales, workspace,
+                                     stream), "pkv_keep_nodes")
+
+
+def copy_pages(src, dst, k_pages, v_pages, kv_scales=None, workspace: Optional[Workspace] = None, stream=None):
+    """Pages src [n] to pages dst [n] of the pools of all layers (given as for keep_nodes); pairs with a negative page are
+    skipped. No dst may be another pair's src or dst."""
+    _check(_lib.binding().copy_pages(src, dst, k_pages, v_pages, kv_scales, workspace, stream), "pkv_copy_pages")
 
 
 def prefill_chunk_attn(q, k_pages, v_pages, block_table, prefix_lens, cu_q_lens, out, scale: float, max_q_len: int,

@@ -57,6 +57,13 @@ PROTOTYPES = {
     "pkv_mixed_workspace_bytes": (_sz, [_dp, _i32, _i32, _i32, _i32]),
     "pkv_mixed_step_attn": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp,
                                            _vp, _i32, _i32, _f32, _vp, _dp, _vp, _sz]),
+    "pkv_tree_workspace_bytes": (_sz, [_dp, _i32, _i32]),
+    "pkv_tree_attn": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _f32, _vp, _dp, _i32, _vp,
+                                     _sz]),
+    "pkv_tree_attn_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _f32, _vp, _dp, _i32,
+                                         _vp, _sz]),
+    "pkv_keep_nodes": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _dp, _vp, _vp, _sz]),
+    "pkv_copy_pages": (ctypes.c_int, [_vp, _vp, _i32, _vp, _vp, _vp, _i32, _dp, _vp, _vp, _sz]),
     "pkv_decode_attn_noalloc": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _dp, _i32, _i32]),
     "pkv_selftest_wait_timeout": (ctypes.c_int, [_vp, _sz, ctypes.c_int64, _vp]),
 }

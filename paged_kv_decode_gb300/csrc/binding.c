@@ -1,7 +1,8 @@
 /*
  * binding.c -- CPython side of the calls whose kernels take a few
  * microseconds: pkv_append_rope, pkv_append_rope_fp8, pkv_decode_attn_fp8,
- * pkv_decode_append_attn_fp8 and pkv_expand_fp8. It reads the torch tensors' attributes, checks them and makes
+ * pkv_decode_append_attn_fp8, pkv_expand_fp8, pkv_tree_attn, pkv_tree_attn_fp8,
+ * pkv_keep_nodes and pkv_copy_pages. It reads the torch tensors' attributes, checks them and makes
  * the C call. Written against the CPython API alone (no torch headers): a
  * tensor is asked for its dtype, device, strides and address like any object.
  * In Python, with ctypes, the same checks and call take 8.7 us
@@ -13,19 +14,20 @@
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <string.h>
 
 #include "pkv.h"
 
 /* Attribute names and torch objects, looked up once. */
 static PyObject *s_dtype, *s_get_device, *s_is_contiguous, *s_data_ptr, *s_shape, *s_stride, *s_tensor, *s_cuda_stream,
     *s_device, *s_index;
-static PyObject *t_bf16, *t_i32, *t_f32, *t_e4m3, *t_e8m0;
+static PyObject *t_bf16, *t_i32, *t_i64, *t_f32, *t_e4m3, *t_e8m0;
 static PyObject *f_raw_stream, *f_get_device, *f_exchange_device;
 
 typedef struct {
   void* ptr;
   int nd;
-  long long shape[4];
+  long long shape[5];
 } Tensor;
 
 static long as_long(PyObject* o) { /* steals o; -1 with an exception set on failure */
@@ -35,7 +37,7 @@ static long as_long(PyObject* o) { /* steals o; -1 with an exception set on fail
   return v;
 }
 
-/* Up to 4 entries of a tuple of ints (a shape or strides); *nd is its length. Steals `t`. */
+/* Up to 5 entries of a tuple of ints (a shape or strides); *nd is its length. Steals `t`. */
 static int read_ints(PyObject* t, const char* name, int* nd, long long* v) {
   if (t == NULL) return -1;
   if (!PyTuple_Check(t)) {
@@ -45,7 +47,7 @@ static int read_ints(PyObject* t, const char* name, int* nd, long long* v) {
   }
   const Py_ssize_t n = PyTuple_GET_SIZE(t);
   *nd = (int)n;
-  for (Py_ssize_t i = 0; i < n && i < 4; ++i) {
+  for (Py_ssize_t i = 0; i < n && i < 5; ++i) {
     v[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(t, i));
     if (v[i] == -1 && PyErr_Occurred()) {
       Py_DECREF(t);
@@ -112,7 +114,7 @@ static int get_tensor(PyObject* t, const char* name, PyObject* dtype, long* dev,
 static int get_rows(PyObject* t, const char* name, long* dev, long long n, long long heads, long long d, Tensor* out,
                     long long* stride) {
   if (check_place(t, name, t_bf16, dev) != 0) return -1;
-  long long st[4];
+  long long st[5];
   int nd;
   if (read_ints(PyObject_GetAttr(t, s_shape), name, &out->nd, out->shape) != 0) return -1;
   if (out->nd != 3 || out->shape[0] != n || out->shape[1] != heads || out->shape[2] != d) {
@@ -130,7 +132,7 @@ static int get_rows(PyObject* t, const char* name, long* dev, long long n, long 
 
 static int same_shape(const Tensor* a, const Tensor* b) {
   if (a->nd != b->nd) return 0;
-  for (int i = 0; i < a->nd && i < 4; ++i)
+  for (int i = 0; i < a->nd && i < 5; ++i)
     if (a->shape[i] != b->shape[i]) return 0;
   return 1;
 }
@@ -460,12 +462,207 @@ static PyObject* expand_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n_arg
   return leave_device(back, rc);
 }
 
+/* (q, k_pages, v_pages, kv_scales or None, block_table, prefix_lens, cu_nodes, tree_mask or None, out, scale, max_nodes,
+ * workspace, stream) */
+static PyObject* tree_any(PyObject* const* a, Py_ssize_t n_args, int fp8) {
+  if (count_args("tree_attn", n_args, 13) != 0) return NULL;
+  long dev = -1, back;
+  Tensor kp, vp, sc, q, out, bt, pl, cu, mask;
+  pkv_cache_desc d;
+  if (get_cache(a[1], a[2], fp8 ? a[3] : NULL, &dev, &kp, &vp, &sc, &d) != 0) return NULL;
+  if (get_tensor(a[0], "q", t_bf16, &dev, 3, &q) != 0 || get_tensor(a[8], "out", t_bf16, &dev, 3, &out) != 0 ||
+      get_tensor(a[4], "block_table", t_i32, &dev, 2, &bt) != 0 ||
+      get_tensor(a[5], "prefix_lens", t_i32, &dev, -1, &pl) != 0 || get_tensor(a[6], "cu_nodes", t_i32, &dev, -1, &cu) != 0)
+    return NULL;
+  if (q.shape[2] != d.head_dim || !same_shape(&q, &out) || numel(&pl) != bt.shape[0] || numel(&cu) != bt.shape[0] + 1)
+    return bad_shape("shape mismatch"), NULL;
+  mask.ptr = NULL;
+  if (a[7] != Py_None) {
+    if (get_tensor(a[7], "tree_mask", t_i64, &dev, -1, &mask) != 0) return NULL;
+    if (numel(&mask) != q.shape[0]) return bad_shape("tree_mask must be [total_nodes]"), NULL;
+  }
+  if (fits_i32(q.shape[0], q.shape[1], bt.shape[0]) != 0 || fits_i32(bt.shape[1], 0, 0) != 0) return NULL;
+  d.num_q_heads = (int32_t)q.shape[1];
+  const double scale = PyFloat_AsDouble(a[9]);
+  if (scale == -1.0 && PyErr_Occurred()) return NULL;
+  const long max_nodes = PyLong_AsLong(a[10]);
+  if ((max_nodes == -1 && PyErr_Occurred()) || fits_i32(max_nodes, 0, 0) != 0) return NULL;
+  if (max_nodes < 0) return bad_shape("max_nodes is negative"), NULL;
+  void* ws;
+  size_t ws_bytes;
+  pkv_stream_t stream;
+  if (get_workspace(a[11], dev, &ws, &ws_bytes) != 0 || get_stream(a[12], dev, &stream) != 0) return NULL;
+  if (enter_device(dev, &back) != 0) return NULL;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = fp8 ? pkv_tree_attn_fp8(q.ptr, kp.ptr, vp.ptr, sc.ptr, bt.ptr, pl.ptr, cu.ptr, mask.ptr, (int32_t)bt.shape[0],
+                               (int32_t)q.shape[0], (int32_t)max_nodes, out.ptr, (float)scale, stream, &d,
+                               (int32_t)bt.shape[1], ws, ws_bytes)
+           : pkv_tree_attn(q.ptr, kp.ptr, vp.ptr, bt.ptr, pl.ptr, cu.ptr, mask.ptr, (int32_t)bt.shape[0],
+                           (int32_t)q.shape[0], (int32_t)max_nodes, out.ptr, (float)scale, stream, &d,
+                           (int32_t)bt.shape[1], ws, ws_bytes);
+  Py_END_ALLOW_THREADS;
+  return leave_device(back, rc);
+}
+
+static PyObject* tree_attn(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  return tree_any(a, n, 0);
+}
+
+static PyObject* tree_attn_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  return tree_any(a, n, 1);
+}
+
+/* The pools of one kind of all layers: a tensor of 4 dimensions (one layer), one of 5 (all layers, stacked) or a list or
+ * tuple of the former. *first is the shape of one pool; ptrs (PyMem) holds *n addresses. */
+static int get_layers(PyObject* o, const char* name, PyObject* dtype, long* dev, Tensor* first, void*** ptrs, long long* n) {
+  const int many = PyList_Check(o) || PyTuple_Check(o);
+  Tensor t;
+  *ptrs = NULL;
+  if (!many) {
+    if (get_tensor(o, name, dtype, dev, -1, &t) != 0) return -1;
+    if (t.nd != 4 && t.nd != 5) {
+      PyErr_Format(PyExc_ValueError, "%s must have 4 dimensions, or 5 for the pools of all layers, got %d", name, t.nd);
+      return -1;
+    }
+    *n = t.nd == 5 ? t.shape[0] : 1;
+    first->nd = 4;
+    long long bytes = dtype == t_bf16 ? 2 : 1;
+    for (int i = 0; i < 4; ++i) bytes *= first->shape[i] = t.shape[i + t.nd - 4];
+    if (fits_i32(*n, 0, 0) != 0) return -1;
+    if ((*ptrs = PyMem_Malloc((size_t)(*n + 1) * sizeof(void*))) == NULL) return PyErr_NoMemory(), -1;
+    for (long long i = 0; i < *n; ++i) (*ptrs)[i] = (char*)t.ptr + i * bytes;
+    return 0;
+  }
+  *n = PySequence_Fast_GET_SIZE(o);
+  if (fits_i32(*n, 0, 0) != 0) return -1;
+  if ((*ptrs = PyMem_Malloc((size_t)(*n + 1) * sizeof(void*))) == NULL) return PyErr_NoMemory(), -1;
+  first->nd = 0;
+  for (long long i = 0; i < *n; ++i) {
+    if (i >= PySequence_Fast_GET_SIZE(o)) return bad_shape("the list of pools changed its length");
+    PyObject* pool = PySequence_Fast_GET_ITEM(o, i);
+    Py_INCREF(pool);
+    const int rc = get_tensor(pool, name, dtype, dev, 4, &t);
+    Py_DECREF(pool);
+    if (rc != 0) return -1;
+    if (i == 0) *first = t;
+    if (!same_shape(first, &t)) {
+      PyErr_Format(PyExc_ValueError, "%s: the layers' pools differ in shape", name);
+      return -1;
+    }
+    (*ptrs)[i] = t.ptr;
+  }
+  return 0;
+}
+
+typedef struct {
+  void** p[3]; /* K, V, scales or NULL */
+  long long n;
+  pkv_cache_desc d;
+} Layers;
+
+static void free_layers(Layers* l) {
+  for (int i = 0; i < 3; ++i) PyMem_Free(l->p[i]);
+}
+
+static int get_all_layers(PyObject* k, PyObject* v, PyObject* scales, long* dev, Layers* l) {
+  Tensor tk, tv, ts;
+  long long nv, ns;
+  const int fp8 = scales != Py_None;
+  memset(l, 0, sizeof *l);
+  if (get_layers(k, "k_pages", fp8 ? t_e4m3 : t_bf16, dev, &tk, &l->p[0], &l->n) != 0 ||
+      get_layers(v, "v_pages", fp8 ? t_e4m3 : t_bf16, dev, &tv, &l->p[1], &nv) != 0)
+    return -1;
+  if (l->n < 1) return bad_shape("there are no pools");
+  if (nv != l->n || !same_shape(&tk, &tv)) return bad_shape(kPools);
+  if (fp8) {
+    if (get_layers(scales, "kv_scales", t_e8m0, dev, &ts, &l->p[2], &ns) != 0) return -1;
+    if (ns != l->n || ts.shape[0] != tk.shape[0] || ts.shape[1] != tk.shape[1] || ts.shape[2] != 2 || ts.shape[3] != tk.shape[2])
+      return bad_shape("kv_scales must be [num_pages, num_kv_heads, 2, page_size] of the pools' sizes, for each layer");
+  }
+  if (fits_i32(tk.shape[0], tk.shape[1], tk.shape[2]) != 0 || fits_i32(tk.shape[3], 0, 0) != 0) return -1;
+  l->d.num_pages = (int32_t)tk.shape[0];
+  l->d.num_q_heads = l->d.num_kv_heads = (int32_t)tk.shape[1];
+  l->d.page_size = (int32_t)tk.shape[2];
+  l->d.head_dim = (int32_t)tk.shape[3];
+  return 0;
+}
+
+/* (path, path_lens, prefix_lens, block_table, k_pages, v_pages, kv_scales or None, workspace, stream) */
+static PyObject* keep_nodes(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  (void)self;
+  if (count_args("keep_nodes", n_args, 9) != 0) return NULL;
+  long dev = -1, back;
+  Tensor path, n, pl, bt;
+  Layers l;
+  void* ws;
+  size_t ws_bytes;
+  pkv_stream_t stream;
+  PyObject* done = NULL;
+  if (get_all_layers(a[4], a[5], a[6], &dev, &l) != 0) goto end;
+  if (get_tensor(a[0], "path", t_i32, &dev, 2, &path) != 0 || get_tensor(a[1], "path_lens", t_i32, &dev, -1, &n) != 0 ||
+      get_tensor(a[2], "prefix_lens", t_i32, &dev, -1, &pl) != 0 || get_tensor(a[3], "block_table", t_i32, &dev, 2, &bt) != 0)
+    goto end;
+  if (numel(&n) != path.shape[0] || numel(&pl) != path.shape[0] || bt.shape[0] != path.shape[0]) {
+    bad_shape("shape mismatch");
+    goto end;
+  }
+  if (fits_i32(path.shape[0], path.shape[1], bt.shape[1]) != 0) goto end;
+  if (get_workspace(a[7], dev, &ws, &ws_bytes) != 0 || get_stream(a[8], dev, &stream) != 0) goto end;
+  if (enter_device(dev, &back) != 0) goto end;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = pkv_keep_nodes(path.ptr, n.ptr, pl.ptr, bt.ptr, (int32_t)path.shape[0], (int32_t)path.shape[1], (int32_t)bt.shape[1],
+                      l.p[0], l.p[1], l.p[2], (int32_t)l.n, &l.d, stream, ws, ws_bytes);
+  Py_END_ALLOW_THREADS;
+  done = leave_device(back, rc);
+end:
+  free_layers(&l);
+  return done;
+}
+
+/* (src, dst, k_pages, v_pages, kv_scales or None, workspace, stream) */
+static PyObject* copy_pages(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  (void)self;
+  if (count_args("copy_pages", n_args, 7) != 0) return NULL;
+  long dev = -1, back;
+  Tensor src, dst;
+  Layers l;
+  void* ws;
+  size_t ws_bytes;
+  pkv_stream_t stream;
+  PyObject* done = NULL;
+  if (get_all_layers(a[2], a[3], a[4], &dev, &l) != 0) goto end;
+  if (get_tensor(a[0], "src", t_i32, &dev, 1, &src) != 0 || get_tensor(a[1], "dst", t_i32, &dev, 1, &dst) != 0) goto end;
+  if (src.shape[0] != dst.shape[0]) {
+    bad_shape("src and dst differ in length");
+    goto end;
+  }
+  if (fits_i32(src.shape[0], 0, 0) != 0) goto end;
+  if (get_workspace(a[5], dev, &ws, &ws_bytes) != 0 || get_stream(a[6], dev, &stream) != 0) goto end;
+  if (enter_device(dev, &back) != 0) goto end;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = pkv_copy_pages(src.ptr, dst.ptr, (int32_t)src.shape[0], l.p[0], l.p[1], l.p[2], (int32_t)l.n, &l.d, stream, ws, ws_bytes);
+  Py_END_ALLOW_THREADS;
+  done = leave_device(back, rc);
+end:
+  free_layers(&l);
+  return done;
+}
+
 static PyMethodDef methods[] = {
     {"append_rope", (PyCFunction)(void (*)(void))append_rope, METH_FASTCALL, NULL},
     {"append_rope_fp8", (PyCFunction)(void (*)(void))append_rope_fp8, METH_FASTCALL, NULL},
     {"decode_attn_fp8", (PyCFunction)(void (*)(void))decode_attn_fp8, METH_FASTCALL, NULL},
     {"decode_append_attn_fp8", (PyCFunction)(void (*)(void))decode_append_attn_fp8, METH_FASTCALL, NULL},
     {"expand_fp8", (PyCFunction)(void (*)(void))expand_fp8, METH_FASTCALL, NULL},
+    {"tree_attn", (PyCFunction)(void (*)(void))tree_attn, METH_FASTCALL, NULL},
+    {"tree_attn_fp8", (PyCFunction)(void (*)(void))tree_attn_fp8, METH_FASTCALL, NULL},
+    {"keep_nodes", (PyCFunction)(void (*)(void))keep_nodes, METH_FASTCALL, NULL},
+    {"copy_pages", (PyCFunction)(void (*)(void))copy_pages, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Checks and calls of libpkv's short kernels.", -1,
@@ -490,6 +687,7 @@ PyMODINIT_FUNC PyInit__binding(void) {
     const char* text;
   } objects[] = {{&t_bf16, torch, "bfloat16"},
                  {&t_i32, torch, "int32"},
+                 {&t_i64, torch, "int64"},
                  {&t_f32, torch, "float32"},
                  {&t_e4m3, torch, "float8_e4m3fn"},
                  {&t_e8m0, torch, "float8_e8m0fnu"},

@@ -1,6 +1,6 @@
 // pkv_abi.cu -- the extern "C" entry points of libpkv: argument checks on the
 // host, launch-configuration choice, and the status word helpers. All device
-// work is in append.cu, decode.cu (decode_kernel.cuh) and prefill.cu.
+// work is in the kernels' own files (pkv_kernels.h names them).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -489,6 +489,129 @@ int pkv_expand_fp8(const void* k_pages, const void* v_pages, const void* kv_scal
   a.num_pages = desc->num_pages;
   a.out_pages = out_num_pages;
   return pkv::launch_expand_fp8(a, desc->head_dim, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t num_seqs, int32_t max_nodes) {
+  if (check_desc_decode(desc) != PKV_OK || num_seqs < 0 || max_nodes < 0) return 0;
+  if (num_seqs > pkv::tree_max_seqs() || max_nodes > pkv::tree_max_nodes()) return 0;
+  int sms = 0;
+  if (current_device(&sms) != PKV_OK) return 0;
+  return pkv::tree_workspace_bytes(sms);
+}
+
+// Shared by the bf16 and the 8-bit tree attention (kv_scales is nullptr for the bf16 one).
+static int tree_attn(const pkv::TreeAttn& t, bool fp8, pkv_stream_t stream, const pkv_cache_desc* desc, void* workspace,
+                     size_t workspace_bytes) {
+  int rc = check_desc_decode(desc);
+  if (rc != PKV_OK) return rc;
+  if (t.num_seqs < 0 || t.total_nodes < 0 || t.max_nodes < 0 || t.max_pages < 1) return PKV_ERR_BAD_SHAPE;
+  if (t.max_pages > kMaxTablePages || !table_fits(t.num_seqs, t.max_pages, desc->num_kv_heads)) return PKV_ERR_BAD_SHAPE;
+  if (t.num_seqs > pkv::tree_max_seqs() || t.max_nodes > pkv::tree_max_nodes()) return PKV_ERR_UNSUPPORTED;
+  if (workspace == nullptr) return PKV_ERR_NULL_ARG;
+  if (workspace_bytes < PKV_STATUS_BYTES) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if (t.num_seqs == 0 || t.total_nodes == 0 || t.max_nodes == 0) return PKV_OK;
+  if (!t.q || !t.k_pages || !t.v_pages || (fp8 && !t.kv_scales) || !t.block_table || !t.prefix_lens || !t.cu_nodes || !t.out)
+    return PKV_ERR_NULL_ARG;
+  if (!aligned16(t.q) || !aligned16(t.k_pages) || !aligned16(t.v_pages) || !aligned16(t.kv_scales) || !aligned16(t.out) ||
+      !aligned16(workspace) || (reinterpret_cast<uintptr_t>(t.tree_mask) & 7u) != 0)
+    return PKV_ERR_MISALIGNED;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != PKV_OK) return rc;
+  if (workspace_bytes < pkv::tree_workspace_bytes(sms)) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  return pkv::launch_tree_attn(t, desc->num_q_heads, desc->num_kv_heads, desc->head_dim, desc->num_pages, workspace, sms,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+int pkv_tree_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
+                  const int32_t* prefix_lens, const int32_t* cu_nodes, const int64_t* tree_mask, int32_t num_seqs,
+                  int32_t total_nodes, int32_t max_nodes, void* out, float scale, pkv_stream_t stream,
+                  const pkv_cache_desc* desc, int32_t max_pages_per_seq, void* workspace, size_t workspace_bytes) {
+  const pkv::TreeAttn t = {q,   k_pages, v_pages,  nullptr,     block_table,       prefix_lens, cu_nodes, tree_mask,
+                           out, scale,   num_seqs, total_nodes, max_pages_per_seq, max_nodes};
+  return tree_attn(t, false, stream, desc, workspace, workspace_bytes);
+}
+
+int pkv_tree_attn_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
+                      const int32_t* block_table, const int32_t* prefix_lens, const int32_t* cu_nodes,
+                      const int64_t* tree_mask, int32_t num_seqs, int32_t total_nodes, int32_t max_nodes, void* out,
+                      float scale, pkv_stream_t stream, const pkv_cache_desc* desc, int32_t max_pages_per_seq,
+                      void* workspace, size_t workspace_bytes) {
+  const pkv::TreeAttn t = {q,   k_pages, v_pages,  kv_scales,   block_table,       prefix_lens, cu_nodes, tree_mask,
+                           out, scale,   num_seqs, total_nodes, max_pages_per_seq, max_nodes};
+  return tree_attn(t, true, stream, desc, workspace, workspace_bytes);
+}
+
+// The pools of layers l0 .. of a call that takes arrays of them; PKV_ERR_NULL_ARG / MISALIGNED.
+static int move_pools(void* const* k_pages, void* const* v_pages, void* const* kv_scales, int32_t l0, int32_t n,
+                      pkv::MovePools* out) {
+  for (int32_t i = 0; i < n; ++i) {
+    out->k[i] = k_pages[l0 + i];
+    out->v[i] = v_pages[l0 + i];
+    out->scales[i] = kv_scales != nullptr ? kv_scales[l0 + i] : nullptr;
+    if (!out->k[i] || !out->v[i] || (kv_scales != nullptr && !out->scales[i])) return PKV_ERR_NULL_ARG;
+    if (!aligned16(out->k[i]) || !aligned16(out->v[i]) || !aligned16(out->scales[i])) return PKV_ERR_MISALIGNED;
+  }
+  return PKV_OK;
+}
+
+int pkv_keep_nodes(const int32_t* path, const int32_t* path_lens, const int32_t* prefix_lens,
+                   const int32_t* block_table, int32_t num_seqs, int32_t max_path, int32_t max_pages_per_seq,
+                   void* const* k_pages, void* const* v_pages, void* const* kv_scales, int32_t n_layers,
+                   const pkv_cache_desc* desc, pkv_stream_t stream, void* workspace, size_t workspace_bytes) {
+  int rc = check_desc_decode(desc);
+  if (rc != PKV_OK) return rc;
+  if (num_seqs < 0 || max_path < 0 || max_pages_per_seq < 1 || n_layers < 0) return PKV_ERR_BAD_SHAPE;
+  if (max_pages_per_seq > kMaxTablePages || !table_fits(num_seqs, max_pages_per_seq, desc->num_kv_heads))
+    return PKV_ERR_BAD_SHAPE;
+  if (max_path > pkv::tree_max_nodes()) return PKV_ERR_UNSUPPORTED;
+  if (workspace != nullptr && workspace_bytes < PKV_STATUS_BYTES) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if (num_seqs == 0 || max_path == 0 || n_layers == 0) return PKV_OK;
+  if (!path || !path_lens || !prefix_lens || !block_table || !k_pages || !v_pages) return PKV_ERR_NULL_ARG;
+  pkv::MovePools pools;
+  for (int32_t l0 = 0; l0 < n_layers; l0 += pkv::kMoveLayers) {  // all layers are checked before anything is launched
+    rc = move_pools(k_pages, v_pages, kv_scales, l0, n_layers - l0 < pkv::kMoveLayers ? n_layers - l0 : pkv::kMoveLayers, &pools);
+    if (rc != PKV_OK) return rc;
+  }
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != PKV_OK) return rc;
+  for (int32_t l0 = 0; l0 < n_layers; l0 += pkv::kMoveLayers) {
+    const int32_t n = n_layers - l0 < pkv::kMoveLayers ? n_layers - l0 : pkv::kMoveLayers;
+    move_pools(k_pages, v_pages, kv_scales, l0, n, &pools);
+    rc = pkv::launch_keep_nodes(pools, n, kv_scales != nullptr, path, path_lens, prefix_lens, block_table, num_seqs, max_path,
+                                max_pages_per_seq, desc->num_kv_heads, desc->head_dim, desc->num_pages,
+                                static_cast<int*>(workspace), reinterpret_cast<cudaStream_t>(stream));
+    if (rc != PKV_OK) return rc;
+  }
+  return PKV_OK;
+}
+
+int pkv_copy_pages(const int32_t* src, const int32_t* dst, int32_t n_pairs, void* const* k_pages, void* const* v_pages,
+                   void* const* kv_scales, int32_t n_layers, const pkv_cache_desc* desc, pkv_stream_t stream,
+                   void* workspace, size_t workspace_bytes) {
+  int rc = check_desc_decode(desc);
+  if (rc != PKV_OK) return rc;
+  if (n_pairs < 0 || n_layers < 0) return PKV_ERR_BAD_SHAPE;
+  if (workspace != nullptr && workspace_bytes < PKV_STATUS_BYTES) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if (n_pairs == 0 || n_layers == 0) return PKV_OK;
+  if (!src || !dst || !k_pages || !v_pages) return PKV_ERR_NULL_ARG;
+  pkv::MovePools pools;
+  for (int32_t l0 = 0; l0 < n_layers; l0 += pkv::kMoveLayers) {
+    rc = move_pools(k_pages, v_pages, kv_scales, l0, n_layers - l0 < pkv::kMoveLayers ? n_layers - l0 : pkv::kMoveLayers, &pools);
+    if (rc != PKV_OK) return rc;
+  }
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != PKV_OK) return rc;
+  for (int32_t l0 = 0; l0 < n_layers; l0 += pkv::kMoveLayers) {
+    const int32_t n = n_layers - l0 < pkv::kMoveLayers ? n_layers - l0 : pkv::kMoveLayers;
+    move_pools(k_pages, v_pages, kv_scales, l0, n, &pools);
+    rc = pkv::launch_copy_pages(pools, n, kv_scales != nullptr, src, dst, n_pairs, desc->num_kv_heads, desc->head_dim,
+                                desc->num_pages, static_cast<int*>(workspace), reinterpret_cast<cudaStream_t>(stream));
+    if (rc != PKV_OK) return rc;
+  }
+  return PKV_OK;
 }
 
 int pkv_rope_table(float* table, int32_t max_pos, int32_t head_dim, double theta, pkv_stream_t stream) {

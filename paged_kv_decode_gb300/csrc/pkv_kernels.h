@@ -84,6 +84,40 @@ struct ExpandArgs {
 };
 int launch_expand_fp8(const ExpandArgs& a, int head_dim, int num_sms, cudaStream_t stream);
 
+// Attention of drafted nodes over the cache (tree_attn.cu): decode's geometries, bf16 or (kv_scales given) 8-bit pools.
+// Workspace = [status header | counters, one per SM | records], of one size for all calls on a device.
+struct TreeAttn {
+  const void* q;  // [total_nodes][hq][D]
+  const void* k_pages;
+  const void* v_pages;
+  const void* kv_scales;
+  const int32_t* block_table;  // [num_seqs][max_pages]
+  const int32_t* prefix_lens;
+  const int32_t* cu_nodes;   // [num_seqs + 1]
+  const int64_t* tree_mask;  // [total_nodes], or nullptr: chains
+  void* out;
+  float scale;
+  int32_t num_seqs, total_nodes, max_pages, max_nodes;
+};
+int tree_max_nodes();
+int tree_max_seqs();
+size_t tree_workspace_bytes(int num_sms);
+int launch_tree_attn(const TreeAttn& t, int num_q_heads, int num_kv_heads, int head_dim, int32_t num_pages, void* workspace,
+                     int num_sms, cudaStream_t stream);
+
+// Rows and pages that move within the cache (cache_moves.cu), in the pools of up to kMoveLayers layers at once.
+constexpr int kMoveLayers = 64;
+struct MovePools {
+  void* k[kMoveLayers];
+  void* v[kMoveLayers];
+  void* scales[kMoveLayers];  // 8-bit pools: their scale bytes; bf16 pools: nullptr
+};
+int launch_copy_pages(const MovePools& pools, int layers, bool fp8, const int32_t* src, const int32_t* dst, int n,
+                      int num_kv_heads, int head_dim, int32_t num_pages, int* status, cudaStream_t stream);
+int launch_keep_nodes(const MovePools& pools, int layers, bool fp8, const int32_t* path, const int32_t* path_lens,
+                      const int32_t* prefix_lens, const int32_t* block_table, int num_seqs, int max_path, int max_pages,
+                      int num_kv_heads, int head_dim, int32_t num_pages, int* status, cudaStream_t stream);
+
 // Rotary-embedding table (rope.cu): fp32 [max_pos][head_dim], row p = cos(p w_i) for i < head_dim / 2,
 // then sin(p w_i), w_i = theta^(-2 i / head_dim), angles in double rounded to float once.
 int launch_rope_table(float* table, int32_t max_pos, int32_t head_dim, double theta, cudaStream_t stream);
