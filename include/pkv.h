@@ -565,11 +565,11 @@ int pkv_mixed_step_attn(const void* q, const void* k_pages, const void* v_pages,
                         void* workspace, size_t workspace_bytes);
 
 /*
- * Workspace bytes the tree attention calls need: the status header, a counter
- * per SM of the current device and two partial records per SM (66,560 bytes
- * each), for items whose keys are cut between CTAs. One size for all calls on a
- * device: tree attention calls of any geometry, sizes and cache type may share a
- * workspace (in stream order). Returns 0 for unsupported arguments.
+ * Workspace bytes the tree attention calls need: the status header, a 16-byte
+ * descriptor per SM of the current device and two partial records per SM (66,560
+ * bytes each), for items whose keys are cut between CTAs. One size for all calls
+ * on a device: tree attention calls of any geometry, sizes and cache type may
+ * share a workspace (in stream order). Returns 0 for unsupported arguments.
  */
 size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t num_seqs, int32_t max_nodes);
 
@@ -607,10 +607,11 @@ size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t num_seqs, in
  *                (PKV_ERR_UNSUPPORTED beyond)
  *  num_seqs:     0 .. 1024 (PKV_ERR_UNSUPPORTED beyond); num_seqs *
  *                max_pages_per_seq * max(num_kv_heads, 8) < 2^31
- *  workspace:    >= pkv_tree_workspace_bytes(...), zeroed once by
- *                pkv_workspace_init (the call leaves its counters at zero). It
- *                serves tree attention calls only
- * A request whose lengths are out of bounds, or that has more than max_nodes
+ *  workspace:    >= pkv_tree_workspace_bytes(...), its status header zeroed once
+ *                by pkv_workspace_init; a call writes what it reads of the rest.
+ *                It serves tree attention calls only
+ * Two kernels where a request's keys may be cut between CTAs (tables of more than
+ * 32 pages), else one. A request whose lengths are out of bounds, or that has more than max_nodes
  * nodes, sets PKV_ERR_OUT_OF_BOUNDS and its rows are not written. A page id
  * outside the pool sets it too; the rows of that request are then undefined.
  * Geometry: head_dim 64 or 128, 1 to 8 query heads per KV head, page_size 16.

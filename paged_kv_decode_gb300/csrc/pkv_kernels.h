@@ -85,7 +85,7 @@ struct ExpandArgs {
 int launch_expand_fp8(const ExpandArgs& a, int head_dim, int num_sms, cudaStream_t stream);
 
 // Attention of drafted nodes over the cache (tree_attn.cu): decode's geometries, bf16 or (kv_scales given) 8-bit pools.
-// Workspace = [status header | counters, one per SM | records], of one size for all calls on a device.
+// Workspace = [status header | a descriptor per SM | records], of one size for all calls on a device.
 struct TreeAttn {
   const void* q;  // [total_nodes][hq][D]
   const void* k_pages;

@@ -18,8 +18,9 @@
 //    the M = 128 rows of the products, node-major, heads of a node side by side
 //    (one 3-D TMA box). Items cost kItemCost + ceil((P + T) / 128) units; every
 //    CTA (one per SM) takes an equal contiguous share of the units, cutting
-//    items; a cut item's partial results go to records, and the CTA that
-//    completes an item merges them in CTA order (the same bits every time).
+//    items; a cut item's partial results go to records, and a second small
+//    kernel joins them in CTA order (the same bits every time). Where all items
+//    are small, or whole items balance as well, none is cut.
 //  * Warp 9 loads Q and the K and V tiles of 128 keys through the block table
 //    into rings. Warp 8 issues S = Q K^T into TMEM and O += P V with P as the
 //    tensor-memory operand. Key tiles alternate between two groups of four
@@ -38,6 +39,7 @@
 //    NaN would reach rows that do not see the node the same way: such elements
 //    are zeroed too, and added back, in the epilogue, to the rows that see them.
 #include <cuda.h>
+#include <float.h>
 #include <math_constants.h>
 
 #include "pkv_device.cuh"
@@ -53,21 +55,21 @@ constexpr int kTrKeys = 128;  // keys of a tile
 constexpr int kTrTilePages = kTrKeys / kPageSize;
 constexpr int kTrMaxNodes = 64;
 constexpr int kTrMaxSeqs = 1024;
-constexpr int kTrMmaWarp = 8, kTrTmaWarp = 9;  // bf16: warp 10 mends the value tiles, 8-bit: the others expand tiles
-constexpr int kTrHalfBytes = kTrKeys * 128;                     // 64 columns of a 128-row bf16 tile
+constexpr int kTrMmaWarp = 8, kTrTmaWarp = 9;
+constexpr int kTrHalfBytes = kTrKeys * 128;                        // 64 columns of a 128-row bf16 tile
 constexpr uint32_t kTrColS = 0, kTrColO = 256, kTrTmemCols = 512;  // S_w, O_w at + 128 w
+constexpr long long kDrainCycles = 20000000LL;                     // 10 ms: far more than a copy in flight takes
 
-// Fixed work of an item (query load, pipeline fill and drain, epilogue) in key tiles, and the least share of a
-// CTA: below it another CTA would cost more in merging than it takes over.
+// Fixed work of an item (query load, pipeline fill and drain, epilogue) in key tiles; and the largest item, in the
+// same units, that is never cut where all items are that small.
 #ifndef PKV_TREE_ITEM_COST
 #define PKV_TREE_ITEM_COST 2
 #endif
-#ifndef PKV_TREE_MIN_SHARE
-#define PKV_TREE_MIN_SHARE 4
+#ifndef PKV_TREE_SMALL_ITEM
+#define PKV_TREE_SMALL_ITEM 6
 #endif
-constexpr long long kDrainCycles = 20000000LL;  // 10 ms: far more than a copy in flight takes
 constexpr int kItemCost = PKV_TREE_ITEM_COST;
-constexpr int kMinShare = PKV_TREE_MIN_SHARE;
+constexpr int kSmallItem = PKV_TREE_SMALL_ITEM;
 
 template <int D, bool kFp8>
 struct TrDim {
@@ -75,15 +77,17 @@ struct TrDim {
   static constexpr int kTile = kHalves * kTrHalfBytes;  // K or V tile (bf16)
   static constexpr int kPage = kPageSize * D * 2;       // a page of it
   static constexpr int kSlots = kFp8 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
+  static constexpr int kPieces = kSlots + 1;  // descriptors of pieces in flight
   static constexpr int kRawTile = kTrKeys * D;  // 8-bit tile
   static constexpr int kRawSlots = kFp8 ? (D == 128 ? 2 : 5) : 0;
   static constexpr int kRawAlloc = kFp8 ? kRawSlots : 1;  // array sizes may not be 0
-  static constexpr int kConvWarps = 4;                    // each for K and for V
-  static constexpr int kMenders = kFp8 ? kConvWarps : 1;  // warps that look for infinities and NaN in value rows
-  // pieces whose masks of such rows are kept: a warp that works on a tile kSlots tiles ahead of the products is at most
-  // kSlots pieces ahead of the one whose epilogue may be reading
-  static constexpr int kBadRing = kSlots + 2;
-  static constexpr int kThreads = (kFp8 ? 10 + 2 * kConvWarps : 11) * 32;
+  static constexpr int kConvWarps = 4;                    // each for K (warps 12 ..) and for V (16 ..)
+  // bf16: 12 warps, warp 10 mends value tiles, 11 idle. 8-bit: 20 warps, 10 and 11 idle; the launch gives each thread 96
+  // registers, the two softmax warpgroups rise to 152, the other three drop to 56.
+  static constexpr int kThreads = (kFp8 ? 12 + 2 * kConvWarps : 12) * 32;
+  static constexpr int kRegsSoftmax = 152, kRegsOther = 56;
+  static_assert(!kFp8 || 256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * 96, "register split");
+  static constexpr int kReaders = 9 + (kFp8 ? 2 * kConvWarps : 1);  // warps that read a piece's descriptor
   // shared memory, from a 1024-byte aligned base
   static constexpr int kOffQ = 0;  // one buffer of up to 128 rows, or two of up to 64
   static constexpr int kOffK = kOffQ + kTile;
@@ -96,20 +100,30 @@ struct TrDim {
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(kTrRows, D, true);  // V is MN-major
 };
 
+// The part of an item that a CTA computes.
+struct TrPiece {
+  int k0, k1;         // key tiles [k0, k1); k1 = 0: the end of the share
+  int P, T;           // prefix and nodes of the request
+  int row0;           // q / out row (node) of the item's first node
+  int node0, rows;    // that node's number in the request; rows of the item
+  int h, n;           // KV head, request
+  int slot;           // record of a cut item's piece: 0 or 1, or -1: the item is whole
+  unsigned long long bad;  // nodes whose value rows in these tiles hold infinities or NaN
+};
+
 template <int D, bool kFp8>
 struct TrCtl {
   using Dm = TrDim<D, kFp8>;
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[Dm::kSlots], k_empty[Dm::kSlots], v_full[Dm::kSlots], v_empty[Dm::kSlots];
   uint64_t s_full[2], p_full[2];
-  uint64_t v_fixed[Dm::kSlots];
+  uint64_t v_fixed[kFp8 ? 1 : Dm::kSlots];
   uint64_t o_done, o_free, drain;
   uint64_t raw_k_full[Dm::kRawAlloc], raw_k_empty[Dm::kRawAlloc], raw_v_full[Dm::kRawAlloc], raw_v_empty[Dm::kRawAlloc];
-  long long lo, hi, units, base;  // the CTA's share, all units, units before request `first`
-  int first, ctas;
+  uint64_t piece_full[Dm::kPieces], piece_empty[Dm::kPieces];
+  TrPiece piece[Dm::kPieces];
   uint32_t tmem;
-  int fail, merge;
-  uint32_t bad[Dm::kBadRing][Dm::kMenders][2];  // nodes whose value rows hold infinities or NaN, of the last pieces
+  int fail;
   float stat[2][2][kTrRows];  // [group][m, l][row]
 };
 
@@ -123,7 +137,12 @@ static_assert(tr_smem_bytes<64, false>() > 120 * 1024 && tr_smem_bytes<64, true>
 static_assert(tr_smem_bytes<64, false>() <= 232448 && tr_smem_bytes<64, true>() <= 232448, "shared memory of an SM");
 
 // A record: O (unnormalised) [D / 4][128 rows] float4, then m and l of the rows. Room of head_dim 128's at any.
-constexpr size_t kTrRecBytes = static_cast<size_t>(kTrRows) * (128 + 2) * 4;
+constexpr size_t kTrRecFloats = static_cast<size_t>(kTrRows) * (128 + 2);
+constexpr size_t kTrRecBytes = kTrRecFloats * 4;
+// The cut item whose first key tile a CTA holds: what the joining kernel reads (rows 0: none).
+struct TrCut {
+  int rows, row0, h, last;  // last: the last CTA with a piece of it; the first is the one that wrote this
+};
 
 struct TrArgs {
   const int* block_table;
@@ -133,11 +152,11 @@ struct TrArgs {
   const uint8_t* k_raw;             // 8-bit pools
   const uint8_t* v_raw;
   const uint8_t* scales;
-  const __nv_bfloat16* v_pages;     // bf16 pool (rows added back)
+  const __nv_bfloat16* v_pages;  // bf16 pool (rows added back)
   __nv_bfloat16* out;
   int* status;
-  int* counters;  // [SMs], zero between calls
-  float* records; // [2 * SMs][kTrRecBytes / 4]
+  TrCut* cuts;     // [ctas], written by every call
+  float* records;  // [2 * ctas][kTrRecFloats]
   int num_seqs, total, max_pages, num_pages, max_nodes;
   int hq, hkv, grp;
   int tile_nodes;  // nodes of an item: 128 / grp
@@ -146,13 +165,6 @@ struct TrArgs {
   int q_bufs;      // query buffers: 2 where two fit
   int ctas;        // CTAs of the grid
   float scale_log2;
-};
-
-struct TrPiece {
-  int n, h, rt;          // request, KV head, tile of nodes
-  int P, T, q0;          // prefix, nodes, first row of the request
-  int nt, k0, k1;        // key tiles of the item; [k0, k1) of them here
-  long long fseg, fend;  // the item's units start at fseg; this piece ends at fend
 };
 
 // Prefix and nodes of request n (0 nodes where the lengths are out of bounds).
@@ -168,49 +180,21 @@ __device__ __forceinline__ void tr_request(const TrArgs& a, int n, int& P, int& 
     T = static_cast<int>(t);
   }
 }
-__device__ __forceinline__ int tr_key_tiles(int P, int T) { return (P + T + kTrKeys - 1) / kTrKeys; }
-__device__ __forceinline__ long long tr_units(const TrArgs& a, int P, int T) {
-  return T == 0 ? 0
-                : static_cast<long long>(a.hkv) * ((T + a.tile_nodes - 1) / a.tile_nodes) *
-                      (kItemCost + tr_key_tiles(P, T));
+__device__ __forceinline__ uint32_t tr_key_tiles(int P, int T) {
+  return (static_cast<uint32_t>(P) + T + kTrKeys - 1) / kTrKeys;
 }
-__device__ __forceinline__ long long tr_share(long long c, long long units, int ctas) { return c * units / ctas; }
-__device__ __forceinline__ int tr_cta_of(long long f, long long units, int ctas) {
-  return static_cast<int>(((f + 1) * ctas + units - 1) / units - 1);
+// Items of a request, units of one of them (whole: items are not cut, each counts 1), and of the request. All units of
+// a call fit 32 bits: at most 2^31 / 8 table entries of 8 heads, a tile for 8 of them, 4 node tiles, and 12 units of
+// fixed work for each of 1024 * 65535 (request, head) pairs.
+__device__ __forceinline__ uint32_t tr_node_tiles(const TrArgs& a, int T) {
+  return (static_cast<uint32_t>(T) + a.tile_nodes - 1) / a.tile_nodes;
 }
-
-// The first piece at or behind unit f of the share that ends at hi. (n, base): a request at or before f's and the
-// units before it; both move on.
-__device__ __forceinline__ bool tr_next(const TrArgs& a, long long f, long long hi, int& n, long long& base, TrPiece& pc) {
-  for (; f < hi; f = pc.fend) {
-    int P, T, q0;
-    long long units;
-    for (;; ++n) {
-      if (n >= a.num_seqs) return false;
-      tr_request(a, n, P, T, q0);
-      units = tr_units(a, P, T);
-      if (f < base + units) break;
-      base += units;
-    }
-    pc.n = n;
-    pc.P = P;
-    pc.T = T;
-    pc.q0 = q0;
-    pc.nt = tr_key_tiles(P, T);
-    const int rts = (T + a.tile_nodes - 1) / a.tile_nodes;
-    const int cost = kItemCost + pc.nt;
-    const long long item = (f - base) / cost;
-    pc.h = static_cast<int>(item / rts);
-    pc.rt = static_cast<int>(item - static_cast<long long>(pc.h) * rts);
-    pc.fseg = base + item * cost;
-    const long long p0 = f - pc.fseg;
-    const long long p1 = p0 + (hi - f) < cost ? p0 + (hi - f) : cost;
-    pc.k0 = static_cast<int>(p0 > kItemCost ? p0 - kItemCost : 0);
-    pc.k1 = static_cast<int>(p1 > kItemCost ? p1 - kItemCost : 0);
-    pc.fend = f + (p1 - p0);
-    if (pc.k1 > pc.k0) return true;
-  }
-  return false;
+__device__ __forceinline__ uint32_t tr_cost(int P, int T, bool whole) { return whole ? 1 : kItemCost + tr_key_tiles(P, T); }
+__device__ __forceinline__ uint32_t tr_share(uint32_t c, uint32_t units, uint32_t ctas) {
+  return static_cast<uint32_t>(static_cast<unsigned long long>(c) * units / ctas);
+}
+__device__ __forceinline__ int tr_cta_of(uint32_t f, uint32_t units, uint32_t ctas) {
+  return static_cast<int>(((f + 1ull) * ctas + units - 1) / units - 1);
 }
 
 template <typename Ctl>
@@ -226,10 +210,8 @@ __device__ __forceinline__ bool tr_wait(uint64_t* bar, uint32_t use, Ctl* ctl, i
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ void tr_group_sync(int id) {  // the eight softmax warps
-  asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory");
-}
-__device__ __forceinline__ bool tr_group_all(int id, bool ok) {  // ... and whether all of them say ok
+// A barrier of the eight softmax warps, and whether all of them say ok.
+__device__ __forceinline__ bool tr_group_all(int id, bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.and.pred q, %1, 256, p;\n\t"
@@ -264,39 +246,57 @@ __device__ __forceinline__ uint32_t tr_v_off(int t, int c) {
   return static_cast<uint32_t>((t >> 4) * (kPageSize * D * 2) + (c >> 3) * 2048 + (t & 15) * 128 + (((c & 7) ^ (t & 7)) << 4));
 }
 
-// n values times inv, rounded to bf16
-template <int N>
-__device__ __forceinline__ void tr_store(__nv_bfloat16* dst, const float (&o)[N], float inv) {
-#pragma unroll
-  for (int q = 0; q < N / 8; ++q) {
-    uint4 x;
-    x.x = pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv);
-    x.y = pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
-    x.z = pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
-    x.w = pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
-    reinterpret_cast<uint4*>(dst)[q] = x;
-  }
-}
-
 // Columns col .. col + 31 of a row: the infinities and NaN of the nodes' value rows in `bad` that this piece holds.
 template <int D, bool kFp8>
-__device__ __noinline__ void tr_add_nonfinite(const TrArgs& a, const TrPiece& pc, unsigned long long bad, int col,
-                                              float (&o)[32]) {
+__device__ __noinline__ float tr_nonfinite(const TrArgs& a, const TrPiece* pc, unsigned long long bad, int col) {
+  float sum = 0.f;
   for (int j = 0; j < kTrMaxNodes; ++j) {
-    const int pos = pc.P + j;
-    if (!(bad >> j & 1ull) || pos < pc.k0 * kTrKeys || pos >= pc.k1 * kTrKeys) continue;
-    const int id = __ldg(a.block_table + static_cast<size_t>(pc.n) * a.max_pages + pos / kPageSize);
+    const int pos = pc->P + j;
+    if (!(bad >> j & 1ull) || pos < pc->k0 * kTrKeys || pos >= pc->k1 * kTrKeys) continue;
+    const int id = __ldg(a.block_table + static_cast<size_t>(pc->n) * a.max_pages + pos / kPageSize);
     if (id < 0 || id >= a.num_pages) continue;
-    const size_t at = ((static_cast<size_t>(id) * a.hkv + pc.h) * kPageSize + pos % kPageSize) * D + col;
-    for (int e = 0; e < 32; ++e) {
-      float x;
-      if constexpr (kFp8)
-        x = (a.v_raw[at + e] & 0x7f) == 0x7f ? CUDART_NAN_F : 0.f;
-      else
-        x = __bfloat162float(a.v_pages[at + e]);
-      if (!(fabsf(x) < CUDART_INF_F)) o[e] += x;
-    }
+    const size_t at = ((static_cast<size_t>(id) * a.hkv + pc->h) * kPageSize + pos % kPageSize) * D + col;
+    float x;
+    if constexpr (kFp8)
+      x = (a.v_raw[at] & 0x7f) == 0x7f ? CUDART_NAN_F : 0.f;
+    else
+      x = __bfloat162float(a.v_pages[at]);
+    if (!(fabsf(x) < CUDART_INF_F)) sum += x;
   }
+  return sum;
+}
+
+// 64 columns of S: two loads, one wait
+__device__ __forceinline__ void tr_load64(uint32_t taddr, uint32_t (&x)[2][32]) {
+  tmem_ld32(taddr, x[0]);
+  tmem_ld32(taddr + 32, x[1]);
+  tmem_ld_wait();
+}
+__device__ __forceinline__ float tr_max64(const uint32_t (&x)[2][32], float2 sc2) {
+  float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float2 t = __fmul2_rn(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc2);
+      m0 = fmaxf(m0, t.x);
+      m1 = fmaxf(m1, t.y);
+    }
+  return fmaxf(m0, m1);
+}
+// P = 2^(s * scale - m) of 64 columns, as bf16 over 32 columns; their sum joins l2
+__device__ __forceinline__ void tr_exp64(uint32_t taddr, const uint32_t (&x)[2][32], float2 sc2, float2 nm2, float2& l2) {
+  uint32_t pk[32];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float2 t = __ffma2_rn(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc2, nm2);
+      const float2 p = make_float2(ex2(t.x), ex2(t.y));
+      l2 = __fadd2_rn(l2, p);
+      pk[c * 16 + (e >> 1)] = pack_bf16x2(p.x, p.y);
+    }
+  tmem_st32(taddr, pk);
 }
 
 template <int D, bool kFp8>
@@ -309,61 +309,23 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + Dm::kOffCtl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  grid_dependency_wait();
-  allow_dependents();
+  // ---- before the wait for the kernel in front: nothing here touches an argument buffer
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle atoms need it; no shared memory precedes the array
+    grid_dependency_wait();
     if (tid == 0) set_status(a.status, PKV_ERR_MISALIGNED);
+    if (tid == 0) a.cuts[blockIdx.x].rows = 0;
     return;
   }
-
-  if (warp == 0) {
-    // all units, this CTA's share and the request that it starts in
-    long long units = 0;
-    for (int b0 = 0; b0 < a.num_seqs; b0 += 32) {
-      int P = 0, T = 0, q0;
-      if (b0 + lane < a.num_seqs) tr_request(a, b0 + lane, P, T, q0);
-      units += tr_units(a, P, T);
+  if (warp == kTrMmaWarp) {
+    tmem_alloc(&ctl->tmem, kTrTmemCols);
+    tmem_relinquish();
+  } else if (warp == kTrTmaWarp && lane == 0) {
+    prefetch_tensormap(&qmap);
+    if constexpr (!kFp8) {
+      prefetch_tensormap(&kmap);
+      prefetch_tensormap(&vmap);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
-    const long long want = (units + kMinShare - 1) / kMinShare;
-    const int ctas = static_cast<int>(want < a.ctas ? want : a.ctas);
-    const int me = blockIdx.x;
-    const long long lo = me < ctas ? tr_share(me, units, ctas) : 0, hi = me < ctas ? tr_share(me + 1, units, ctas) : 0;
-    int first = 0;
-    long long base = 0;
-    if (lo < hi) {
-      long long carry = 0;
-      bool found = false;
-      for (int b0 = 0; b0 < a.num_seqs && !found; b0 += 32) {
-        int P = 0, T = 0, q0;
-        if (b0 + lane < a.num_seqs) tr_request(a, b0 + lane, P, T, q0);
-        const long long u = tr_units(a, P, T);
-        long long x = u;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, carry + x > lo);
-        if (hit != 0) {
-          const int src = __ffs(hit) - 1;
-          first = b0 + src;
-          base = carry + __shfl_sync(0xffffffffu, x - u, src);
-          found = true;
-        }
-        carry += __shfl_sync(0xffffffffu, x, 31);
-      }
-    }
-    if (lane == 0) {
-      ctl->lo = lo;
-      ctl->hi = hi;
-      ctl->units = units;
-      ctl->base = base;
-      ctl->first = first;
-      ctl->ctas = ctas;
-    }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 0 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_full[i], 1);
       mbar_init(&ctl->q_empty[i], 1);
@@ -375,7 +337,7 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       mbar_init(&ctl->v_full[i], kFp8 ? Dm::kConvWarps : 1);
       mbar_init(&ctl->k_empty[i], 1);
       mbar_init(&ctl->v_empty[i], 1);
-      mbar_init(&ctl->v_fixed[i], 1);
+      if (!kFp8) mbar_init(&ctl->v_fixed[kFp8 ? 0 : i], 1);
     }
     for (int i = 0; i < Dm::kRawAlloc; ++i) {
       mbar_init(&ctl->raw_k_full[i], 1);
@@ -383,33 +345,127 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       mbar_init(&ctl->raw_k_empty[i], Dm::kConvWarps);
       mbar_init(&ctl->raw_v_empty[i], Dm::kConvWarps);
     }
+    for (int i = 0; i < Dm::kPieces; ++i) {
+      mbar_init(&ctl->piece_full[i], 1);
+      mbar_init(&ctl->piece_empty[i], Dm::kReaders);
+    }
     mbar_init(&ctl->o_done, 1);
     mbar_init(&ctl->o_free, 8);
     mbar_init(&ctl->drain, 1);
     ctl->fail = 0;
     fence_barrier_init();
   }
-  __syncthreads();
-  const long long lo = ctl->lo, hi = ctl->hi;
-  if (lo >= hi) return;
-  if (warp == kTrMmaWarp) {
-    tmem_alloc(&ctl->tmem, kTrTmemCols);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  grid_dependency_wait();
+  allow_dependents();
 
-  int n = ctl->first;  // every role walks the share's pieces by itself
-  long long base = ctl->base;
-  TrPiece pc;
+  // A role walks the pieces that the loading warp publishes: piece pi in entry pi % kPieces, until one with k1 = 0.
+  auto piece_at = [&](uint32_t pi) -> const TrPiece* {
+    if (!tr_wait(&ctl->piece_full[pi % Dm::kPieces], pi / Dm::kPieces, ctl, a.status)) return nullptr;
+    const TrPiece* pc = &ctl->piece[pi % Dm::kPieces];
+    return *reinterpret_cast<const volatile int*>(&pc->k1) == 0 ? nullptr : pc;
+  };
+  auto piece_done = [&](uint32_t pi) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cta(&ctl->piece_empty[pi % Dm::kPieces]);
+  };
 
   if (warp == kTrTmaWarp) {
-    // ---------------------------------------------------------------- loads
+    if constexpr (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Dm::kRegsOther));
+    // ---------------------------------------------------------------- schedule and loads
+    // all units, cut or whole, the largest item
+    uint32_t units = 0, items = 0, largest = 0;
+    for (int b0 = 0; b0 < a.num_seqs; b0 += 32) {
+      int P = 0, T = 0, q0;
+      if (b0 + lane < a.num_seqs) tr_request(a, b0 + lane, P, T, q0);
+      if (T > 0) {
+        const uint32_t cost = tr_cost(P, T, false), mine = a.hkv * tr_node_tiles(a, T);
+        items += mine;
+        units += mine * cost;
+        largest = max(largest, cost);
+      }
+    }
+    units = __reduce_add_sync(0xffffffffu, units);
+    items = __reduce_add_sync(0xffffffffu, items);
+    largest = __reduce_max_sync(0xffffffffu, largest);
+    // whole items where all are small or where they are as good a balance as shares would be
+    const bool whole = largest <= kSmallItem ||
+                       4ull * largest * ((items + a.ctas - 1) / a.ctas) * a.ctas <= 5ull * units;
+    if (whole) units = items;
+    const uint32_t ctas = min(units, static_cast<uint32_t>(a.ctas)), me = blockIdx.x;
+    uint32_t f = me < ctas ? tr_share(me, units, ctas) : 0;
+    const uint32_t hi = me < ctas ? tr_share(me + 1, units, ctas) : 0;
+    // the request that unit f lies in, and the units before it
+    int n = 0;
+    uint32_t base = 0;
+    if (f < hi) {
+      for (int b0 = 0; b0 < a.num_seqs; b0 += 32) {
+        int P = 0, T = 0, q0;
+        if (b0 + lane < a.num_seqs) tr_request(a, b0 + lane, P, T, q0);
+        const uint32_t u = T > 0 ? a.hkv * tr_node_tiles(a, T) * tr_cost(P, T, whole) : 0;
+        uint32_t x = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, base + x > f);
+        if (hit != 0) {
+          const int src = __ffs(hit) - 1;
+          n = b0 + src;
+          base += __shfl_sync(0xffffffffu, x - u, src);
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
     uint32_t g = 0, pi = 0;
     bool run = true;
-    for (long long f = lo; run && tr_next(a, f, hi, n, base, pc); f = pc.fend, ++pi) {
+    TrCut cut = {0, 0, 0, 0};
+    while (run && f < hi) {
+      int P, T, q0;
+      uint32_t cost, rts;
+      for (;; ++n) {  // requests without nodes are passed over
+        if (n >= a.num_seqs) break;  // (lengths that changed under the call)
+        tr_request(a, n, P, T, q0);
+        rts = tr_node_tiles(a, T);
+        cost = tr_cost(P, T, whole);
+        const uint32_t u = a.hkv * rts * cost;
+        if (f - base < u) break;
+        base += u;
+      }
+      if (n >= a.num_seqs) break;
+      const uint32_t item = (f - base) / cost, fseg = base + item * cost;
+      const int h = static_cast<int>(item / rts), rt = static_cast<int>(item - h * rts);
+      const int nt = static_cast<int>(tr_key_tiles(P, T));
+      const uint32_t p0 = f - fseg, p1 = min(p0 + (hi - f), cost);
+      f += p1 - p0;
+      const int k0 = whole ? 0 : static_cast<int>(p0 > kItemCost ? p0 - kItemCost : 0);
+      const int k1 = whole ? nt : static_cast<int>(p1 > kItemCost ? p1 - kItemCost : 0);
+      if (k1 <= k0) continue;  // a share's end inside an item's fixed units
+      const uint32_t e = pi % Dm::kPieces;
+      if (pi >= Dm::kPieces && !tr_wait(&ctl->piece_empty[e], pi / Dm::kPieces - 1, ctl, a.status)) break;
+      const int node0 = rt * a.tile_nodes, nodes = min(a.tile_nodes, T - node0);
+      if (lane == 0) {
+        TrPiece& pc = ctl->piece[e];
+        pc.k0 = k0;
+        pc.k1 = k1;
+        pc.P = P;
+        pc.T = T;
+        pc.row0 = q0 + node0;
+        pc.node0 = node0;
+        pc.rows = nodes * a.grp;
+        pc.h = h;
+        pc.n = n;
+        pc.slot = k0 == 0 ? (k1 == nt ? -1 : 1) : 0;
+        pc.bad = 0;
+        mbar_arrive_cta(&ctl->piece_full[e]);
+        if (pc.slot == 1)  // the item goes on in later CTAs
+          cut = {nodes * a.grp, q0 + node0, h, tr_cta_of(fseg + kItemCost + nt - 1, units, ctas)};
+      }
       const uint32_t qb = pi % a.q_bufs, quse = pi / a.q_bufs;
       if (quse > 0 && !tr_wait(&ctl->q_empty[qb], quse - 1, ctl, a.status)) break;
       if (lane == 0) {
@@ -417,23 +473,22 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
         mbar_arrive_expect_tx(&ctl->q_full[qb], static_cast<uint32_t>(Dm::kHalves * a.box_rows * 128));
 #pragma unroll
         for (int half = 0; half < Dm::kHalves; ++half)
-          tma_load_3d(dst + half * a.q_rows * 128, &qmap, 64 * half, pc.h * a.grp, pc.q0 + pc.rt * a.tile_nodes,
-                      &ctl->q_full[qb]);
+          tma_load_3d(dst + half * a.q_rows * 128, &qmap, 64 * half, h * a.grp, q0 + node0, &ctl->q_full[qb]);
       }
-      const int n_pages = (pc.P + pc.T + kPageSize - 1) / kPageSize;
-      const int* row = a.block_table + static_cast<size_t>(pc.n) * a.max_pages;
-      int id_next = lane < kTrTilePages && pc.k0 * kTrTilePages + lane < n_pages ? __ldg(row + pc.k0 * kTrTilePages + lane) : 0;
-      for (int k = pc.k0; k < pc.k1; ++k, ++g) {
+      const int n_pages = (P + T + kPageSize - 1) / kPageSize;
+      const int* row = a.block_table + static_cast<size_t>(n) * a.max_pages;
+      int id_next = lane < kTrTilePages && k0 * kTrTilePages + lane < n_pages ? __ldg(row + k0 * kTrTilePages + lane) : 0;
+      for (int k = k0; k < k1; ++k, ++g) {
         const int pg = k * kTrTilePages + lane;
         const int id = id_next;
-        if (k + 1 < pc.k1 && lane < kTrTilePages && pg + kTrTilePages < n_pages) id_next = __ldg(row + pg + kTrTilePages);
+        if (k + 1 < k1 && lane < kTrTilePages && pg + kTrTilePages < n_pages) id_next = __ldg(row + pg + kTrTilePages);
         bool valid = lane < kTrTilePages && pg < n_pages;
         if (valid && (id < 0 || id >= a.num_pages)) {
           set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
           valid = false;
         }
         const uint32_t pages = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, valid)));
-        const long long tile = static_cast<long long>(id) * a.hkv + pc.h;
+        const long long tile = static_cast<long long>(id) * a.hkv + h;
         if constexpr (kFp8) {
           const uint32_t rs = g % Dm::kRawAlloc, use = g / Dm::kRawAlloc;
           const uint32_t bytes = pages * static_cast<uint32_t>(kPageSize * D + kPageSize);
@@ -481,7 +536,17 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
                         &ctl->v_full[st]);
         }
       }
+      ++pi;
     }
+    if (lane == 0) a.cuts[me] = cut;
+    const uint32_t e = pi % Dm::kPieces;
+    if (pi < Dm::kPieces || tr_wait(&ctl->piece_empty[e], pi / Dm::kPieces - 1, ctl, a.status)) {
+      if (lane == 0) {
+        ctl->piece[e].k1 = 0;
+        mbar_arrive_cta(&ctl->piece_full[e]);
+      }
+    }
+    __syncwarp();
     if (*reinterpret_cast<volatile int*>(&ctl->fail) != 0) {
       // the CTA gave up: its copies in flight land before it ends (a wait for one that was never issued runs out)
       constexpr uint32_t kRing = kFp8 ? Dm::kRawAlloc : Dm::kSlots;
@@ -495,35 +560,29 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
         mbar_wait_bounded(&ctl->q_full[i % a.q_bufs], (i / a.q_bufs) & 1u, kDrainCycles);
     }
   } else if (warp == kTrMmaWarp) {
+    if constexpr (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Dm::kRegsOther));
     // ---------------------------------------------------------------- products
     // S of tile g + 2 follows the values of tile g (same group, S and P share their columns); tiles run across pieces
     struct Tile {
-      TrPiece pc;
-      int n, k;
-      long long base;
       uint32_t pi, g;
+      int k, k0, k1;
       bool ok;
     };
-    auto start = [&](Tile& t) {
-      t.n = n;
-      t.base = base;
-      t.pi = t.g = 0;
-      t.ok = tr_next(a, lo, hi, t.n, t.base, t.pc);
-      t.k = t.pc.k0;
-    };
-    auto step = [&](Tile& t) {
-      ++t.g;
-      if (++t.k < t.pc.k1) return;
-      ++t.pi;
-      t.ok = tr_next(a, t.pc.fend, hi, t.n, t.base, t.pc);
-      t.k = t.pc.k0;
+    auto open = [&](Tile& t) {
+      const TrPiece* pc = piece_at(t.pi);
+      t.ok = pc != nullptr;
+      if (t.ok) {
+        t.k = t.k0 = pc->k0;
+        t.k1 = pc->k1;
+      }
     };
     Tile s, v;
-    start(s);
-    start(v);
+    s.pi = s.g = v.pi = v.g = 0;
+    open(s);
+    open(v);
     auto scores = [&]() {
       const uint32_t st = s.g % Dm::kSlots, w = s.g & 1u, qb = s.pi % a.q_bufs;
-      if (s.k == s.pc.k0 && !tr_wait(&ctl->q_full[qb], s.pi / a.q_bufs, ctl, a.status)) return false;
+      if (s.k == s.k0 && !tr_wait(&ctl->q_full[qb], s.pi / a.q_bufs, ctl, a.status)) return false;
       if (!tr_wait(&ctl->k_full[st], s.g / Dm::kSlots, ctl, a.status)) return false;
       tc_fence_after();
       if (lane == 0) {
@@ -535,10 +594,14 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
                  sdesc_sw128(kb + (i >> 2) * kTrHalfBytes + (i & 3) * 32, 16, 1024), Dm::kIdescQK, i > 0 ? 1u : 0u);
         mma_commit(&ctl->s_full[w]);
         mma_commit(&ctl->k_empty[st]);
-        if (s.k == s.pc.k1 - 1) mma_commit(&ctl->q_empty[qb]);
+        if (s.k == s.k1 - 1) mma_commit(&ctl->q_empty[qb]);
       }
       __syncwarp();
-      step(s);
+      ++s.g;
+      if (++s.k == s.k1) {
+        ++s.pi;
+        open(s);
+      }
       return true;
     };
     bool ok = true;
@@ -546,16 +609,16 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       if (ok && s.ok) ok = scores();
     while (ok && v.ok) {
       const uint32_t st = v.g % Dm::kSlots, w = v.g & 1u;
-      const bool first = v.k == v.pc.k0, last = v.k == v.pc.k1 - 1;
+      const bool first = v.k == v.k0, last = v.k == v.k1 - 1;
       // the previous piece's O is read
       if (first && v.pi > 0 && !(ok = tr_wait(&ctl->o_free, v.pi - 1, ctl, a.status))) break;
       if (!(ok = tr_wait(&ctl->v_full[st], v.g / Dm::kSlots, ctl, a.status))) break;
-      if (!kFp8 && !(ok = tr_wait(&ctl->v_fixed[st], v.g / Dm::kSlots, ctl, a.status))) break;
+      if (!kFp8 && !(ok = tr_wait(&ctl->v_fixed[kFp8 ? 0 : st], v.g / Dm::kSlots, ctl, a.status))) break;
       if (!(ok = tr_wait(&ctl->p_full[w], v.g >> 1, ctl, a.status))) break;
       tc_fence_after();
       if (lane == 0) {
         const uint32_t vb = smem_u32(smem + Dm::kOffV + st * Dm::kTile);
-        const bool fresh = v.k - v.pc.k0 < 2;  // the group's first tile of the piece
+        const bool fresh = v.k - v.k0 < 2;  // the group's first tile of the piece
 #pragma unroll
         for (int i = 0; i < kTrTilePages; ++i)
           mma_ts(tmem + kTrColO + 128 * w, tmem + kTrColS + 128 * w + 8 * i, sdesc_sw128(vb + i * Dm::kPage, 2048, 1024),
@@ -564,10 +627,15 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
         if (last) mma_commit(&ctl->o_done);
       }
       __syncwarp();
-      step(v);
+      ++v.g;
+      if (++v.k == v.k1) {
+        piece_done(v.pi);
+        ++v.pi;
+        open(v);
+      }
       if (s.ok) ok = scores();
     }
-    if (!ok) {  // the CTA gave up: the products in flight end before it frees their memory
+    if (*reinterpret_cast<volatile int*>(&ctl->fail) != 0) {  // the CTA gave up: the products in flight end first
       if (lane == 0) {
         mma_commit(&ctl->drain);
         mbar_wait_bounded(&ctl->drain, 0, kDrainCycles);
@@ -575,33 +643,40 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       __syncwarp();
     }
   } else if (warp < 8) {
+    if constexpr (kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Dm::kRegsSoftmax));
     // ---------------------------------------------------------------- softmax and epilogue
     const int w = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int own_node = r / a.grp, own_head = r - own_node * a.grp;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lanes + kTrColS + 128 * w, t_o = tmem + lanes + kTrColO;
+    // what a masked score is set to: -infinity once it is scaled
+    const uint32_t masked = __float_as_uint(a.scale_log2 < 0.f ? CUDART_INF_F : -CUDART_INF_F);
+    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
     uint32_t g = 0, pi = 0;
-    bool ok = true;
-    for (long long f = lo; ok && tr_next(a, f, hi, n, base, pc); f = pc.fend, ++pi) {
-      const int nodes = min(a.tile_nodes, pc.T - pc.rt * a.tile_nodes);
-      const int rows = nodes * a.grp;
-      const bool work = quarter * 32 < rows;
-      const int node = pc.rt * a.tile_nodes + r / a.grp;
+    for (;; ++pi) {
+      const TrPiece* pc = piece_at(pi);
+      // (a warp that gives up in this wait leaves alone: the others' next barrier wants to hear of it, so all agree here)
+      if (!tr_group_all(1, pc != nullptr)) break;
+      const int k0 = pc->k0, k1 = pc->k1, P = pc->P;
+      const bool live = r < pc->rows, work = quarter * 32 < pc->rows;
       unsigned long long mask = 0;
-      if (r < rows) {
-        mask = a.masks != nullptr ? __ldg(a.masks + pc.q0 + node) : (2ull << node) - 1;
-        mask &= pc.T < 64 ? (1ull << pc.T) - 1 : ~0ull;
+      if (live) {
+        const int node = pc->node0 + own_node, T = pc->T;
+        mask = a.masks != nullptr ? __ldg(a.masks + pc->row0 + own_node) : (2ull << node) - 1;
+        mask &= T < 64 ? (1ull << T) - 1 : ~0ull;
       }
       float m = -CUDART_INF_F, l = 0.f;
-      int mine = 0;  // this group's tiles so far
-      for (int k = pc.k0; k < pc.k1; ++k, ++g) {
-        if ((g & 1u) != static_cast<uint32_t>(w)) continue;
-        if (!(ok = tr_wait(&ctl->s_full[w], g >> 1, ctl, a.status))) break;
+      bool fresh = true, ok = true;  // fresh: this group's first tile of the piece
+      const uint32_t g0 = g;
+      for (int k = k0; k < k1; ++k, ++g) {
+        if ((g & 1u) != static_cast<uint32_t>(w) || !ok) continue;
+        if (!(ok = tr_wait(&ctl->s_full[w], g >> 1, ctl, a.status))) continue;
         if (work) {
           tc_fence_after();
-          const bool tail = (k + 1) * kTrKeys > pc.P;  // nodes, or keys past the end, among the tile's
-          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-          if (tail) {
-            const int sh = pc.P - k * kTrKeys;  // keys of the prefix in this tile
+          uint32_t x[2][32];
+          if ((k + 1) * kTrKeys > P) {
+            // nodes, or keys past the end, among the tile's: 128 bits of what the row sees
+            const int sh = P - k * kTrKeys;  // keys of the prefix in this tile
             unsigned long long v0, v1;
             if (sh <= 0) {
               v0 = sh > -64 ? mask >> -sh : 0;
@@ -613,42 +688,38 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
               v0 = ~0ull;
               v1 = sh == 64 ? mask : (mask << (sh - 64)) | ((1ull << (sh - 64)) - 1);
             }
-            vis[0] = static_cast<uint32_t>(v0);
-            vis[1] = static_cast<uint32_t>(v0 >> 32);
-            vis[2] = static_cast<uint32_t>(v1);
-            vis[3] = static_cast<uint32_t>(v1 >> 32);
-          }
-          const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
-          float mx = -CUDART_INF_F;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t vis = static_cast<uint32_t>((c < 2 ? v0 : v1) >> (32 * (c & 1)));
+              tmem_ld32(t_s + 32 * c, x[0]);
+              tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t sr[32];
-            tmem_ld32(t_s + 32 * c, sr);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float2 x = __fmul2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sc2);
-              if (tail) {
-                if (!(vis[c] >> e & 1u)) x.x = -CUDART_INF_F;
-                if (!(vis[c] >> (e + 1) & 1u)) x.y = -CUDART_INF_F;
-              }
-              mx = fmaxf(mx, fmaxf(x.x, x.y));
+              for (int e = 0; e < 32; ++e)
+                if (!(vis >> e & 1u)) x[0][e] = masked;
+              tmem_st32(t_s + 32 * c, x[0]);
             }
+            tmem_st_wait();
           }
+          // the second half for its maximum, the first half, which then stays in registers; the weights of the first
+          // half overwrite its own columns alone
+          tr_load64(t_s + 64, x);
+          float mx = tr_max64(x, sc2);
+          tr_load64(t_s, x);
+          mx = fmaxf(mx, tr_max64(x, sc2));
           // the maximum moves, and O with it, only when it grows by more than 2^8 (weights up to 2^8 are fine)
           const float m_new = fmaxf(m, mx);
           const bool grow = m == -CUDART_INF_F ? m_new != -CUDART_INF_F : m_new - m > 8.f;
           if (__any_sync(0xffffffffu, grow)) {
             const float alpha = !grow ? 1.f : m == -CUDART_INF_F ? 0.f : ex2(m - m_new);
-            if (mine > 0) {
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(t_o + 128 * w + 32 * c, o);
+            if (!fresh) {
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(t_o + 128 * w + 16 * c, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tmem_st32(t_o + 128 * w + 32 * c, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st16(t_o + 128 * w + 16 * c, o);
               }
             }
             if (grow) {
@@ -659,30 +730,14 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
           const float base_m = m == -CUDART_INF_F ? 0.f : -m;
           const float2 nm2 = make_float2(base_m, base_m);
           float2 l2 = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t sr[32], pk[16];
-            tmem_ld32(t_s + 32 * c, sr);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 t =
-                  __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), sc2, nm2);
-              float2 p = make_float2(ex2(t.x), ex2(t.y));
-              if (tail) {
-                if (!(vis[c] >> e & 1u)) p.x = 0.f;
-                if (!(vis[c] >> (e + 1) & 1u)) p.y = 0.f;
-              }
-              l2 = __fadd2_rn(l2, p);
-              pk[e >> 1] = pack_bf16x2(p.x, p.y);
-            }
-            tmem_st16(t_s + 16 * c, pk);  // columns that are read: 16 c + 16 <= 32 c + 32
-          }
+          tr_exp64(t_s, x, sc2, nm2, l2);
+          tr_load64(t_s + 64, x);
+          tr_exp64(t_s + 32, x, sc2, nm2, l2);
           l += l2.x + l2.y;
           tmem_st_wait();
           tc_fence_before();
         }
-        ++mine;
+        fresh = false;
         __syncwarp();
         if (lane == 0) mbar_arrive_cta(&ctl->p_full[w]);
       }
@@ -691,231 +746,189 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       ctl->stat[w][1][r] = l;
       ok = ok && tr_wait(&ctl->o_done, pi, ctl, a.status);
       tc_fence_after();
-      if (!(ok = tr_group_all(1, ok))) break;  // all eight warps go on, or none
+      if (!tr_group_all(2, ok)) break;  // all eight warps go on, or none
       const float m0 = ctl->stat[0][0][r], l0 = ctl->stat[0][1][r], m1 = ctl->stat[1][0][r], l1 = ctl->stat[1][1][r];
       const float M = fmaxf(m0, m1);
       // (a half that saw nothing has sum 0, or NaN where every score was NaN)
       const float a0 = m0 == -CUDART_INF_F ? 0.f : ex2(m0 - M), a1 = m1 == -CUDART_INF_F ? 0.f : ex2(m1 - M);
       const float L = (m0 == -CUDART_INF_F ? l0 : l0 * a0) + (m1 == -CUDART_INF_F ? l1 : l1 * a1);
-      const bool both = pc.k1 - pc.k0 > 1;
-      const uint32_t w0 = (g - static_cast<uint32_t>(pc.k1 - pc.k0)) & 1u;  // the group of the first tile
-      const bool have0 = both || w0 == 0, have1 = both || w0 == 1;
-      unsigned long long bad = 0;
-      if (pc.k1 * kTrKeys > pc.P) {
-#pragma unroll
-        for (int i = 0; i < Dm::kMenders; ++i) {
-          const volatile uint32_t* b = ctl->bad[pi % Dm::kBadRing][i];
-          bad |= static_cast<unsigned long long>(b[1]) << 32 | b[0];
-        }
-        bad &= mask;
-      }
-      const bool whole = pc.k0 == 0 && pc.k1 == pc.nt;
+      const bool have0 = k1 - k0 > 1 || (g0 & 1u) == 0, have1 = k1 - k0 > 1 || (g0 & 1u) == 1;
+      const int slot = pc->slot;
+      const unsigned long long bad = k1 * kTrKeys > P ? mask & *reinterpret_cast<const volatile unsigned long long*>(&pc->bad) : 0;
       const float inv = L == 0.f ? 0.f : 1.f / L;
-      __nv_bfloat16* orow = a.out + (static_cast<size_t>(pc.q0 + node) * a.hq + pc.h * a.grp + r % a.grp) * D + w * (D / 2);
-      // record: slot 1 of the CTA where the item's first key tile is, slot 0 of the others
-      float* rec = a.records + (static_cast<size_t>(blockIdx.x) * 2 + (pc.k0 == 0 ? 1 : 0)) * (kTrRecBytes / 4);
+      const int col0 = w * (D / 2);
+      __nv_bfloat16* orow =
+          a.out + (static_cast<size_t>(pc->row0 + own_node) * a.hq + pc->h * a.grp + own_head) * D + col0;
+      float4* rec = reinterpret_cast<float4*>(a.records + (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * kTrRecFloats);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {  // 16 columns at a time: this code runs once an item, its size is its cost
+        float o[16];
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t x[32], y[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = y[e] = 0u;
+        for (int e = 0; e < 16; ++e) o[e] = 0.f;
         __syncwarp();
         if (work) {
-          const uint32_t at = t_o + w * (D / 2) + 32 * c;
-          if (have0) tmem_ld32(at, x);
-          if (have1) tmem_ld32(at + 128, y);
-          tmem_ld_wait();
-        }
-        if (c == D / 64 - 1) {  // O is read: the next piece's products may overwrite it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cta(&ctl->o_free);
-        }
-        float o[32];
+          uint32_t x[16];
+          const uint32_t at = t_o + col0 + 16 * c;
+          if (have0) {
+            tmem_ld16(at, x);
+            tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = a0 * __uint_as_float(x[e]) + a1 * __uint_as_float(y[e]);
-        if (bad != 0) tr_add_nonfinite<D, kFp8>(a, pc, bad, w * (D / 2) + 32 * c, o);
-        if (r < rows) {
-          if (whole) {
-            tr_store<32>(orow + 32 * c, o, inv);
+            for (int e = 0; e < 16; ++e) o[e] = a0 * __uint_as_float(x[e]);
+          }
+          if (have1) {
+            tmem_ld16(at + 128, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(a1, __uint_as_float(x[e]), o[e]);
+          }
+        }
+        if (bad != 0) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] += tr_nonfinite<D, kFp8>(a, pc, bad, col0 + 16 * c + e);
+        }
+        if (live) {
+          if (slot < 0) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint4 y;
+              y.x = pack_bf16x2(o[8 * q] * inv, o[8 * q + 1] * inv);
+              y.y = pack_bf16x2(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
+              y.z = pack_bf16x2(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
+              y.w = pack_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
+              reinterpret_cast<uint4*>(orow + 16 * c)[q] = y;
+            }
           } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              reinterpret_cast<float4*>(rec)[(w * (D / 8) + c * 8 + q) * kTrRows + r] =
-                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int q = 0; q < 4; ++q)
+              rec[(col0 / 4 + 4 * c + q) * kTrRows + r] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
         }
       }
-      if (!whole) {
-        if (r < rows && w == 0) {
-          rec[128 * kTrRows + r] = M;
-          rec[129 * kTrRows + r] = L;
-        }
-        __threadfence();
+      if (slot >= 0 && live && w == 0) {
+        reinterpret_cast<float*>(rec)[128 * kTrRows + r] = M;
+        reinterpret_cast<float*>(rec)[129 * kTrRows + r] = L;
       }
-      tr_group_sync(2);  // the rows' maxima and sums are read, the record is written
-      if (!whole) {
-        const long long units = ctl->units;
-        const int ctas = ctl->ctas;
-        const int c0 = tr_cta_of(pc.fseg + kItemCost, units, ctas);
-        const int c1 = tr_cta_of(pc.fseg + kItemCost + pc.nt - 1, units, ctas);
-        if (tid == 0) {
-          const int done = atomicAdd(a.counters + c0, 1) == c1 - c0;
-          if (done) a.counters[c0] = 0;
-          __threadfence();
-          *reinterpret_cast<volatile int*>(&ctl->merge) = done;
-        }
-        tr_group_sync(1);
-        if (*reinterpret_cast<volatile int*>(&ctl->merge) != 0 && r < rows) {
-          // all pieces are there: joined in CTA order
-          auto record = [&](int c) { return a.records + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * (kTrRecBytes / 4); };
-          float top = -CUDART_INF_F;
-          for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(record(c) + 128 * kTrRows + r));
-#pragma unroll
-          for (int ch = 0; ch < D / 64; ++ch) {
-            float o[32], sum = 0.f;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
-            for (int c = c0; c <= c1; ++c) {
-              const float* x = record(c);
-              const float mc = __ldcg(x + 128 * kTrRows + r), lc = __ldcg(x + 129 * kTrRows + r);
-              const float wc = mc == -CUDART_INF_F ? 0.f : ex2(mc - top);
-              sum += mc == -CUDART_INF_F ? lc : lc * wc;
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(x) + (w * (D / 8) + ch * 8 + q) * kTrRows + r);
-                o[4 * q] += wc * y.x;
-                o[4 * q + 1] += wc * y.y;
-                o[4 * q + 2] += wc * y.z;
-                o[4 * q + 3] += wc * y.w;
-              }
-            }
-            tr_store<32>(orow + 32 * ch, o, sum == 0.f ? 0.f : 1.f / sum);
-          }
-        }
-      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&ctl->o_free);  // O is read: the next piece's products may overwrite it
+      piece_done(pi);
     }
-  } else if constexpr (!kFp8) {
+  } else if (warp == 10 && !kFp8) {
     // ---------------------------------------------------------------- value tiles with nodes or an end in them
-    uint32_t g = 0, pi = 0;
+    uint32_t g = 0;
     bool ok = true;
-    for (long long f = lo; ok && tr_next(a, f, hi, n, base, pc); f = pc.fend, ++pi) {
+    for (uint32_t pi = 0; ok; ++pi) {
+      const TrPiece* pc = piece_at(pi);
+      if (pc == nullptr) break;
+      const int k0 = pc->k0, k1 = pc->k1, P = pc->P, T = pc->T;
       unsigned long long bad = 0;
-      for (int k = pc.k0; k < pc.k1; ++k, ++g) {
+      for (int k = k0; k < k1 && ok; ++k, ++g) {
         const uint32_t st = g % Dm::kSlots;
         if (!(ok = tr_wait(&ctl->v_full[st], g / Dm::kSlots, ctl, a.status))) break;
-        if ((k + 1) * kTrKeys <= pc.P) {
-          if (lane == 0) mbar_arrive_cta(&ctl->v_fixed[st]);
-          continue;
-        }
-        const int len = pc.P + pc.T - k * kTrKeys;          // rows of the tile before the end
-        const int t0 = max(pc.P - k * kTrKeys, 0);          // its first row behind the prefix
-        unsigned char* vt = smem + Dm::kOffV + st * Dm::kTile;
-        constexpr int kChunks = D / 8;
-        for (int i = t0 * kChunks + lane; i < kTrKeys * kChunks; i += 32) {
-          const int t = i / kChunks;
-          uint4* at = reinterpret_cast<uint4*>(vt + tr_v_off<D>(t, i % kChunks));
-          if (t >= len) {
-            *at = make_uint4(0, 0, 0, 0);
-            continue;
-          }
-          uint4 x = *at;
-          if (nonfinite_bf16x2(x.x) || nonfinite_bf16x2(x.y) || nonfinite_bf16x2(x.z) || nonfinite_bf16x2(x.w)) {
-            *at = make_uint4(finite_bf16x2(x.x), finite_bf16x2(x.y), finite_bf16x2(x.z), finite_bf16x2(x.w));
-            bad |= 1ull << (k * kTrKeys + t - pc.P);
-          }
-        }
-        // (the nodes' bits are complete before the products of the piece's last tile)
-        const uint32_t b0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bad));
-        const uint32_t b1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bad >> 32));
-        if (lane == 0) {
-          ctl->bad[pi % Dm::kBadRing][0][0] = b0;
-          ctl->bad[pi % Dm::kBadRing][0][1] = b1;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cta(&ctl->v_fixed[st]);
-      }
-    }
-  } else {
-    // ---------------------------------------------------------------- 8-bit tiles as bf16 tiles
-    const int kv = (warp - 10) / Dm::kConvWarps;                  // 0: K, 1: V
-    const int sub = ((warp - 10) % Dm::kConvWarps);               // this warp's rows: 32 sub ..
-    uint64_t* full = kv ? ctl->v_full : ctl->k_full;
-    uint64_t* empty = kv ? ctl->v_empty : ctl->k_empty;
-    uint64_t* raw_full = kv ? ctl->raw_v_full : ctl->raw_k_full;
-    uint64_t* raw_empty = kv ? ctl->raw_v_empty : ctl->raw_k_empty;
-    uint32_t g = 0, pi = 0;
-    bool ok = true;
-    for (long long f = lo; ok && tr_next(a, f, hi, n, base, pc); f = pc.fend, ++pi) {
-      unsigned long long bad = 0;
-      for (int k = pc.k0; k < pc.k1; ++k, ++g) {
-        const uint32_t st = g % Dm::kSlots, use = g / Dm::kSlots, rs = g % Dm::kRawAlloc;
-        if (!(ok = tr_wait(&raw_full[rs], g / Dm::kRawAlloc, ctl, a.status))) break;
-        if (use > 0 && !(ok = tr_wait(&empty[st], use - 1, ctl, a.status))) break;
-        const unsigned char* src = smem + (kv ? Dm::kOffRawV : Dm::kOffRawK) + rs * Dm::kRawTile;
-        const unsigned char* sc = smem + Dm::kOffScales + (rs * 2 + kv) * kTrKeys;
-        unsigned char* dst = smem + (kv ? Dm::kOffV : Dm::kOffK) + st * Dm::kTile;
-        const bool tail = kv && (k + 1) * kTrKeys > pc.P;
-        const int len = pc.P + pc.T - k * kTrKeys;
-        // 16 values a lane at a time. Of 8 lanes four take one half of a row, four the other half of the next, so
-        // that the reads (128-byte rows) and the writes (swizzled) both hit every bank once.
-        constexpr int kC = D / 16;  // 16-value chunks of a row
-#pragma unroll 4
-        for (int i = 0; i < 32 * kC / 32; ++i) {
-          int t, c;
-          if constexpr (D == 128) {
-            const int pair = lane >> 3, bit = (lane >> 2) & 1;
-            t = 32 * sub + (i >> 1) * 8 + pair * 2 + bit;
-            c = (lane & 3) + 4 * (bit ^ (i & 1));
-          } else {
-            t = 32 * sub + i * 8 + (lane >> 2);
-            c = lane & 3;
-          }
-          const uint4 x = *reinterpret_cast<const uint4*>(src + t * D + c * 16);
-          const float s = __uint_as_float(static_cast<uint32_t>(sc[t]) << 23);
-          uint32_t y[8];
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t lo2, hi2;
-            e4m3x4_to_f16x4(xs[q], lo2, hi2);
-            const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&lo2));
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hi2));
-            y[2 * q] = pack_bf16x2(u.x * s, u.y * s);
-            y[2 * q + 1] = pack_bf16x2(v.x * s, v.y * s);
-          }
-          if (tail && k * kTrKeys + t >= pc.P) {
-            bool odd = false;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              if (t >= len) y[q] = 0u;
-              if (nonfinite_bf16x2(y[q])) {
-                odd = true;
-                y[q] = finite_bf16x2(y[q]);
-              }
+        if ((k + 1) * kTrKeys > P) {
+          const int len = P + T - k * kTrKeys;     // rows of the tile before the end
+          const int t0 = max(P - k * kTrKeys, 0);  // its first row behind the prefix
+          unsigned char* vt = smem + Dm::kOffV + st * Dm::kTile;
+          constexpr int kChunks = D / 8;
+          for (int i = t0 * kChunks + lane; i < kTrKeys * kChunks; i += 32) {
+            const int t = i / kChunks;
+            uint4* at = reinterpret_cast<uint4*>(vt + tr_v_off<D>(t, i % kChunks));
+            if (t >= len) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
             }
-            if (odd) bad |= 1ull << (k * kTrKeys + t - pc.P);
+            const uint4 x = *at;
+            if (nonfinite_bf16x2(x.x) || nonfinite_bf16x2(x.y) || nonfinite_bf16x2(x.z) || nonfinite_bf16x2(x.w)) {
+              *at = make_uint4(finite_bf16x2(x.x), finite_bf16x2(x.y), finite_bf16x2(x.z), finite_bf16x2(x.w));
+              bad |= 1ull << (k * kTrKeys + t - P);
+            }
           }
-          const uint32_t o0 = kv ? tr_v_off<D>(t, 2 * c) : tr_k_off(t, 2 * c);
-          const uint32_t o1 = kv ? tr_v_off<D>(t, 2 * c + 1) : tr_k_off(t, 2 * c + 1);
-          *reinterpret_cast<uint4*>(dst + o0) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(dst + o1) = make_uint4(y[4], y[5], y[6], y[7]);
+          if (bad != 0) atomicOr(&ctl->piece[pi % Dm::kPieces].bad, bad);
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        if (tail) {  // (the nodes' bits are complete before the products of the piece's last tile)
-          const uint32_t b0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bad));
-          const uint32_t b1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bad >> 32));
+        if (lane == 0) mbar_arrive_cta(&ctl->v_fixed[kFp8 ? 0 : st]);
+      }
+      piece_done(pi);
+    }
+  } else if (kFp8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Dm::kRegsOther));
+    if (warp >= 12) {
+      // ---------------------------------------------------------------- 8-bit tiles as bf16 tiles
+      const int kv = (warp - 12) / Dm::kConvWarps;   // 0: K, 1: V
+      const int sub = (warp - 12) % Dm::kConvWarps;  // this warp's rows: 32 sub ..
+      uint64_t* full = kv ? ctl->v_full : ctl->k_full;
+      uint64_t* empty = kv ? ctl->v_empty : ctl->k_empty;
+      uint64_t* raw_full = kv ? ctl->raw_v_full : ctl->raw_k_full;
+      uint64_t* raw_empty = kv ? ctl->raw_v_empty : ctl->raw_k_empty;
+      uint32_t g = 0;
+      bool ok = true;
+      for (uint32_t pi = 0; ok; ++pi) {
+        const TrPiece* pc = piece_at(pi);
+        if (pc == nullptr) break;
+        const int k0 = pc->k0, k1 = pc->k1, P = pc->P, T = pc->T;
+        for (int k = k0; k < k1 && ok; ++k, ++g) {
+          const uint32_t st = g % Dm::kSlots, use = g / Dm::kSlots, rs = g % Dm::kRawAlloc;
+          if (!(ok = tr_wait(&raw_full[rs], g / Dm::kRawAlloc, ctl, a.status))) break;
+          if (use > 0 && !(ok = tr_wait(&empty[st], use - 1, ctl, a.status))) break;
+          const unsigned char* src = smem + (kv ? Dm::kOffRawV : Dm::kOffRawK) + rs * Dm::kRawTile;
+          const unsigned char* sc = smem + Dm::kOffScales + (rs * 2 + kv) * kTrKeys;
+          unsigned char* dst = smem + (kv ? Dm::kOffV : Dm::kOffK) + st * Dm::kTile;
+          const bool tail = kv && (k + 1) * kTrKeys > P;
+          const int len = P + T - k * kTrKeys;
+          // 16 values a lane at a time. Of 8 lanes four take one half of a row, four the other half of the next, so
+          // that the reads (128-byte rows) and the writes (swizzled) both hit every bank once.
+          constexpr int kSteps = D / 16;
+#pragma unroll 2
+          for (int i = 0; i < kSteps; ++i) {
+            int t, c;
+            if constexpr (D == 128) {
+              const int bit = (lane >> 2) & 1;
+              t = 32 * sub + (i >> 1) * 8 + (lane >> 3) * 2 + bit;
+              c = (lane & 3) + 4 * (bit ^ (i & 1));
+            } else {
+              t = 32 * sub + i * 8 + (lane >> 2);
+              c = lane & 3;
+            }
+            const uint4 x = *reinterpret_cast<const uint4*>(src + t * D + c * 16);
+            const float s = __uint_as_float(static_cast<uint32_t>(sc[t]) << 23);
+            const float2 s2 = make_float2(s, s);
+            uint32_t y[8];
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t lo2, hi2;
+              e4m3x4_to_f16x4(xs[q], lo2, hi2);
+              const float2 u = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&lo2)), s2);
+              const float2 v = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&hi2)), s2);
+              y[2 * q] = pack_bf16x2(u.x, u.y);
+              y[2 * q + 1] = pack_bf16x2(v.x, v.y);
+            }
+            if (tail && k * kTrKeys + t >= P) {
+              bool odd = false;
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                if (t >= len) y[q] = 0u;
+                if (nonfinite_bf16x2(y[q])) {
+                  odd = true;
+                  y[q] = finite_bf16x2(y[q]);
+                }
+              }
+              if (odd) atomicOr(&ctl->piece[pi % Dm::kPieces].bad, 1ull << (k * kTrKeys + t - P));
+            }
+            const uint32_t o0 = kv ? tr_v_off<D>(t, 2 * c) : tr_k_off(t, 2 * c);
+            const uint32_t o1 = kv ? tr_v_off<D>(t, 2 * c + 1) : tr_k_off(t, 2 * c + 1);
+            *reinterpret_cast<uint4*>(dst + o0) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + o1) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
           if (lane == 0) {
-            ctl->bad[pi % Dm::kBadRing][sub][0] = b0;
-            ctl->bad[pi % Dm::kBadRing][sub][1] = b1;
+            mbar_arrive_cta(&raw_empty[rs]);
+            mbar_arrive_cta(&full[st]);
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cta(&raw_empty[rs]);
-          mbar_arrive_cta(&full[st]);
-        }
+        piece_done(pi);
       }
     }
   }
@@ -925,6 +938,45 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kTrMmaWarp) tmem_dealloc(tmem, kTrTmemCols);
+}
+
+// The records of cut items, joined in CTA order: o = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M). CTA (c, quarter,
+// part) takes 32 rows of the item that begins in CTA c of the attention kernel, 8 groups of 4 columns of them, a warp
+// each, a thread to a row. A kernel of its own: joined by the last CTA of an item instead, the 20 records of a long
+// request's item took that one SM 17 us, and counting the pieces 1 us everywhere.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TrArgs a) {
+  grid_dependency_wait();
+  allow_dependents();
+  const int c0 = blockIdx.x, quarter = blockIdx.y & 3, part = blockIdx.y >> 2;
+  const int4 w = __ldcg(reinterpret_cast<const int4*>(a.cuts + c0));
+  const int rows = w.x, row0 = w.y, h = w.z, c1 = w.w;
+  const int r = quarter * 32 + (threadIdx.x & 31), q = part * 8 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  // the first piece is in slot 1 of its CTA, the others in slot 0 of theirs
+  const float* first = a.records + (static_cast<size_t>(c0) * 2 + 1) * kTrRecFloats;
+  auto record = [&](int c) { return c == c0 ? first : a.records + static_cast<size_t>(c) * 2 * kTrRecFloats; };
+  float M = -CUDART_INF_F, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int c = c0; c <= c1; ++c) {
+    const float* x = record(c);
+    const float m = __ldcg(x + 128 * kTrRows + r), l = __ldcg(x + 129 * kTrRows + r);
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(x) + q * kTrRows + r);
+    const float top = fmaxf(M, m);
+    const float old = M == -CUDART_INF_F ? 0.f : ex2(M - top), now = m == -CUDART_INF_F ? 0.f : ex2(m - top);
+    L = (M == -CUDART_INF_F ? L : L * old) + (m == -CUDART_INF_F ? l : l * now);
+    o.x = o.x * old + y.x * now;
+    o.y = o.y * old + y.y * now;
+    o.z = o.z * old + y.z * now;
+    o.w = o.w * old + y.w * now;
+    M = top;
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int node = r / a.grp;
+  __nv_bfloat16* dst = a.out + (static_cast<size_t>(row0 + node) * a.hq + h * a.grp + r - node * a.grp) * D + 4 * q;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -943,9 +995,8 @@ EncodeTiledFn encoder() {
   return fn;
 }
 
-// Counters (one per CTA: the CTA that holds an item's first key tile, where that item is cut) in a block of fixed
-// size, then the records: what a call leaves in the records never lies where another one looks for zeros.
-size_t counter_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * 4 + 255) / 256 * 256; }
+// The cut items' descriptors, one per CTA, in front of the records. Every call writes what it reads of both.
+size_t cut_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * sizeof(TrCut) + 255) / 256 * 256; }
 
 template <int D, bool kFp8>
 int launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap, const TrArgs& a, cudaStream_t stream) {
@@ -958,8 +1009,13 @@ int launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& 
       return PKV_ERR_CUDA;
     if (dev < 64) attr_set[dev] = true;
   }
-  return launch_pdl(tree_attn_kernel<D, kFp8>, dim3(static_cast<unsigned>(a.ctas)), dim3(TrDim<D, kFp8>::kThreads),
-                    tr_smem_bytes<D, kFp8>(), stream, qmap, kmap, vmap, a) == cudaSuccess
+  if (launch_pdl(tree_attn_kernel<D, kFp8>, dim3(static_cast<unsigned>(a.ctas)), dim3(TrDim<D, kFp8>::kThreads),
+                 tr_smem_bytes<D, kFp8>(), stream, qmap, kmap, vmap, a) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  // a table so narrow that no item can be cut needs no joining
+  if (kItemCost + (static_cast<long long>(a.max_pages) + kTrTilePages - 1) / kTrTilePages <= kSmallItem) return PKV_OK;
+  return launch_pdl(tree_join_kernel<D>, dim3(static_cast<unsigned>(a.ctas), 4 * (D / 32)), dim3(kJoinThreads), 0, stream, a) ==
+                 cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
 }
@@ -969,7 +1025,7 @@ int launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& 
 int tree_max_nodes() { return kTrMaxNodes; }
 int tree_max_seqs() { return kTrMaxSeqs; }
 
-size_t tree_workspace_bytes(int num_sms) { return PKV_STATUS_BYTES + counter_bytes(num_sms) + 2 * num_sms * kTrRecBytes; }
+size_t tree_workspace_bytes(int num_sms) { return PKV_STATUS_BYTES + cut_bytes(num_sms) + 2 * num_sms * kTrRecBytes; }
 
 int launch_tree_attn(const TreeAttn& t, int num_q_heads, int num_kv_heads, int head_dim, int32_t num_pages, void* workspace,
                      int num_sms, cudaStream_t stream) {
@@ -989,8 +1045,8 @@ int launch_tree_attn(const TreeAttn& t, int num_q_heads, int num_kv_heads, int h
   a.out = static_cast<__nv_bfloat16*>(t.out);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.status = reinterpret_cast<int*>(ws);
-  a.counters = reinterpret_cast<int*>(ws + PKV_STATUS_BYTES);
-  a.records = reinterpret_cast<float*>(ws + PKV_STATUS_BYTES + counter_bytes(num_sms));
+  a.cuts = reinterpret_cast<TrCut*>(ws + PKV_STATUS_BYTES);
+  a.records = reinterpret_cast<float*>(ws + PKV_STATUS_BYTES + cut_bytes(num_sms));
   a.num_seqs = t.num_seqs;
   a.total = t.total_nodes;
   a.max_pages = t.max_pages;
@@ -1005,6 +1061,7 @@ int launch_tree_attn(const TreeAttn& t, int num_q_heads, int num_kv_heads, int h
   a.q_bufs = a.q_rows <= kTrRows / 2 ? 2 : 1;
   a.ctas = num_sms;
   a.scale_log2 = t.scale * kLog2e;
+  if (a.scale_log2 == 0.f) a.scale_log2 = FLT_MIN;  // a masked score, infinity, times 0 would be NaN
 
   const cuuint64_t hd = static_cast<cuuint64_t>(head_dim);
   const cuuint32_t ones[4] = {1, 1, 1, 1};

@@ -68,33 +68,33 @@ def test_host_argument_checks(lib, fp8):
         assert lib.pkv_tree_workspace_bytes(*bad) == 0
 
 
-def _pieces(items, grid, cost=2, least=4):
-    """The schedule of tree_attn.cu, restated: (cta, item, k0, k1) of every piece, for items of so many key tiles."""
-    units = sum(cost + n for n in items)
-    ctas = min(grid, -(-units // least))
-    starts = np.concatenate([[0], np.cumsum([cost + n for n in items])])
+def _pieces(items, grid, cost=2, small=6):
+    """The schedule of tree_attn.cu, restated: (cta, item, k0, k1) of every piece, for items of so many key tiles, and for
+    each item the last CTA with a piece of it."""
+    units, largest = sum(cost + n for n in items), cost + max(items)
+    whole = largest <= small or 4 * largest * -(-len(items) // grid) * grid <= 5 * units
+    size = [1 if whole else cost + n for n in items]
+    units = sum(size)
+    ctas = min(grid, units)
+    starts = np.concatenate([[0], np.cumsum(size)])
     got = []
     for c in range(ctas):
         lo, hi = c * units // ctas, (c + 1) * units // ctas
         for i, n in enumerate(items):
             a, b = max(lo, int(starts[i])), min(hi, int(starts[i + 1]))
-            k0, k1 = max(0, a - int(starts[i]) - cost), max(0, b - int(starts[i]) - cost)
+            k0, k1 = (0, n) if whole else (max(0, a - int(starts[i]) - cost), max(0, b - int(starts[i]) - cost))
             if a < b and k1 > k0:
                 got.append((c, i, k0, k1))
-    cta_of = lambda f: ((f + 1) * ctas + units - 1) // units - 1  # noqa: E731
-    first = [cta_of(int(starts[i]) + cost) for i in range(len(items))]
-    last = [cta_of(int(starts[i + 1]) - 1) for i in range(len(items))]
-    return got, first, last
+    return got, [((int(starts[i + 1]) - 1 + 1) * ctas + units - 1) // units - 1 for i in range(len(items))]
 
 
 @pytest.mark.parametrize("grid", [1, 7, 152])
 def test_shares_cover_the_items_and_records_are_distinct(grid):
     rng = np.random.default_rng(3)
-    for items in ([1], [1] * 300, [313], [5, 1, 400, 2, 2, 60], rng.integers(1, 30, size=128).tolist(), [63] * 8, [4000] * 2):
-        pieces, first, last = _pieces(items, grid)
-        seen = {}
-        slots = set()
-        counters = set()
+    for items in ([1], [1] * 300, [313], [5, 1, 400, 2, 2, 60], rng.integers(1, 30, size=128).tolist(), [63] * 8, [4000] * 2,
+                  [16] * 152, [4, 1, 3] * 90, [5] * 9):
+        pieces, last = _pieces(items, grid)
+        seen, slots, cuts = {}, set(), set()
         for c, i, k0, k1 in pieces:
             seen.setdefault(i, []).append((k0, k1, c))
             if (k0, k1) != (0, items[i]):  # a record: its slot is its own
@@ -104,11 +104,10 @@ def test_shares_cover_the_items_and_records_are_distinct(grid):
         for i, n in enumerate(items):
             parts = sorted(seen[i])
             assert parts[0][0] == 0 and parts[-1][1] == n and all(a[1] == b[0] for a, b in zip(parts, parts[1:]))
-            # the CTAs that the kernel counts and merges: consecutive, each with a piece
-            assert [c for _, _, c in parts] == list(range(first[i], last[i] + 1))
-            if len(parts) > 1:  # and the cut item's counter is its own
-                assert first[i] not in counters
-                counters.add(first[i])
+            if len(parts) > 1:  # the CTAs that are joined: consecutive, each with a piece; one descriptor for each cut item
+                assert [c for _, _, c in parts] == list(range(parts[0][2], last[i] + 1))
+                assert parts[0][2] not in cuts
+                cuts.add(parts[0][2])
 
 
 # ---------------------------------------------------------------------------------------------- GPU
@@ -260,8 +259,7 @@ def test_cut_items_twice_on_one_workspace(cuda_device, case, fp8):
     c = Tree(12, GEOMS[geom], reqs, cuda_device, fp8=fp8)
     first = c.step().clone()
     c.check()
-    c.ws.tensor[4096:] = 0xFF  # what calls leave in the records does not matter (NaN here); the counters lie before
+    c.ws.tensor[256:] = 0xFF  # what calls leave behind the status header does not matter (NaN here)
     c.out.fill_(7.0)
     assert torch.equal(c.step().view(torch.int16), first.view(torch.int16))
-    torch.cuda.synchronize()
-    assert torch.count_nonzero(c.ws.tensor[:1024]).item() == 0  # status and counters are as they were
+    c.check()
