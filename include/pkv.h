@@ -566,7 +566,7 @@ int pkv_mixed_step_attn(const void* q, const void* k_pages, const void* v_pages,
 
 /*
  * Workspace bytes the tree attention calls need: the status header, a 16-byte
- * descriptor per SM of the current device and two partial records per SM (66,560
+ * descriptor per SM of the current device and two partial records per SM (67,584
  * bytes each), for items whose keys are cut between CTAs. One size for all calls
  * on a device: tree attention calls of any geometry, sizes and cache type may
  * share a workspace (in stream order). Returns 0 for unsupported arguments.

@@ -21,8 +21,8 @@
 //    items; a cut item's partial results go to records, and a second small
 //    kernel joins them in CTA order (the same bits every time). Where all items
 //    are small, or whole items balance as well, none is cut.
-//  * Warp 9 loads Q and the K and V tiles of 128 keys through the block table
-//    into rings. Warp 8 issues S = Q K^T into TMEM and O += P V with P as the
+//  * Warp 9 plans the CTA's pieces and loads Q and the K and V tiles of 128 keys
+//    through the block table into rings. Warp 8 issues S = Q K^T into TMEM and O += P V with P as the
 //    tensor-memory operand. Key tiles alternate between two groups of four
 //    softmax warps, each with its own S, P, O, maximum and sum: one group's
 //    exponentials run beside the other's products. The two halves of a row are
@@ -55,7 +55,7 @@ constexpr int kTrKeys = 128;  // keys of a tile
 constexpr int kTrTilePages = kTrKeys / kPageSize;
 constexpr int kTrMaxNodes = 64;
 constexpr int kTrMaxSeqs = 1024;
-constexpr int kTrMmaWarp = 8, kTrTmaWarp = 9;
+constexpr int kTrMmaWarp = 8, kTrTmaWarp = 9, kTrMendWarp = 10;
 constexpr int kTrHalfBytes = kTrKeys * 128;                        // 64 columns of a 128-row bf16 tile
 constexpr uint32_t kTrColS = 0, kTrColO = 256, kTrTmemCols = 512;  // S_w, O_w at + 128 w
 constexpr long long kDrainCycles = 20000000LL;                     // 10 ms: far more than a copy in flight takes
@@ -82,8 +82,8 @@ struct TrDim {
   static constexpr int kRawSlots = kFp8 ? (D == 128 ? 2 : 5) : 0;
   static constexpr int kRawAlloc = kFp8 ? kRawSlots : 1;  // array sizes may not be 0
   static constexpr int kConvWarps = 4;                    // each for K (warps 12 ..) and for V (16 ..)
-  // bf16: 12 warps, warp 10 mends value tiles, 11 idle. 8-bit: 20 warps, 10 and 11 idle; the launch gives each thread 96
-  // registers, the two softmax warpgroups rise to 152, the other three drop to 56.
+  // bf16: 12 warps, 11 idle. 8-bit: 20 warps, 10 and 11 idle; the launch gives each thread 96 registers, the two softmax
+  // warpgroups rise to 152, the other three drop to 56.
   static constexpr int kThreads = (kFp8 ? 12 + 2 * kConvWarps : 12) * 32;
   static constexpr int kRegsSoftmax = 152, kRegsOther = 56;
   static_assert(!kFp8 || 256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * 96, "register split");
@@ -136,8 +136,8 @@ static_assert(tr_smem_bytes<64, false>() > 120 * 1024 && tr_smem_bytes<64, true>
               "one CTA per SM: each holds all TMEM columns");
 static_assert(tr_smem_bytes<64, false>() <= 232448 && tr_smem_bytes<64, true>() <= 232448, "shared memory of an SM");
 
-// A record: O (unnormalised) [D / 4][128 rows] float4, then m and l of the rows. Room of head_dim 128's at any.
-constexpr size_t kTrRecFloats = static_cast<size_t>(kTrRows) * (128 + 2);
+// A record: float4 [D / 4 + 1][128 rows]: (m, l, 0, 0) of the rows, then O (unnormalised). Room of head_dim 128's at any.
+constexpr size_t kTrRecFloats = static_cast<size_t>(kTrRows) * (128 + 4);
 constexpr size_t kTrRecBytes = kTrRecFloats * 4;
 // The cut item whose first key tile a CTA holds: what the joining kernel reads (rows 0: none).
 struct TrCut {
@@ -160,6 +160,7 @@ struct TrArgs {
   int num_seqs, total, max_pages, num_pages, max_nodes;
   int hq, hkv, grp;
   int tile_nodes;  // nodes of an item: 128 / grp
+  uint32_t node_magic;  // 2^32 / tile_nodes, rounded up: x * node_magic >> 32 = x / tile_nodes for the x < 2^15 here
   int box_rows;    // rows of the query box: grp * min(tile_nodes, max_nodes)
   int q_rows;      // ... rounded up to whole swizzle atoms of 8 rows
   int q_bufs;      // query buffers: 2 where two fit
@@ -186,16 +187,10 @@ __device__ __forceinline__ uint32_t tr_key_tiles(int P, int T) {
 // Items of a request, units of one of them (whole: items are not cut, each counts 1), and of the request. All units of
 // a call fit 32 bits: at most 2^31 / 8 table entries of 8 heads, a tile for 8 of them, 4 node tiles, and 12 units of
 // fixed work for each of 1024 * 65535 (request, head) pairs.
-__device__ __forceinline__ uint32_t tr_node_tiles(const TrArgs& a, int T) {
-  return (static_cast<uint32_t>(T) + a.tile_nodes - 1) / a.tile_nodes;
+__device__ __forceinline__ uint32_t tr_node_tiles(const TrArgs& a, int T) {  // T / tile_nodes, rounded up
+  return __umulhi(static_cast<uint32_t>(T) + a.tile_nodes - 1, a.node_magic);
 }
 __device__ __forceinline__ uint32_t tr_cost(int P, int T, bool whole) { return whole ? 1 : kItemCost + tr_key_tiles(P, T); }
-__device__ __forceinline__ uint32_t tr_share(uint32_t c, uint32_t units, uint32_t ctas) {
-  return static_cast<uint32_t>(static_cast<unsigned long long>(c) * units / ctas);
-}
-__device__ __forceinline__ int tr_cta_of(uint32_t f, uint32_t units, uint32_t ctas) {
-  return static_cast<int>(((f + 1ull) * ctas + units - 1) / units - 1);
-}
 
 template <typename Ctl>
 __device__ __forceinline__ bool tr_wait(uint64_t* bar, uint32_t use, Ctl* ctl, int* status) {
@@ -313,7 +308,6 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzle atoms need it; no shared memory precedes the array
     grid_dependency_wait();
     if (tid == 0) set_status(a.status, PKV_ERR_MISALIGNED);
-    if (tid == 0) a.cuts[blockIdx.x].rows = 0;
     return;
   }
   if (warp == kTrMmaWarp) {
@@ -376,13 +370,21 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
   if (warp == kTrTmaWarp) {
     if constexpr (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Dm::kRegsOther));
     // ---------------------------------------------------------------- schedule and loads
+    // (this is on the way to the first load: few divisions, some 130 cycles each, and the lengths are read once)
+    // lane i holds request 32 blk + i
+    int blk = -1, lane_P = 0, lane_T = 0, lane_q0 = 0;
+    auto load_block = [&](int b) {
+      if (b == blk) return;
+      blk = b;
+      lane_T = 0;
+      if (32 * b + lane < a.num_seqs) tr_request(a, 32 * b + lane, lane_P, lane_T, lane_q0);
+    };
     // all units, cut or whole, the largest item
     uint32_t units = 0, items = 0, largest = 0;
-    for (int b0 = 0; b0 < a.num_seqs; b0 += 32) {
-      int P = 0, T = 0, q0;
-      if (b0 + lane < a.num_seqs) tr_request(a, b0 + lane, P, T, q0);
-      if (T > 0) {
-        const uint32_t cost = tr_cost(P, T, false), mine = a.hkv * tr_node_tiles(a, T);
+    for (int b = (a.num_seqs - 1) / 32; b >= 0; --b) {  // (the first block last: the search below begins there)
+      load_block(b);
+      if (lane_T > 0) {
+        const uint32_t cost = tr_cost(lane_P, lane_T, false), mine = a.hkv * tr_node_tiles(a, lane_T);
         items += mine;
         units += mine * cost;
         largest = max(largest, cost);
@@ -391,65 +393,83 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
     units = __reduce_add_sync(0xffffffffu, units);
     items = __reduce_add_sync(0xffffffffu, items);
     largest = __reduce_max_sync(0xffffffffu, largest);
-    // whole items where all are small or where they are as good a balance as shares would be
+    // whole items where all are small, or where the CTAs' largest number of them is as good a balance as shares would be
+    // (within a quarter; every CTA computes the same floats)
+    const float rounds = ceilf(static_cast<float>(items) / static_cast<float>(a.ctas));
     const bool whole = largest <= kSmallItem ||
-                       4ull * largest * ((items + a.ctas - 1) / a.ctas) * a.ctas <= 5ull * units;
+                       4.f * static_cast<float>(largest) * rounds * static_cast<float>(a.ctas) <= 5.f * static_cast<float>(units);
     if (whole) units = items;
+    // CTA c's share: units / ctas of them, one more for the first units % ctas
     const uint32_t ctas = min(units, static_cast<uint32_t>(a.ctas)), me = blockIdx.x;
-    uint32_t f = me < ctas ? tr_share(me, units, ctas) : 0;
-    const uint32_t hi = me < ctas ? tr_share(me + 1, units, ctas) : 0;
+    const uint32_t quota = ctas > 0 ? units / ctas : 0, more = units - quota * ctas;
+    uint32_t f = me < ctas ? me * quota + min(me, more) : 0;
+    const uint32_t hi = me < ctas ? f + quota + (me < more ? 1 : 0) : 0;
+    auto cta_of = [&](uint32_t u) {  // the CTA whose share has unit u
+      const uint32_t split = more * (quota + 1);
+      return static_cast<int>(u < split ? u / (quota + 1) : more + (u - split) / quota);
+    };
     // the request that unit f lies in, and the units before it
     int n = 0;
     uint32_t base = 0;
-    if (f < hi) {
-      for (int b0 = 0; b0 < a.num_seqs; b0 += 32) {
-        int P = 0, T = 0, q0;
-        if (b0 + lane < a.num_seqs) tr_request(a, b0 + lane, P, T, q0);
-        const uint32_t u = T > 0 ? a.hkv * tr_node_tiles(a, T) * tr_cost(P, T, whole) : 0;
-        uint32_t x = u;
+    for (int b = 0; f < hi && 32 * b < a.num_seqs; ++b) {
+      load_block(b);
+      const uint32_t u = lane_T > 0 ? a.hkv * tr_node_tiles(a, lane_T) * tr_cost(lane_P, lane_T, whole) : 0;
+      uint32_t x = u;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, base + x > f);
-        if (hit != 0) {
-          const int src = __ffs(hit) - 1;
-          n = b0 + src;
-          base += __shfl_sync(0xffffffffu, x - u, src);
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, x, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
       }
+      const unsigned hit = __ballot_sync(0xffffffffu, base + x > f);
+      if (hit != 0) {
+        const int src = __ffs(hit) - 1;
+        n = 32 * b + src;
+        base += __shfl_sync(0xffffffffu, x - u, src);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, x, 31);
     }
+    constexpr uint32_t kRing = kFp8 ? Dm::kRawAlloc : Dm::kSlots;  // tiles that the loads may be ahead
     uint32_t g = 0, pi = 0;
     bool run = true;
     TrCut cut = {0, 0, 0, 0};
     while (run && f < hi) {
-      int P, T, q0;
-      uint32_t cost, rts;
-      for (;; ++n) {  // requests without nodes are passed over
-        if (n >= a.num_seqs) break;  // (lengths that changed under the call)
-        tr_request(a, n, P, T, q0);
+      int P = 0, T = 0, q0 = 0;
+      uint32_t cost = 1, rts = 1;
+      for (; n < a.num_seqs; ++n) {  // requests without nodes are passed over
+        load_block(n / 32);
+        P = __shfl_sync(0xffffffffu, lane_P, n % 32);
+        T = __shfl_sync(0xffffffffu, lane_T, n % 32);
+        q0 = __shfl_sync(0xffffffffu, lane_q0, n % 32);
         rts = tr_node_tiles(a, T);
         cost = tr_cost(P, T, whole);
         const uint32_t u = a.hkv * rts * cost;
         if (f - base < u) break;
         base += u;
       }
-      if (n >= a.num_seqs) break;
-      const uint32_t item = (f - base) / cost, fseg = base + item * cost;
-      const int h = static_cast<int>(item / rts), rt = static_cast<int>(item - h * rts);
+      if (n >= a.num_seqs) break;  // (lengths that changed under the call)
+      const uint32_t item = whole ? f - base : (f - base) / cost, p0 = f - base - item * cost, p1 = min(p0 + (hi - f), cost);
       const int nt = static_cast<int>(tr_key_tiles(P, T));
-      const uint32_t p0 = f - fseg, p1 = min(p0 + (hi - f), cost);
       f += p1 - p0;
       const int k0 = whole ? 0 : static_cast<int>(p0 > kItemCost ? p0 - kItemCost : 0);
       const int k1 = whole ? nt : static_cast<int>(p1 > kItemCost ? p1 - kItemCost : 0);
       if (k1 <= k0) continue;  // a share's end inside an item's fixed units
+      const int n_pages = (P + T + kPageSize - 1) / kPageSize;
+      const int* row = a.block_table + static_cast<size_t>(n) * a.max_pages;
+      // this lane's page of the first tile; then of each next tile while the one before waits for its place
+      int id_next = lane < kTrTilePages && k0 * kTrTilePages + lane < n_pages ? __ldg(row + k0 * kTrTilePages + lane) : 0;
+      const int h = static_cast<int>(rts == 1 ? item : item / rts), rt = static_cast<int>(item - h * rts);
+      const int node0 = rt * a.tile_nodes, nodes = min(a.tile_nodes, T - node0);
+      const uint32_t qb = pi % a.q_bufs, quse = pi / a.q_bufs;
+      if (quse > 0 && !tr_wait(&ctl->q_empty[qb], quse - 1, ctl, a.status)) break;
       const uint32_t e = pi % Dm::kPieces;
       if (pi >= Dm::kPieces && !tr_wait(&ctl->piece_empty[e], pi / Dm::kPieces - 1, ctl, a.status)) break;
-      const int node0 = rt * a.tile_nodes, nodes = min(a.tile_nodes, T - node0);
       if (lane == 0) {
+        unsigned char* dst = smem + Dm::kOffQ + qb * Dm::kHalves * a.q_rows * 128;
+        mbar_arrive_expect_tx(&ctl->q_full[qb], static_cast<uint32_t>(Dm::kHalves * a.box_rows * 128));
+#pragma unroll
+        for (int half = 0; half < Dm::kHalves; ++half)
+          tma_load_3d(dst + half * a.q_rows * 128, &qmap, 64 * half, h * a.grp, q0 + node0, &ctl->q_full[qb]);
         TrPiece& pc = ctl->piece[e];
         pc.k0 = k0;
         pc.k1 = k1;
@@ -460,27 +480,13 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
         pc.rows = nodes * a.grp;
         pc.h = h;
         pc.n = n;
-        pc.slot = k0 == 0 ? (k1 == nt ? -1 : 1) : 0;
         pc.bad = 0;
+        pc.slot = k0 == 0 ? (k1 == nt ? -1 : 1) : 0;
         mbar_arrive_cta(&ctl->piece_full[e]);
-        if (pc.slot == 1)  // the item goes on in later CTAs
-          cut = {nodes * a.grp, q0 + node0, h, tr_cta_of(fseg + kItemCost + nt - 1, units, ctas)};
       }
-      const uint32_t qb = pi % a.q_bufs, quse = pi / a.q_bufs;
-      if (quse > 0 && !tr_wait(&ctl->q_empty[qb], quse - 1, ctl, a.status)) break;
-      if (lane == 0) {
-        unsigned char* dst = smem + Dm::kOffQ + qb * Dm::kHalves * a.q_rows * 128;
-        mbar_arrive_expect_tx(&ctl->q_full[qb], static_cast<uint32_t>(Dm::kHalves * a.box_rows * 128));
-#pragma unroll
-        for (int half = 0; half < Dm::kHalves; ++half)
-          tma_load_3d(dst + half * a.q_rows * 128, &qmap, 64 * half, h * a.grp, q0 + node0, &ctl->q_full[qb]);
-      }
-      const int n_pages = (P + T + kPageSize - 1) / kPageSize;
-      const int* row = a.block_table + static_cast<size_t>(n) * a.max_pages;
-      int id_next = lane < kTrTilePages && k0 * kTrTilePages + lane < n_pages ? __ldg(row + k0 * kTrTilePages + lane) : 0;
+      __syncwarp();
       for (int k = k0; k < k1; ++k, ++g) {
-        const int pg = k * kTrTilePages + lane;
-        const int id = id_next;
+        const int pg = k * kTrTilePages + lane, id = id_next;
         if (k + 1 < k1 && lane < kTrTilePages && pg + kTrTilePages < n_pages) id_next = __ldg(row + pg + kTrTilePages);
         bool valid = lane < kTrTilePages && pg < n_pages;
         if (valid && (id < 0 || id >= a.num_pages)) {
@@ -488,54 +494,40 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
           valid = false;
         }
         const uint32_t pages = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, valid)));
+        const uint32_t bytes = pages * static_cast<uint32_t>(kFp8 ? kPageSize * D + kPageSize : Dm::kPage);
         const long long tile = static_cast<long long>(id) * a.hkv + h;
-        if constexpr (kFp8) {
-          const uint32_t rs = g % Dm::kRawAlloc, use = g / Dm::kRawAlloc;
-          const uint32_t bytes = pages * static_cast<uint32_t>(kPageSize * D + kPageSize);
+        const uint32_t st = g % kRing, use = g / kRing;
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            uint64_t* full = kv ? &ctl->raw_v_full[rs] : &ctl->raw_k_full[rs];
-            uint64_t* empty = kv ? &ctl->raw_v_empty[rs] : &ctl->raw_k_empty[rs];
-            if (use > 0 && !tr_wait(empty, use - 1, ctl, a.status)) {
-              run = false;
-              break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-            __syncwarp();
-            if (valid) {
-              bulk_load(smem + (kv ? Dm::kOffRawV : Dm::kOffRawK) + rs * Dm::kRawTile + lane * (kPageSize * D),
-                        (kv ? a.v_raw : a.k_raw) + tile * (kPageSize * D), kPageSize * D, full);
-              bulk_load(smem + Dm::kOffScales + (rs * 2 + kv) * kTrKeys + lane * kPageSize,
-                        a.scales + tile * kScaleBytes + kv * kPageSize, kPageSize, full);
-            }
-          }
-          if (!run) break;
-        } else {
-          const uint32_t st = g % Dm::kSlots, use = g / Dm::kSlots;
-          const uint32_t bytes = pages * static_cast<uint32_t>(Dm::kPage);
-          if (use > 0 && !tr_wait(&ctl->k_empty[st], use - 1, ctl, a.status)) {
+        for (int kv = 0; kv < 2; ++kv) {
+          uint64_t* full = kFp8 ? (kv ? &ctl->raw_v_full[kFp8 ? st : 0] : &ctl->raw_k_full[kFp8 ? st : 0])
+                                : (kv ? &ctl->v_full[kFp8 ? 0 : st] : &ctl->k_full[kFp8 ? 0 : st]);
+          uint64_t* empty = kFp8 ? (kv ? &ctl->raw_v_empty[kFp8 ? st : 0] : &ctl->raw_k_empty[kFp8 ? st : 0])
+                                 : (kv ? &ctl->v_empty[kFp8 ? 0 : st] : &ctl->k_empty[kFp8 ? 0 : st]);
+          if (use > 0 && !tr_wait(empty, use - 1, ctl, a.status)) {
             run = false;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&ctl->k_full[st], bytes);
+          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
           __syncwarp();
-          if (valid) {
+          if (!valid) continue;
+          if constexpr (kFp8) {
+            bulk_load(smem + (kv ? Dm::kOffRawV : Dm::kOffRawK) + st * Dm::kRawTile + lane * (kPageSize * D),
+                      (kv ? a.v_raw : a.k_raw) + tile * (kPageSize * D), kPageSize * D, full);
+            bulk_load(smem + Dm::kOffScales + (st * 2 + kv) * kTrKeys + lane * kPageSize,
+                      a.scales + tile * kScaleBytes + kv * kPageSize, kPageSize, full);
+          } else if (kv) {
+            tma_load_4d(smem + Dm::kOffV + st * Dm::kTile + lane * Dm::kPage, &vmap, 0, 0, 0, static_cast<int>(tile), full);
+          } else {
             unsigned char* kd = smem + Dm::kOffK + st * Dm::kTile + lane * (kPageSize * 128);
 #pragma unroll
             for (int half = 0; half < Dm::kHalves; ++half)
-              tma_load_4d(kd + half * kTrHalfBytes, &kmap, 0, 0, half, static_cast<int>(tile), &ctl->k_full[st]);
+              tma_load_4d(kd + half * kTrHalfBytes, &kmap, 0, 0, half, static_cast<int>(tile), full);
           }
-          if (use > 0 && !tr_wait(&ctl->v_empty[st], use - 1, ctl, a.status)) {
-            run = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&ctl->v_full[st], bytes);
-          __syncwarp();
-          if (valid)
-            tma_load_4d(smem + Dm::kOffV + st * Dm::kTile + lane * Dm::kPage, &vmap, 0, 0, 0, static_cast<int>(tile),
-                        &ctl->v_full[st]);
         }
+        if (!run) break;
       }
+      if (k0 == 0 && k1 < nt)  // the item goes on in later CTAs, to the one that has its last unit
+        cut = {nodes * a.grp, q0 + node0, h, cta_of(base + (item + 1) * cost - 1)};
       ++pi;
     }
     if (lane == 0) a.cuts[me] = cut;
@@ -549,10 +541,10 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
     __syncwarp();
     if (*reinterpret_cast<volatile int*>(&ctl->fail) != 0) {
       // the CTA gave up: its copies in flight land before it ends (a wait for one that was never issued runs out)
-      constexpr uint32_t kRing = kFp8 ? Dm::kRawAlloc : Dm::kSlots;
       for (uint32_t i = g > kRing ? g - kRing : 0; i <= g; ++i) {
-        uint64_t* kf = kFp8 ? &ctl->raw_k_full[i % Dm::kRawAlloc] : &ctl->k_full[i % Dm::kSlots];
-        uint64_t* vf = kFp8 ? &ctl->raw_v_full[i % Dm::kRawAlloc] : &ctl->v_full[i % Dm::kSlots];
+        const uint32_t st = i % kRing;
+        uint64_t* kf = kFp8 ? &ctl->raw_k_full[kFp8 ? st : 0] : &ctl->k_full[kFp8 ? 0 : st];
+        uint64_t* vf = kFp8 ? &ctl->raw_v_full[kFp8 ? st : 0] : &ctl->v_full[kFp8 ? 0 : st];
         mbar_wait_bounded(kf, (i / kRing) & 1u, kDrainCycles);
         mbar_wait_bounded(vf, (i / kRing) & 1u, kDrainCycles);
       }
@@ -580,18 +572,24 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
     s.pi = s.g = v.pi = v.g = 0;
     open(s);
     open(v);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + Dm::kOffQ), 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + Dm::kOffK), 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + Dm::kOffV), 2048, 1024);
+    const uint32_t q_half = (a.q_rows * 128) >> 4;
     auto scores = [&]() {
       const uint32_t st = s.g % Dm::kSlots, w = s.g & 1u, qb = s.pi % a.q_bufs;
       if (s.k == s.k0 && !tr_wait(&ctl->q_full[qb], s.pi / a.q_bufs, ctl, a.status)) return false;
       if (!tr_wait(&ctl->k_full[st], s.g / Dm::kSlots, ctl, a.status)) return false;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t qa = smem_u32(smem + Dm::kOffQ + qb * Dm::kHalves * a.q_rows * 128);
-        const uint32_t kb = smem_u32(smem + Dm::kOffK + st * Dm::kTile);
+        // (a descriptor's low bits are the address / 16: steps are plain sums)
+        const uint64_t qa = q_desc + ((qb * Dm::kHalves * a.q_rows * 128) >> 4), kb = k_desc + ((st * Dm::kTile) >> 4);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          mma_ss(tmem + kTrColS + 128 * w, sdesc_sw128(qa + (i >> 2) * a.q_rows * 128 + (i & 3) * 32, 16, 1024),
-                 sdesc_sw128(kb + (i >> 2) * kTrHalfBytes + (i & 3) * 32, 16, 1024), Dm::kIdescQK, i > 0 ? 1u : 0u);
+        for (int half = 0; half < Dm::kHalves; ++half)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_ss(tmem + kTrColS + 128 * w, qa + half * q_half + 2 * i, kb + ((half * kTrHalfBytes) >> 4) + 2 * i, Dm::kIdescQK,
+                   half + i > 0 ? 1u : 0u);
         mma_commit(&ctl->s_full[w]);
         mma_commit(&ctl->k_empty[st]);
         if (s.k == s.k1 - 1) mma_commit(&ctl->q_empty[qb]);
@@ -617,12 +615,12 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       if (!(ok = tr_wait(&ctl->p_full[w], v.g >> 1, ctl, a.status))) break;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t vb = smem_u32(smem + Dm::kOffV + st * Dm::kTile);
+        const uint64_t vb = v_desc + ((st * Dm::kTile) >> 4);
         const bool fresh = v.k - v.k0 < 2;  // the group's first tile of the piece
 #pragma unroll
         for (int i = 0; i < kTrTilePages; ++i)
-          mma_ts(tmem + kTrColO + 128 * w, tmem + kTrColS + 128 * w + 8 * i, sdesc_sw128(vb + i * Dm::kPage, 2048, 1024),
-                 Dm::kIdescPV, (!fresh || i > 0) ? 1u : 0u);
+          mma_ts(tmem + kTrColO + 128 * w, tmem + kTrColS + 128 * w + 8 * i, vb + ((i * Dm::kPage) >> 4), Dm::kIdescPV,
+                 (!fresh || i > 0) ? 1u : 0u);
         mma_commit(&ctl->v_empty[st]);
         if (last) mma_commit(&ctl->o_done);
       }
@@ -657,12 +655,12 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       const TrPiece* pc = piece_at(pi);
       // (a warp that gives up in this wait leaves alone: the others' next barrier wants to hear of it, so all agree here)
       if (!tr_group_all(1, pc != nullptr)) break;
-      const int k0 = pc->k0, k1 = pc->k1, P = pc->P;
+      const int k0 = pc->k0, k1 = pc->k1, P = pc->P, row0 = pc->row0;
       const bool live = r < pc->rows, work = quarter * 32 < pc->rows;
       unsigned long long mask = 0;
       if (live) {
         const int node = pc->node0 + own_node, T = pc->T;
-        mask = a.masks != nullptr ? __ldg(a.masks + pc->row0 + own_node) : (2ull << node) - 1;
+        mask = a.masks != nullptr ? __ldg(a.masks + row0 + own_node) : (2ull << node) - 1;
         mask &= T < 64 ? (1ull << T) - 1 : ~0ull;
       }
       float m = -CUDART_INF_F, l = 0.f;
@@ -758,7 +756,7 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       const float inv = L == 0.f ? 0.f : 1.f / L;
       const int col0 = w * (D / 2);
       __nv_bfloat16* orow =
-          a.out + (static_cast<size_t>(pc->row0 + own_node) * a.hq + pc->h * a.grp + own_head) * D + col0;
+          a.out + (static_cast<size_t>(row0 + own_node) * a.hq + pc->h * a.grp + own_head) * D + col0;
       float4* rec = reinterpret_cast<float4*>(a.records + (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * kTrRecFloats);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {  // 16 columns at a time: this code runs once an item, its size is its cost
@@ -767,19 +765,15 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
         for (int e = 0; e < 16; ++e) o[e] = 0.f;
         __syncwarp();
         if (work) {
-          uint32_t x[16];
+          uint32_t x[16], y[16];
           const uint32_t at = t_o + col0 + 16 * c;
-          if (have0) {
-            tmem_ld16(at, x);
-            tmem_ld_wait();
+          tmem_ld16(at, x);
+          tmem_ld16(at + 128, y);
+          tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = a0 * __uint_as_float(x[e]);
-          }
-          if (have1) {
-            tmem_ld16(at + 128, x);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = fmaf(a1, __uint_as_float(x[e]), o[e]);
+          for (int e = 0; e < 16; ++e) {  // (a group without a tile: what its columns hold is not a number of this piece)
+            if (have0) o[e] = a0 * __uint_as_float(x[e]);
+            if (have1) o[e] = fmaf(a1, __uint_as_float(y[e]), o[e]);
           }
         }
         if (bad != 0) {
@@ -800,20 +794,17 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
           } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              rec[(col0 / 4 + 4 * c + q) * kTrRows + r] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+              rec[(col0 / 4 + 4 * c + q + 1) * kTrRows + r] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
         }
       }
-      if (slot >= 0 && live && w == 0) {
-        reinterpret_cast<float*>(rec)[128 * kTrRows + r] = M;
-        reinterpret_cast<float*>(rec)[129 * kTrRows + r] = L;
-      }
+      if (slot >= 0 && live && w == 0) rec[r] = make_float4(M, L, 0.f, 0.f);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&ctl->o_free);  // O is read: the next piece's products may overwrite it
       piece_done(pi);
     }
-  } else if (warp == 10 && !kFp8) {
+  } else if (warp == kTrMendWarp && !kFp8) {
     // ---------------------------------------------------------------- value tiles with nodes or an end in them
     uint32_t g = 0;
     bool ok = true;
@@ -940,43 +931,72 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
   if (warp == kTrMmaWarp) tmem_dealloc(tmem, kTrTmemCols);
 }
 
-// The records of cut items, joined in CTA order: o = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M). CTA (c, quarter,
-// part) takes 32 rows of the item that begins in CTA c of the attention kernel, 8 groups of 4 columns of them, a warp
-// each, a thread to a row. A kernel of its own: joined by the last CTA of an item instead, the 20 records of a long
-// request's item took that one SM 17 us, and counting the pieces 1 us everywhere.
-constexpr int kJoinThreads = 256;
+// The records of cut items, joined: o = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M), each warp over every eighth
+// record, then over the warps, in order: the same bits every time. CTA (c, part, quarter) takes 32 columns and 32 rows (a
+// thread to a row) of the item that begins in CTA c of the attention kernel. A kernel of its own: joined by the last CTA of
+// an item instead, the 20 records of a long request's item took that one SM 17 us; shared out between the item's CTAs by
+// atomics, each of which takes 0.8 us, 5 us.
+constexpr int kJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TrArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TrArgs a) {
+  __shared__ float4 part_o[kJoinWarps][8][32];
+  __shared__ float part_m[kJoinWarps][32], part_l[kJoinWarps][32];
   grid_dependency_wait();
   allow_dependents();
-  const int c0 = blockIdx.x, quarter = blockIdx.y & 3, part = blockIdx.y >> 2;
-  const int4 w = __ldcg(reinterpret_cast<const int4*>(a.cuts + c0));
-  const int rows = w.x, row0 = w.y, h = w.z, c1 = w.w;
-  const int r = quarter * 32 + (threadIdx.x & 31), q = part * 8 + (threadIdx.x >> 5);
-  if (r >= rows) return;
-  // the first piece is in slot 1 of its CTA, the others in slot 0 of theirs
-  const float* first = a.records + (static_cast<size_t>(c0) * 2 + 1) * kTrRecFloats;
-  auto record = [&](int c) { return c == c0 ? first : a.records + static_cast<size_t>(c) * 2 * kTrRecFloats; };
+  const int c0 = blockIdx.x, q0 = blockIdx.y * 8;
+  const int4 cut = __ldcg(reinterpret_cast<const int4*>(a.cuts + c0));
+  const int rows = cut.x, row0 = cut.y, h = cut.z, c1 = cut.w;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.z * 32 + lane;
+  if (static_cast<int>(blockIdx.z) * 32 >= rows) return;
   float M = -CUDART_INF_F, L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) {
-    const float* x = record(c);
-    const float m = __ldcg(x + 128 * kTrRows + r), l = __ldcg(x + 129 * kTrRows + r);
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(x) + q * kTrRows + r);
-    const float top = fmaxf(M, m);
-    const float old = M == -CUDART_INF_F ? 0.f : ex2(M - top), now = m == -CUDART_INF_F ? 0.f : ex2(m - top);
-    L = (M == -CUDART_INF_F ? L : L * old) + (m == -CUDART_INF_F ? l : l * now);
-    o.x = o.x * old + y.x * now;
-    o.y = o.y * old + y.y * now;
-    o.z = o.z * old + y.z * now;
-    o.w = o.w * old + y.w * now;
+  float4 o[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0 + warp; c <= c1 && r < rows; c += kJoinWarps) {
+    // the first piece is in slot 1 of its CTA, the others in slot 0 of theirs
+    const float4* x =
+        reinterpret_cast<const float4*>(a.records + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kTrRecFloats) + r;
+    const float4 ml = __ldcg(x);
+    float4 y[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y[q] = __ldcg(x + (q0 + q + 1) * kTrRows);
+    const float top = fmaxf(M, ml.x);
+    const float old = M == -CUDART_INF_F ? 0.f : ex2(M - top), now = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - top);
+    L = (M == -CUDART_INF_F ? L : L * old) + (ml.x == -CUDART_INF_F ? ml.y : ml.y * now);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      o[q].x = o[q].x * old + y[q].x * now;
+      o[q].y = o[q].y * old + y[q].y * now;
+      o[q].z = o[q].z * old + y[q].z * now;
+      o[q].w = o[q].w * old + y[q].w * now;
+    }
     M = top;
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) part_o[warp][q][lane] = o[q];
+  part_m[warp][lane] = M;
+  part_l[warp][lane] = L;
+  __syncthreads();
+  if (r >= rows) return;
+  // thread (row, 4 columns): the warps' parts
+  float top = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, part_m[w][lane]);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float m = part_m[w][lane], l = part_l[w][lane], now = m == -CUDART_INF_F ? 0.f : ex2(m - top);
+    const float4 y = part_o[w][warp][lane];
+    sum += m == -CUDART_INF_F ? l : l * now;
+    s.x += y.x * now;
+    s.y += y.y * now;
+    s.z += y.z * now;
+    s.w += y.w * now;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int node = r / a.grp;
-  __nv_bfloat16* dst = a.out + (static_cast<size_t>(row0 + node) * a.hq + h * a.grp + r - node * a.grp) * D + 4 * q;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  __nv_bfloat16* dst = a.out + (static_cast<size_t>(row0 + node) * a.hq + h * a.grp + r - node * a.grp) * D + 4 * (q0 + warp);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1014,10 +1034,8 @@ int launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& 
     return PKV_ERR_CUDA;
   // a table so narrow that no item can be cut needs no joining
   if (kItemCost + (static_cast<long long>(a.max_pages) + kTrTilePages - 1) / kTrTilePages <= kSmallItem) return PKV_OK;
-  return launch_pdl(tree_join_kernel<D>, dim3(static_cast<unsigned>(a.ctas), 4 * (D / 32)), dim3(kJoinThreads), 0, stream, a) ==
-                 cudaSuccess
-             ? PKV_OK
-             : PKV_ERR_CUDA;
+  const dim3 grid(static_cast<unsigned>(a.ctas), D / 32, static_cast<unsigned>((a.box_rows + 31) / 32));
+  return launch_pdl(tree_join_kernel<D>, grid, dim3(kJoinWarps * 32), 0, stream, a) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace
@@ -1056,6 +1074,7 @@ int launch_tree_attn(const TreeAttn& t, int num_q_heads, int num_kv_heads, int h
   a.hkv = num_kv_heads;
   a.grp = num_q_heads / num_kv_heads;
   a.tile_nodes = kTrRows / a.grp;
+  a.node_magic = static_cast<uint32_t>(((1ull << 32) + a.tile_nodes - 1) / a.tile_nodes);
   a.box_rows = a.grp * (t.max_nodes < a.tile_nodes ? t.max_nodes : a.tile_nodes);
   a.q_rows = (a.box_rows + 7) / 8 * 8;
   a.q_bufs = a.q_rows <= kTrRows / 2 ? 2 : 1;

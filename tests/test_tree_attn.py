@@ -70,22 +70,26 @@ def test_host_argument_checks(lib, fp8):
 
 def _pieces(items, grid, cost=2, small=6):
     """The schedule of tree_attn.cu, restated: (cta, item, k0, k1) of every piece, for items of so many key tiles, and for
-    each item the last CTA with a piece of it."""
+    each item the CTA with its last unit."""
     units, largest = sum(cost + n for n in items), cost + max(items)
     whole = largest <= small or 4 * largest * -(-len(items) // grid) * grid <= 5 * units
     size = [1 if whole else cost + n for n in items]
     units = sum(size)
     ctas = min(grid, units)
+    quota, more = divmod(units, ctas)
     starts = np.concatenate([[0], np.cumsum(size)])
     got = []
     for c in range(ctas):
-        lo, hi = c * units // ctas, (c + 1) * units // ctas
+        lo = c * quota + min(c, more)
+        hi = lo + quota + (c < more)
         for i, n in enumerate(items):
             a, b = max(lo, int(starts[i])), min(hi, int(starts[i + 1]))
             k0, k1 = (0, n) if whole else (max(0, a - int(starts[i]) - cost), max(0, b - int(starts[i]) - cost))
             if a < b and k1 > k0:
                 got.append((c, i, k0, k1))
-    return got, [((int(starts[i + 1]) - 1 + 1) * ctas + units - 1) // units - 1 for i in range(len(items))]
+    split = more * (quota + 1)
+    cta_of = lambda u: u // (quota + 1) if u < split else more + (u - split) // quota  # noqa: E731
+    return got, [cta_of(int(s) - 1) for s in starts[1:]]
 
 
 @pytest.mark.parametrize("grid", [1, 7, 152])
