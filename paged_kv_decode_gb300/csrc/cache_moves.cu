@@ -61,11 +61,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------------------- rows
-// A thread takes one 16-byte column of one KV head's rows and walks the path in order, eight rows at a time, loads
-// before stores. A path's numbers rise, so row i of it moves down or stays (path[i] >= i) and the rows that a thread
+// A thread takes one 16-byte column of one KV head's rows in one pool and walks the path in order, eight rows at a time,
+// loads before stores. A path's numbers rise, so row i of it moves down or stays (path[i] >= i) and the rows that a thread
 // has yet to read lie behind all that it has written: no thread needs another's, and nothing is read after it is
-// overwritten.
-constexpr int kKeepThreads = 128;
+// overwritten. A CTA takes 256 columns of a request, across heads, K and V and layers: where the rows lie is worked out
+// once for them.
+constexpr int kKeepThreads = 256;
 constexpr int kMaxPath = 64;
 constexpr int kBatch = 8;
 
@@ -76,69 +77,91 @@ struct KeepArgs {
   const int* prefix_lens;
   const int* block_table;
   int* status;
-  int max_path, max_pages, num_pages, hkv, cols, blocks;  // cols: 16-byte columns of a row; blocks: CTAs of a (request, pool)
+  int max_path, max_pages, num_pages, hkv, cols;  // cols: 16-byte columns of a row
+  int blocks;                                     // CTAs of a request
+  long long columns;                              // of a request: layers * 2 * hkv * cols
 };
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kKeepThreads) keep_nodes_kernel(const __grid_constant__ KeepArgs a) {
-  __shared__ long long from[kMaxPath], to[kMaxPath];  // row numbers in the pool of head 0; from < 0: nothing to move
+  // the rows to move, in order: (page, slot) in 32 bits each of where from and where to
+  __shared__ int from_page[kMaxPath], to_page[kMaxPath], slots[kMaxPath], count;
   grid_dependency_wait();
   allow_dependents();
   const int s = blockIdx.x / a.blocks, part = blockIdx.x - s * a.blocks;
-  const int layer = blockIdx.y >> 1, kv = blockIdx.y & 1;
-  int n = __ldg(a.path_lens + s);
-  const int prefix = __ldg(a.prefix_lens + s);
-  if (n < 0 || n > a.max_path || prefix < 0) {
-    if (threadIdx.x == 0) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
-    n = n < 0 || prefix < 0 ? 0 : a.max_path;
-  }
-  const int i = threadIdx.x;
-  if (i < n) {
-    const int x = __ldg(a.path + static_cast<size_t>(s) * a.max_path + i);
-    const int before = i > 0 ? __ldg(a.path + static_cast<size_t>(s) * a.max_path + i - 1) : -1;
-    const long long at = static_cast<long long>(prefix) + x, put = static_cast<long long>(prefix) + i;
-    long long f = -1, t = -1;
-    bool fine = x > before && x >= i && at < static_cast<long long>(a.max_pages) * kPageSize;
-    if (fine && x != i) {
-      const int* row = a.block_table + static_cast<size_t>(s) * a.max_pages;
-      const int p = __ldg(row + at / kPageSize), q = __ldg(row + put / kPageSize);
-      fine = p >= 0 && p < a.num_pages && q >= 0 && q < a.num_pages;
-      if (fine) {
-        f = static_cast<long long>(p) * a.hkv * kPageSize + at % kPageSize;
-        t = static_cast<long long>(q) * a.hkv * kPageSize + put % kPageSize;
-      }
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int prefix = __ldg(a.prefix_lens + s), given = __ldg(a.path_lens + s);
+    // (entries of the path are read before its length is known: the row is max_path long)
+    int node[kMaxPath / 32];
+#pragma unroll
+    for (int b = 0; b < kMaxPath / 32; ++b)
+      node[b] = 32 * b + lane < a.max_path ? __ldg(a.path + static_cast<size_t>(s) * a.max_path + 32 * b + lane) : -1;
+    int n = given;
+    if (n < 0 || n > a.max_path || prefix < 0) {
+      if (lane == 0) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
+      n = n < 0 || prefix < 0 ? 0 : a.max_path;
     }
-    if (!fine) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
-    from[i] = f;
-    to[i] = t;
+    int moves = 0, before = -1;
+#pragma unroll
+    for (int b = 0; b < kMaxPath / 32; ++b) {
+      const int i = 32 * b + lane, x = node[b];
+      const int up = __shfl_up_sync(0xffffffffu, x, 1);
+      const int prev = lane == 0 ? before : up;
+      before = __shfl_sync(0xffffffffu, x, 31);
+      bool move = false;
+      int p = 0, q = 0;
+      const long long at = static_cast<long long>(prefix) + x, put = static_cast<long long>(prefix) + i;
+      if (i < n) {
+        bool fine = x > prev && x >= i && at < static_cast<long long>(a.max_pages) * kPageSize;
+        if (fine && x != i) {
+          const int* row = a.block_table + static_cast<size_t>(s) * a.max_pages;
+          p = __ldg(row + at / kPageSize);
+          q = __ldg(row + put / kPageSize);
+          move = fine = p >= 0 && p < a.num_pages && q >= 0 && q < a.num_pages;
+        }
+        if (!fine) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
+      }
+      const unsigned vote = __ballot_sync(0xffffffffu, move);
+      if (move) {
+        const int m = moves + __popc(vote & ((1u << lane) - 1));
+        from_page[m] = p;
+        to_page[m] = q;
+        slots[m] = static_cast<int>(at % kPageSize) | static_cast<int>(put % kPageSize) << 8;
+      }
+      moves += __popc(vote);
+    }
+    if (lane == 0) count = moves;
   }
   __syncthreads();
-  const int c = part * kKeepThreads + threadIdx.x;
-  if (c >= a.hkv * a.cols) return;
-  const int h = c / a.cols, col = c - h * a.cols;
+  const int n = count;
+  const long long column = static_cast<long long>(part) * kKeepThreads + threadIdx.x;
+  if (column >= a.columns) return;
+  const int per = a.hkv * a.cols;  // columns of a pool's row
+  const int pool_i = static_cast<int>(column / per), c = static_cast<int>(column - static_cast<long long>(pool_i) * per);
+  const int layer = pool_i >> 1, kv = pool_i & 1, h = c / a.cols, col = c - h * a.cols;
   uint4* pool = static_cast<uint4*>(kv ? a.pools.v[layer] : a.pools.k[layer]) + static_cast<size_t>(h) * kPageSize * a.cols + col;
+  const size_t page_cols = static_cast<size_t>(a.hkv) * kPageSize * a.cols;
   uint8_t* sc = nullptr;
   if (kFp8 && col == 0)
     sc = static_cast<uint8_t*>(a.pools.scales[layer]) + static_cast<size_t>(h) * kScaleBytes + kv * kPageSize;
-  // row number r = page * hkv * 16 + slot; its scale byte lies at page * hkv * 32 + slot
-  auto scale_at = [&](long long r) {
-    const long long page = r / (static_cast<long long>(a.hkv) * kPageSize);
-    return page * a.hkv * kScaleBytes + (r - page * a.hkv * kPageSize);
-  };
+  const size_t page_scales = static_cast<size_t>(a.hkv) * kScaleBytes;
   for (int b = 0; b < n; b += kBatch) {
     uint4 x[kBatch];
     uint8_t y[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
-      if (b + j < n && from[b + j] >= 0) {
-        x[j] = pool[from[b + j] * a.cols];
-        if (sc != nullptr) y[j] = sc[scale_at(from[b + j])];
+      if (b + j < n) {
+        const int slot = slots[b + j] & 0xff;
+        x[j] = pool[from_page[b + j] * page_cols + slot * a.cols];
+        if (sc != nullptr) y[j] = sc[from_page[b + j] * page_scales + slot];
       }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
-      if (b + j < n && from[b + j] >= 0) {
-        pool[to[b + j] * a.cols] = x[j];
-        if (sc != nullptr) sc[scale_at(to[b + j])] = y[j];
+      if (b + j < n) {
+        const int slot = slots[b + j] >> 8;
+        pool[to_page[b + j] * page_cols + slot * a.cols] = x[j];
+        if (sc != nullptr) sc[to_page[b + j] * page_scales + slot] = y[j];
       }
   }
 }
@@ -180,11 +203,11 @@ int launch_keep_nodes(const MovePools& pools, int layers, bool fp8, const int32_
   a.num_pages = num_pages;
   a.hkv = num_kv_heads;
   a.cols = head_dim * (fp8 ? 1 : 2) / 16;
-  const long long cols = static_cast<long long>(num_kv_heads) * a.cols;
-  a.blocks = static_cast<int>((cols + kKeepThreads - 1) / kKeepThreads);
+  a.columns = static_cast<long long>(layers) * 2 * num_kv_heads * a.cols;
+  a.blocks = static_cast<int>((a.columns + kKeepThreads - 1) / kKeepThreads);
   const long long grid = static_cast<long long>(num_seqs) * a.blocks;
   if (grid > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>(2 * layers)), b(kKeepThreads);
+  const dim3 g(static_cast<unsigned>(grid)), b(kKeepThreads);
   const cudaError_t e = fp8 ? launch_pdl(keep_nodes_kernel<true>, g, b, 0, stream, a)
                             : launch_pdl(keep_nodes_kernel<false>, g, b, 0, stream, a);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

@@ -55,18 +55,17 @@ constexpr int kTrKeys = 128;  // keys of a tile
 constexpr int kTrTilePages = kTrKeys / kPageSize;
 constexpr int kTrMaxNodes = 64;
 constexpr int kTrMaxSeqs = 1024;
-constexpr int kTrMmaWarp = 8, kTrTmaWarp = 9, kTrMendWarp = 10;
-constexpr int kTrHalfBytes = kTrKeys * 128;                        // 64 columns of a 128-row bf16 tile
+constexpr int kTrMmaWarp = 8, kTrTmaWarp = 9, kTrMendWarp = 10, kTrPvWarp = 11;
 constexpr uint32_t kTrColS = 0, kTrColO = 256, kTrTmemCols = 512;  // S_w, O_w at + 128 w
 constexpr long long kDrainCycles = 20000000LL;                     // 10 ms: far more than a copy in flight takes
 
 // Fixed work of an item (query load, pipeline fill and drain, epilogue) in key tiles; and the largest item, in the
 // same units, that is never cut where all items are that small.
 #ifndef PKV_TREE_ITEM_COST
-#define PKV_TREE_ITEM_COST 2
+#define PKV_TREE_ITEM_COST 3
 #endif
 #ifndef PKV_TREE_SMALL_ITEM
-#define PKV_TREE_SMALL_ITEM 6
+#define PKV_TREE_SMALL_ITEM 7
 #endif
 constexpr int kItemCost = PKV_TREE_ITEM_COST;
 constexpr int kSmallItem = PKV_TREE_SMALL_ITEM;
@@ -74,7 +73,7 @@ constexpr int kSmallItem = PKV_TREE_SMALL_ITEM;
 template <int D, bool kFp8>
 struct TrDim {
   static constexpr int kHalves = D / 64;
-  static constexpr int kTile = kHalves * kTrHalfBytes;  // K or V tile (bf16)
+  static constexpr int kTile = kTrKeys * D * 2;  // K or V tile (bf16)
   static constexpr int kPage = kPageSize * D * 2;       // a page of it
   static constexpr int kSlots = kFp8 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
   static constexpr int kPieces = kSlots + 1;  // descriptors of pieces in flight
@@ -87,7 +86,7 @@ struct TrDim {
   static constexpr int kThreads = (kFp8 ? 12 + 2 * kConvWarps : 12) * 32;
   static constexpr int kRegsSoftmax = 152, kRegsOther = 56;
   static_assert(!kFp8 || 256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * 96, "register split");
-  static constexpr int kReaders = 9 + (kFp8 ? 2 * kConvWarps : 1);  // warps that read a piece's descriptor
+  static constexpr int kReaders = 10 + (kFp8 ? 2 * kConvWarps : 1);  // warps that read a piece's descriptor
   // shared memory, from a 1024-byte aligned base
   static constexpr int kOffQ = 0;  // one buffer of up to 128 rows, or two of up to 64
   static constexpr int kOffK = kOffQ + kTile;
@@ -118,7 +117,7 @@ struct TrCtl {
   uint64_t k_full[Dm::kSlots], k_empty[Dm::kSlots], v_full[Dm::kSlots], v_empty[Dm::kSlots];
   uint64_t s_full[2], p_full[2];
   uint64_t v_fixed[kFp8 ? 1 : Dm::kSlots];
-  uint64_t o_done, o_free, drain;
+  uint64_t o_done, o_free, drain, pv_done[2];
   uint64_t raw_k_full[Dm::kRawAlloc], raw_k_empty[Dm::kRawAlloc], raw_v_full[Dm::kRawAlloc], raw_v_empty[Dm::kRawAlloc];
   uint64_t piece_full[Dm::kPieces], piece_empty[Dm::kPieces];
   TrPiece piece[Dm::kPieces];
@@ -139,9 +138,10 @@ static_assert(tr_smem_bytes<64, false>() <= 232448 && tr_smem_bytes<64, true>() 
 // A record: float4 [D / 4 + 1][128 rows]: (m, l, 0, 0) of the rows, then O (unnormalised). Room of head_dim 128's at any.
 constexpr size_t kTrRecFloats = static_cast<size_t>(kTrRows) * (128 + 4);
 constexpr size_t kTrRecBytes = kTrRecFloats * 4;
-// The cut item whose first key tile a CTA holds: what the joining kernel reads (rows 0: none).
+// A cut item: what the joining kernel reads (rows 0: none).
 struct TrCut {
-  int rows, row0, h, last;  // last: the last CTA with a piece of it; the first is the one that wrote this
+  int rows, row0, h;
+  uint32_t span;  // the CTAs with its first and (in the high half) its last piece
 };
 
 struct TrArgs {
@@ -155,7 +155,10 @@ struct TrArgs {
   const __nv_bfloat16* v_pages;  // bf16 pool (rows added back)
   __nv_bfloat16* out;
   int* status;
-  TrCut* cuts;     // [ctas], written by every call
+  TrCut* cuts;     // [ctas], written by every call: of item (n * hkv + h) * node_tiles + rt where by_item, else of the item
+                   // whose first key tile CTA i has
+  int by_item;     // num_seqs * hkv * node_tiles where that is at most ctas, else 0
+  int node_tiles;  // items of a (request, KV head), at most
   float* records;  // [2 * ctas][kTrRecFloats]
   int num_seqs, total, max_pages, num_pages, max_nodes;
   int hq, hkv, grp;
@@ -222,6 +225,14 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gmem_src, 
                "l"(gmem_src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
+// A whole page of one KV head: all of a box's dims but the tile number start at 0.
+__device__ __forceinline__ void tma_load_5d(void* smem_dst, const CUtensorMap* map, int tile, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %2, %3}], "
+      "[%4];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(tile), "r"(smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ bool nonfinite_bf16x2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
@@ -231,14 +242,13 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t x) {  // infinities a
   return x;
 }
 
-// Byte offset of 16-byte chunk c (8 dims) of token row t: in a K tile ([half][128 rows], 128-byte swizzle), in a V
-// tile ([page][half][16 rows], so that a page is one TMA box and one step of the value product).
-__device__ __forceinline__ uint32_t tr_k_off(int t, int c) {
-  return static_cast<uint32_t>((c >> 3) * kTrHalfBytes + t * 128 + (((c & 7) ^ (t & 7)) << 4));
-}
+// Byte offset of 16-byte chunk c (8 dims) of token row t in a K or V tile: [8 rows][64-dim half][row of 128 bytes], each
+// such block of 1 KiB an atom of the 128-byte swizzle. A page is one TMA box of 4 KiB, and the blocks of a half lie at one
+// stride through the whole tile, which is what a descriptor can say of K (8-row groups of a K-major operand) and of V
+// (8-key groups of an MN-major one).
 template <int D>
-__device__ __forceinline__ uint32_t tr_v_off(int t, int c) {
-  return static_cast<uint32_t>((t >> 4) * (kPageSize * D * 2) + (c >> 3) * 2048 + (t & 15) * 128 + (((c & 7) ^ (t & 7)) << 4));
+__device__ __forceinline__ uint32_t tr_off(int t, int c) {
+  return static_cast<uint32_t>((t >> 3) * (8 * D * 2) + (c >> 3) * 1024 + (t & 7) * 128 + (((c & 7) ^ (t & 7)) << 4));
 }
 
 // Columns col .. col + 31 of a row: the infinities and NaN of the nodes' value rows in `bad` that this piece holds.
@@ -334,8 +344,8 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       if (!kFp8) mbar_init(&ctl->v_fixed[kFp8 ? 0 : i], 1);
     }
     for (int i = 0; i < Dm::kRawAlloc; ++i) {
-      mbar_init(&ctl->raw_k_full[i], 1);
-      mbar_init(&ctl->raw_v_full[i], 1);
+      mbar_init(&ctl->raw_k_full[i], 33);  // the copies' bytes, and each lane's scales
+      mbar_init(&ctl->raw_v_full[i], 33);
       mbar_init(&ctl->raw_k_empty[i], Dm::kConvWarps);
       mbar_init(&ctl->raw_v_empty[i], Dm::kConvWarps);
     }
@@ -345,7 +355,9 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
     }
     mbar_init(&ctl->o_done, 1);
     mbar_init(&ctl->o_free, 8);
-    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->drain, 2);
+    mbar_init(&ctl->pv_done[0], 1);
+    mbar_init(&ctl->pv_done[1], 1);
     ctl->fail = 0;
     fence_barrier_init();
   }
@@ -430,6 +442,35 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       base += __shfl_sync(0xffffffffu, x, 31);
     }
     constexpr uint32_t kRing = kFp8 ? Dm::kRawAlloc : Dm::kSlots;  // tiles that the loads may be ahead
+    // This lane's page of a tile of K or of V (kv = 1), < 0: none; eight lanes have a tile's. `full` completes with them.
+    // (One copy a page: a copy costs the TMA unit 27 ns and 13.5 ns a KiB, so that boxes of 2 KiB held it to 1.5 us for a
+    // tile of K and V, no faster than the memory; scales, 16 bytes a page, go by the load units instead.)
+    auto load = [&](int kv, uint32_t i, long long tile) {
+      const uint32_t st = i % kRing, use = i / kRing;
+      uint64_t* full = kFp8 ? (kv ? &ctl->raw_v_full[kFp8 ? st : 0] : &ctl->raw_k_full[kFp8 ? st : 0])
+                            : (kv ? &ctl->v_full[kFp8 ? 0 : st] : &ctl->k_full[kFp8 ? 0 : st]);
+      uint64_t* empty = kFp8 ? (kv ? &ctl->raw_v_empty[kFp8 ? st : 0] : &ctl->raw_k_empty[kFp8 ? st : 0])
+                             : (kv ? &ctl->v_empty[kFp8 ? 0 : st] : &ctl->k_empty[kFp8 ? 0 : st]);
+      const uint32_t pages = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, tile >= 0)));
+      if (use > 0 && !tr_wait(empty, use - 1, ctl, a.status)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(full, pages * static_cast<uint32_t>(kFp8 ? kPageSize * D : Dm::kPage));
+      __syncwarp();
+      if constexpr (kFp8) {
+        if (tile >= 0) {
+          bulk_load(smem + (kv ? Dm::kOffRawV : Dm::kOffRawK) + st * Dm::kRawTile + lane * (kPageSize * D),
+                    (kv ? a.v_raw : a.k_raw) + tile * (kPageSize * D), kPageSize * D, full);
+          cp_async16(smem_u32(smem + Dm::kOffScales + (st * 2 + kv) * kTrKeys + lane * kPageSize),
+                     a.scales + tile * kScaleBytes + kv * kPageSize);
+        }
+        // (every lane: its arrival comes when its own copies have landed)
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
+      } else if (tile >= 0) {
+        tma_load_5d(smem + (kv ? Dm::kOffV : Dm::kOffK) + st * Dm::kTile + lane * Dm::kPage, kv ? &vmap : &kmap,
+                    static_cast<int>(tile), full);
+      }
+      __syncwarp();
+      return true;
+    };
     uint32_t g = 0, pi = 0;
     bool run = true;
     TrCut cut = {0, 0, 0, 0};
@@ -493,44 +534,21 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
           set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
           valid = false;
         }
-        const uint32_t pages = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, valid)));
-        const uint32_t bytes = pages * static_cast<uint32_t>(kFp8 ? kPageSize * D + kPageSize : Dm::kPage);
-        const long long tile = static_cast<long long>(id) * a.hkv + h;
-        const uint32_t st = g % kRing, use = g / kRing;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          uint64_t* full = kFp8 ? (kv ? &ctl->raw_v_full[kFp8 ? st : 0] : &ctl->raw_k_full[kFp8 ? st : 0])
-                                : (kv ? &ctl->v_full[kFp8 ? 0 : st] : &ctl->k_full[kFp8 ? 0 : st]);
-          uint64_t* empty = kFp8 ? (kv ? &ctl->raw_v_empty[kFp8 ? st : 0] : &ctl->raw_k_empty[kFp8 ? st : 0])
-                                 : (kv ? &ctl->v_empty[kFp8 ? 0 : st] : &ctl->k_empty[kFp8 ? 0 : st]);
-          if (use > 0 && !tr_wait(empty, use - 1, ctl, a.status)) {
-            run = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-          __syncwarp();
-          if (!valid) continue;
-          if constexpr (kFp8) {
-            bulk_load(smem + (kv ? Dm::kOffRawV : Dm::kOffRawK) + st * Dm::kRawTile + lane * (kPageSize * D),
-                      (kv ? a.v_raw : a.k_raw) + tile * (kPageSize * D), kPageSize * D, full);
-            bulk_load(smem + Dm::kOffScales + (st * 2 + kv) * kTrKeys + lane * kPageSize,
-                      a.scales + tile * kScaleBytes + kv * kPageSize, kPageSize, full);
-          } else if (kv) {
-            tma_load_4d(smem + Dm::kOffV + st * Dm::kTile + lane * Dm::kPage, &vmap, 0, 0, 0, static_cast<int>(tile), full);
-          } else {
-            unsigned char* kd = smem + Dm::kOffK + st * Dm::kTile + lane * (kPageSize * 128);
-#pragma unroll
-            for (int half = 0; half < Dm::kHalves; ++half)
-              tma_load_4d(kd + half * kTrHalfBytes, &kmap, 0, 0, half, static_cast<int>(tile), full);
-          }
-        }
-        if (!run) break;
+        const long long tile = valid ? static_cast<long long>(id) * a.hkv + h : -1;
+        if (!(run = load(0, g, tile) && load(1, g, tile))) break;
       }
       if (k0 == 0 && k1 < nt)  // the item goes on in later CTAs, to the one that has its last unit
-        cut = {nodes * a.grp, q0 + node0, h, cta_of(base + (item + 1) * cost - 1)};
+        cut = {nodes * a.grp, q0 + node0, h, me | static_cast<uint32_t>(cta_of(base + (item + 1) * cost - 1)) << 16};
+      if (a.by_item && k0 == 0 && lane == 0)
+        a.cuts[(n * a.hkv + h) * a.node_tiles + rt] = k1 < nt ? cut : TrCut{0, 0, 0, 0};
       ++pi;
     }
-    if (lane == 0) a.cuts[me] = cut;
+    if (lane == 0 && a.by_item == 0) a.cuts[me] = cut;
+    if (lane == 0 && static_cast<int>(me) < a.by_item) {  // an item that there could be and is not
+      int P, T, q0;
+      tr_request(a, static_cast<int>(me) / (a.hkv * a.node_tiles), P, T, q0);
+      if (me % a.node_tiles >= tr_node_tiles(a, T)) a.cuts[me].rows = 0;
+    }
     const uint32_t e = pi % Dm::kPieces;
     if (pi < Dm::kPieces || tr_wait(&ctl->piece_empty[e], pi / Dm::kPieces - 1, ctl, a.status)) {
       if (lane == 0) {
@@ -553,85 +571,78 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
     }
   } else if (warp == kTrMmaWarp) {
     if constexpr (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Dm::kRegsOther));
-    // ---------------------------------------------------------------- products
-    // S of tile g + 2 follows the values of tile g (same group, S and P share their columns); tiles run across pieces
-    struct Tile {
-      uint32_t pi, g;
-      int k, k0, k1;
-      bool ok;
-    };
-    auto open = [&](Tile& t) {
-      const TrPiece* pc = piece_at(t.pi);
-      t.ok = pc != nullptr;
-      if (t.ok) {
-        t.k = t.k0 = pc->k0;
-        t.k1 = pc->k1;
-      }
-    };
-    Tile s, v;
-    s.pi = s.g = v.pi = v.g = 0;
-    open(s);
-    open(v);
+    // ---------------------------------------------------------------- S = Q K^T
     const uint64_t q_desc = sdesc_sw128(smem_u32(smem + Dm::kOffQ), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + Dm::kOffK), 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + Dm::kOffV), 2048, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + Dm::kOffK), 16, 8 * D * 2);
     const uint32_t q_half = (a.q_rows * 128) >> 4;
-    auto scores = [&]() {
-      const uint32_t st = s.g % Dm::kSlots, w = s.g & 1u, qb = s.pi % a.q_bufs;
-      if (s.k == s.k0 && !tr_wait(&ctl->q_full[qb], s.pi / a.q_bufs, ctl, a.status)) return false;
-      if (!tr_wait(&ctl->k_full[st], s.g / Dm::kSlots, ctl, a.status)) return false;
-      tc_fence_after();
-      if (lane == 0) {
-        // (a descriptor's low bits are the address / 16: steps are plain sums)
-        const uint64_t qa = q_desc + ((qb * Dm::kHalves * a.q_rows * 128) >> 4), kb = k_desc + ((st * Dm::kTile) >> 4);
-#pragma unroll
-        for (int half = 0; half < Dm::kHalves; ++half)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_ss(tmem + kTrColS + 128 * w, qa + half * q_half + 2 * i, kb + ((half * kTrHalfBytes) >> 4) + 2 * i, Dm::kIdescQK,
-                   half + i > 0 ? 1u : 0u);
-        mma_commit(&ctl->s_full[w]);
-        mma_commit(&ctl->k_empty[st]);
-        if (s.k == s.k1 - 1) mma_commit(&ctl->q_empty[qb]);
-      }
-      __syncwarp();
-      ++s.g;
-      if (++s.k == s.k1) {
-        ++s.pi;
-        open(s);
-      }
-      return true;
-    };
+    uint32_t g = 0;
     bool ok = true;
-    for (int i = 0; i < 2; ++i)
-      if (ok && s.ok) ok = scores();
-    while (ok && v.ok) {
-      const uint32_t st = v.g % Dm::kSlots, w = v.g & 1u;
-      const bool first = v.k == v.k0, last = v.k == v.k1 - 1;
-      // the previous piece's O is read
-      if (first && v.pi > 0 && !(ok = tr_wait(&ctl->o_free, v.pi - 1, ctl, a.status))) break;
-      if (!(ok = tr_wait(&ctl->v_full[st], v.g / Dm::kSlots, ctl, a.status))) break;
-      if (!kFp8 && !(ok = tr_wait(&ctl->v_fixed[kFp8 ? 0 : st], v.g / Dm::kSlots, ctl, a.status))) break;
-      if (!(ok = tr_wait(&ctl->p_full[w], v.g >> 1, ctl, a.status))) break;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint64_t vb = v_desc + ((st * Dm::kTile) >> 4);
-        const bool fresh = v.k - v.k0 < 2;  // the group's first tile of the piece
+    for (uint32_t pi = 0; ok; ++pi) {
+      const TrPiece* pc = piece_at(pi);
+      if (pc == nullptr) break;
+      const int tiles = pc->k1 - pc->k0;
+      piece_done(pi);
+      const uint32_t qb = pi % a.q_bufs;
+      if (!(ok = tr_wait(&ctl->q_full[qb], pi / a.q_bufs, ctl, a.status))) break;
+      const uint64_t qa = q_desc + ((qb * Dm::kHalves * a.q_rows * 128) >> 4);
+      for (int k = 0; k < tiles; ++k, ++g) {
+        const uint32_t st = g % Dm::kSlots, w = g & 1u;
+        // S and P share their columns: the values of the group's tile before are done
+        if (g >= 2 && !(ok = tr_wait(&ctl->pv_done[w], (g >> 1) - 1, ctl, a.status))) break;
+        if (!(ok = tr_wait(&ctl->k_full[st], g / Dm::kSlots, ctl, a.status))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t kb = k_desc + ((st * Dm::kTile) >> 4);
 #pragma unroll
-        for (int i = 0; i < kTrTilePages; ++i)
-          mma_ts(tmem + kTrColO + 128 * w, tmem + kTrColS + 128 * w + 8 * i, vb + ((i * Dm::kPage) >> 4), Dm::kIdescPV,
-                 (!fresh || i > 0) ? 1u : 0u);
-        mma_commit(&ctl->v_empty[st]);
-        if (last) mma_commit(&ctl->o_done);
+          for (int half = 0; half < Dm::kHalves; ++half)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_ss(tmem + kTrColS + 128 * w, qa + half * q_half + 2 * i, kb + half * (1024 >> 4) + 2 * i, Dm::kIdescQK,
+                     half + i > 0 ? 1u : 0u);
+          mma_commit(&ctl->s_full[w]);
+          mma_commit(&ctl->k_empty[st]);
+          if (k == tiles - 1) mma_commit(&ctl->q_empty[qb]);
+        }
+        __syncwarp();
+      }
+    }
+    if (*reinterpret_cast<volatile int*>(&ctl->fail) != 0) {
+      if (lane == 0) {
+        mma_commit(&ctl->drain);
+        mbar_wait_bounded(&ctl->drain, 0, kDrainCycles);
       }
       __syncwarp();
-      ++v.g;
-      if (++v.k == v.k1) {
-        piece_done(v.pi);
-        ++v.pi;
-        open(v);
+    }
+  } else if (warp == kTrPvWarp) {
+    if constexpr (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Dm::kRegsOther));
+    // ---------------------------------------------------------------- O += P V
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + Dm::kOffV), 1024, 8 * D * 2);
+    uint32_t g = 0;
+    bool ok = true;
+    for (uint32_t pi = 0; ok; ++pi) {
+      const TrPiece* pc = piece_at(pi);
+      if (pc == nullptr) break;
+      const int tiles = pc->k1 - pc->k0;
+      piece_done(pi);
+      if (pi > 0 && !(ok = tr_wait(&ctl->o_free, pi - 1, ctl, a.status))) break;
+      for (int k = 0; k < tiles; ++k, ++g) {
+        const uint32_t st = g % Dm::kSlots, w = g & 1u;
+        if (!(ok = tr_wait(&ctl->v_full[st], g / Dm::kSlots, ctl, a.status))) break;
+        if (!kFp8 && !(ok = tr_wait(&ctl->v_fixed[kFp8 ? 0 : st], g / Dm::kSlots, ctl, a.status))) break;
+        if (!(ok = tr_wait(&ctl->p_full[w], g >> 1, ctl, a.status))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t vb = v_desc + ((st * Dm::kTile) >> 4);
+#pragma unroll
+          for (int i = 0; i < kTrTilePages; ++i)
+            mma_ts(tmem + kTrColO + 128 * w, tmem + kTrColS + 128 * w + 8 * i, vb + ((i * Dm::kPage) >> 4), Dm::kIdescPV,
+                   (k >= 2 || i > 0) ? 1u : 0u);
+          mma_commit(&ctl->pv_done[w]);
+          mma_commit(&ctl->v_empty[st]);
+          if (k == tiles - 1) mma_commit(&ctl->o_done);
+        }
+        __syncwarp();
       }
-      if (s.ok) ok = scores();
     }
     if (*reinterpret_cast<volatile int*>(&ctl->fail) != 0) {  // the CTA gave up: the products in flight end first
       if (lane == 0) {
@@ -801,7 +812,7 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       if (slot >= 0 && live && w == 0) rec[r] = make_float4(M, L, 0.f, 0.f);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&ctl->o_free);  // O is read: the next piece's products may overwrite it
+      if (lane == 0) mbar_arrive_cta(&ctl->o_free);
       piece_done(pi);
     }
   } else if (warp == kTrMendWarp && !kFp8) {
@@ -823,7 +834,7 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
           constexpr int kChunks = D / 8;
           for (int i = t0 * kChunks + lane; i < kTrKeys * kChunks; i += 32) {
             const int t = i / kChunks;
-            uint4* at = reinterpret_cast<uint4*>(vt + tr_v_off<D>(t, i % kChunks));
+            uint4* at = reinterpret_cast<uint4*>(vt + tr_off<D>(t, i % kChunks));
             if (t >= len) {
               *at = make_uint4(0, 0, 0, 0);
               continue;
@@ -907,10 +918,8 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
               }
               if (odd) atomicOr(&ctl->piece[pi % Dm::kPieces].bad, 1ull << (k * kTrKeys + t - P));
             }
-            const uint32_t o0 = kv ? tr_v_off<D>(t, 2 * c) : tr_k_off(t, 2 * c);
-            const uint32_t o1 = kv ? tr_v_off<D>(t, 2 * c + 1) : tr_k_off(t, 2 * c + 1);
-            *reinterpret_cast<uint4*>(dst + o0) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(dst + o1) = make_uint4(y[4], y[5], y[6], y[7]);
+            *reinterpret_cast<uint4*>(dst + tr_off<D>(t, 2 * c)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + tr_off<D>(t, 2 * c + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -932,39 +941,41 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
 }
 
 // The records of cut items, joined: o = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M), each warp over every eighth
-// record, then over the warps, in order: the same bits every time. CTA (c, part, quarter) takes 32 columns and 32 rows (a
-// thread to a row) of the item that begins in CTA c of the attention kernel. A kernel of its own: joined by the last CTA of
+// record, then over the warps, in order: the same bits every time. CTA (i, part, quarter) takes 4 N columns and 32 rows (a
+// thread to a row) of cut item i. N = 8 keeps the grid within one wave of CTAs for batches (152 x 4 for 32 rows); few items
+// are spread over more CTAs with N = 2. A kernel of its own: joined by the last CTA of
 // an item instead, the 20 records of a long request's item took that one SM 17 us; shared out between the item's CTAs by
 // atomics, each of which takes 0.8 us, 5 us.
 constexpr int kJoinWarps = 8;
-template <int D>
+template <int D, int N>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TrArgs a) {
-  __shared__ float4 part_o[kJoinWarps][8][32];
+  __shared__ float4 part_o[kJoinWarps][N][32];
   __shared__ float part_m[kJoinWarps][32], part_l[kJoinWarps][32];
   grid_dependency_wait();
   allow_dependents();
-  const int c0 = blockIdx.x, q0 = blockIdx.y * 8;
-  const int4 cut = __ldcg(reinterpret_cast<const int4*>(a.cuts + c0));
-  const int rows = cut.x, row0 = cut.y, h = cut.z, c1 = cut.w;
+  const int q0 = blockIdx.y * N;
+  const int4 cut = __ldcg(reinterpret_cast<const int4*>(a.cuts + blockIdx.x));
+  const int rows = cut.x, row0 = cut.y, h = cut.z, c0 = cut.w & 0xffff, c1 = static_cast<uint32_t>(cut.w) >> 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.z * 32 + lane;
   if (static_cast<int>(blockIdx.z) * 32 >= rows) return;
   float M = -CUDART_INF_F, L = 0.f;
-  float4 o[8];
+  float4 o[N];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q = 0; q < N; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll(N == 8 ? 1 : 3)
   for (int c = c0 + warp; c <= c1 && r < rows; c += kJoinWarps) {
     // the first piece is in slot 1 of its CTA, the others in slot 0 of theirs
     const float4* x =
         reinterpret_cast<const float4*>(a.records + (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kTrRecFloats) + r;
     const float4 ml = __ldcg(x);
-    float4 y[8];
+    float4 y[N];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) y[q] = __ldcg(x + (q0 + q + 1) * kTrRows);
+    for (int q = 0; q < N; ++q) y[q] = __ldcg(x + (q0 + q + 1) * kTrRows);
     const float top = fmaxf(M, ml.x);
     const float old = M == -CUDART_INF_F ? 0.f : ex2(M - top), now = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - top);
     L = (M == -CUDART_INF_F ? L : L * old) + (ml.x == -CUDART_INF_F ? ml.y : ml.y * now);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < N; ++q) {
       o[q].x = o[q].x * old + y[q].x * now;
       o[q].y = o[q].y * old + y[q].y * now;
       o[q].z = o[q].z * old + y[q].z * now;
@@ -973,11 +984,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TrArgs
     M = top;
   }
 #pragma unroll
-  for (int q = 0; q < 8; ++q) part_o[warp][q][lane] = o[q];
+  for (int q = 0; q < N; ++q) part_o[warp][q][lane] = o[q];
   part_m[warp][lane] = M;
   part_l[warp][lane] = L;
   __syncthreads();
-  if (r >= rows) return;
+  if (r >= rows || warp >= N) return;
   // thread (row, 4 columns): the warps' parts
   float top = -CUDART_INF_F, sum = 0.f;
 #pragma unroll
@@ -1034,8 +1045,13 @@ int launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& 
     return PKV_ERR_CUDA;
   // a table so narrow that no item can be cut needs no joining
   if (kItemCost + (static_cast<long long>(a.max_pages) + kTrTilePages - 1) / kTrTilePages <= kSmallItem) return PKV_OK;
-  const dim3 grid(static_cast<unsigned>(a.ctas), D / 32, static_cast<unsigned>((a.box_rows + 31) / 32));
-  return launch_pdl(tree_join_kernel<D>, grid, dim3(kJoinWarps * 32), 0, stream, a) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  const unsigned items = static_cast<unsigned>(a.by_item > 0 ? a.by_item : a.ctas);
+  const unsigned quarters = static_cast<unsigned>((a.box_rows + 31) / 32);
+  const cudaError_t e =
+      items * quarters * (D / 8) <= 4u * a.ctas
+          ? launch_pdl(tree_join_kernel<D, 2>, dim3(items, D / 8, quarters), dim3(kJoinWarps * 32), 0, stream, a)
+          : launch_pdl(tree_join_kernel<D, 8>, dim3(items, D / 32, quarters), dim3(kJoinWarps * 32), 0, stream, a);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace
@@ -1079,11 +1095,14 @@ int launch_tree_attn(const TreeAttn& t, int num_q_heads, int num_kv_heads, int h
   a.q_rows = (a.box_rows + 7) / 8 * 8;
   a.q_bufs = a.q_rows <= kTrRows / 2 ? 2 : 1;
   a.ctas = num_sms;
+  a.node_tiles = (t.max_nodes + a.tile_nodes - 1) / a.tile_nodes;
+  const long long items = static_cast<long long>(t.num_seqs) * num_kv_heads * a.node_tiles;
+  a.by_item = items <= num_sms ? static_cast<int>(items) : 0;
   a.scale_log2 = t.scale * kLog2e;
   if (a.scale_log2 == 0.f) a.scale_log2 = FLT_MIN;  // a masked score, infinity, times 0 would be NaN
 
   const cuuint64_t hd = static_cast<cuuint64_t>(head_dim);
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   CUtensorMap qmap, kmap, vmap;
   {
     const cuuint64_t dims[3] = {hd, static_cast<cuuint64_t>(num_q_heads), static_cast<cuuint64_t>(t.total_nodes)};
@@ -1099,17 +1118,21 @@ int launch_tree_attn(const TreeAttn& t, int num_q_heads, int num_kv_heads, int h
     vmap = qmap;
     return head_dim == 64 ? launch<64, true>(qmap, kmap, vmap, a, stream) : launch<128, true>(qmap, kmap, vmap, a, stream);
   }
-  const int rc = encode_page_maps(t.k_pages, t.v_pages, head_dim, num_pages, num_kv_heads, &kmap, &vmap);
-  if (rc != PKV_OK) return rc;
   {
-    // K in boxes of one 64-dim half of a page: the halves of a tile's 128 rows lie apart in shared memory
-    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(kPageSize), hd / 64, static_cast<cuuint64_t>(num_pages) * num_kv_heads};
-    const cuuint64_t strides[3] = {hd * 2, 128, hd * 2 * kPageSize};
-    const cuuint32_t box[4] = {64, kPageSize, 1, 1};
-    if (enc(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.k_pages), dims, strides, box, ones,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return PKV_ERR_CUDA;
+    // (dim of a half, row of 8, half, 8-row group, tile): a box is a page, laid out as tr_off says
+    const long long tiles = static_cast<long long>(num_pages) * num_kv_heads;
+    if (tiles > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // tile coordinates are 32-bit
+    const cuuint32_t halves = static_cast<cuuint32_t>(head_dim / 64);
+    const cuuint64_t dims[5] = {64, 8, halves, 2, static_cast<cuuint64_t>(tiles)};
+    const cuuint64_t strides[4] = {hd * 2, 128, hd * 2 * 8, hd * 2 * kPageSize};
+    const cuuint32_t box[5] = {64, 8, halves, 2, 1};
+    const void* pools[2] = {t.k_pages, t.v_pages};
+    CUtensorMap* maps[2] = {&kmap, &vmap};
+    for (int i = 0; i < 2; ++i)
+      if (enc(maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(pools[i]), dims, strides, box, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return PKV_ERR_CUDA;
   }
   return head_dim == 64 ? launch<64, false>(qmap, kmap, vmap, a, stream) : launch<128, false>(qmap, kmap, vmap, a, stream);
 }

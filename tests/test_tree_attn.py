@@ -68,7 +68,7 @@ def test_host_argument_checks(lib, fp8):
         assert lib.pkv_tree_workspace_bytes(*bad) == 0
 
 
-def _pieces(items, grid, cost=2, small=6):
+def _pieces(items, grid, cost=3, small=7):
     """The schedule of tree_attn.cu, restated: (cta, item, k0, k1) of every piece, for items of so many key tiles, and for
     each item the CTA with its last unit."""
     units, largest = sum(cost + n for n in items), cost + max(items)
