@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(kKeepThreads) keep_nodes_kernel(const __grid_c
   const int per = a.hkv * a.cols;  // columns of a pool's row
   const int pool_i = static_cast<int>(column / per), c = static_cast<int>(column - static_cast<long long>(pool_i) * per);
   const int layer = pool_i >> 1, kv = pool_i & 1, h = c / a.cols, col = c - h * a.cols;
-  uint4* pool = static_cast<uint4*>(kv ? a.pools.v[layer] : a.pools.k[layer]) + static_cast<size_t>(h) * kPageSize * a.cols + col;
+  uint4* pool =
+      static_cast<uint4*>(kv ? a.pools.v[layer] : a.pools.k[layer]) + static_cast<size_t>(h) * kPageSize * a.cols + col;
   const size_t page_cols = static_cast<size_t>(a.hkv) * kPageSize * a.cols;
   uint8_t* sc = nullptr;
   if (kFp8 && col == 0)

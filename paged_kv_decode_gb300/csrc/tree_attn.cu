@@ -21,8 +21,9 @@
 //    items; a cut item's partial results go to records, and a second small
 //    kernel joins them in CTA order (the same bits every time). Where all items
 //    are small, or whole items balance as well, none is cut.
-//  * Warp 9 plans the CTA's pieces and loads Q and the K and V tiles of 128 keys
-//    through the block table into rings. Warp 8 issues S = Q K^T into TMEM and O += P V with P as the
+//  * Warp 9 plans the CTA's pieces, publishes them to the other warps and loads
+//    Q and the K and V tiles of 128 keys through the block table into rings.
+//    Warp 8 issues S = Q K^T into TMEM, warp 11 O += P V with P as the
 //    tensor-memory operand. Key tiles alternate between two groups of four
 //    softmax warps, each with its own S, P, O, maximum and sum: one group's
 //    exponentials run beside the other's products. The two halves of a row are
@@ -32,12 +33,25 @@
 //    for V expand each tile into the bf16 ring and everything behind that is
 //    the bf16 kernel: the outputs are those of pkv_expand_fp8 followed by the
 //    bf16 call, bit for bit.
-//  * P is rounded to bf16 before it multiplies V, the operand type of the product (at
-//    most 2^-9 of a weight; the sum l keeps the unrounded weights in fp32).
+//  * P is rounded to bf16 before it multiplies V, the operand type of the product
+//    (off by at most 2^-9 of a weight); the sum l keeps the unrounded weights in
+//    fp32.
 //  * Value rows behind the last node are zeroed in shared memory (they may hold
 //    anything, and 0 * NaN = NaN). A node's value row that holds infinities or
 //    NaN would reach rows that do not see the node the same way: such elements
 //    are zeroed too, and added back, in the epilogue, to the rows that see them.
+//
+// Measured on one GB300 (us in a graph, inputs resident, of 16 / 8 / 128 where not
+// said otherwise; in brackets the cache's bytes at 6682 GB/s): 16 requests of 300
+// to 3000 tokens with 16 nodes 31.8 (20.0), one of 40k tokens with 32 nodes 35.6
+// (24.6), 27 ragged requests of 32 / 8 / 128 118 (65), two of 37 and 200 tokens
+// 7.4; 8-bit cache: the 16 requests 35.5 (10.2). What is left: long batches run at 92 % of the
+// memory's rate (16 requests of 6600 tokens: 70.2 of 64.9); shorter ones pay 4 us
+// from the launch to the first tile (the lengths, the table and the tile are
+// three dependent reads), 2 us an item and 3.5 us for the join and its launch.
+// Neither the products nor the softmax bound it: leaving out either changes no
+// time. The 8-bit form is bound by the expansion of its tiles (without it 1.25
+// instead of 1.85 us a tile).
 #include <cuda.h>
 #include <float.h>
 #include <math_constants.h>
@@ -55,7 +69,7 @@ constexpr int kTrKeys = 128;  // keys of a tile
 constexpr int kTrTilePages = kTrKeys / kPageSize;
 constexpr int kTrMaxNodes = 64;
 constexpr int kTrMaxSeqs = 1024;
-constexpr int kTrMmaWarp = 8, kTrTmaWarp = 9, kTrMendWarp = 10, kTrPvWarp = 11;
+constexpr int kTrQkWarp = 8, kTrTmaWarp = 9, kTrMendWarp = 10, kTrPvWarp = 11;
 constexpr uint32_t kTrColS = 0, kTrColO = 256, kTrTmemCols = 512;  // S_w, O_w at + 128 w
 constexpr long long kDrainCycles = 20000000LL;                     // 10 ms: far more than a copy in flight takes
 
@@ -81,8 +95,8 @@ struct TrDim {
   static constexpr int kRawSlots = kFp8 ? (D == 128 ? 2 : 5) : 0;
   static constexpr int kRawAlloc = kFp8 ? kRawSlots : 1;  // array sizes may not be 0
   static constexpr int kConvWarps = 4;                    // each for K (warps 12 ..) and for V (16 ..)
-  // bf16: 12 warps, 11 idle. 8-bit: 20 warps, 10 and 11 idle; the launch gives each thread 96 registers, the two softmax
-  // warpgroups rise to 152, the other three drop to 56.
+  // bf16: 12 warps. 8-bit: 20 warps, 10 idle; the launch gives each thread 96 registers, the two softmax warpgroups rise
+  // to 152, the other three drop to 56.
   static constexpr int kThreads = (kFp8 ? 12 + 2 * kConvWarps : 12) * 32;
   static constexpr int kRegsSoftmax = 152, kRegsOther = 56;
   static_assert(!kFp8 || 256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * 96, "register split");
@@ -95,7 +109,6 @@ struct TrDim {
   static constexpr int kOffRawV = kOffRawK + kRawSlots * kRawTile;
   static constexpr int kOffScales = kOffRawV + kRawSlots * kRawTile;  // [raw slot][K, V][128] bytes
   static constexpr int kOffCtl = kOffScales + kRawSlots * 2 * kTrKeys;
-  static constexpr uint32_t kIdescQK = idesc_bf16_f32(kTrRows, kTrKeys, false);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(kTrRows, D, true);  // V is MN-major
 };
 
@@ -168,7 +181,8 @@ struct TrArgs {
   int q_rows;      // ... rounded up to whole swizzle atoms of 8 rows
   int q_bufs;      // query buffers: 2 where two fit
   int ctas;        // CTAs of the grid
-  float scale_log2;
+  float scale_log2;      // |scale| / ln 2
+  uint32_t idesc_qk;     // S = Q K^T, with -Q where the scale is negative
 };
 
 // Prefix and nodes of request n (0 nodes where the lengths are out of bounds).
@@ -187,9 +201,9 @@ __device__ __forceinline__ void tr_request(const TrArgs& a, int n, int& P, int& 
 __device__ __forceinline__ uint32_t tr_key_tiles(int P, int T) {
   return (static_cast<uint32_t>(P) + T + kTrKeys - 1) / kTrKeys;
 }
-// Items of a request, units of one of them (whole: items are not cut, each counts 1), and of the request. All units of
-// a call fit 32 bits: at most 2^31 / 8 table entries of 8 heads, a tile for 8 of them, 4 node tiles, and 12 units of
-// fixed work for each of 1024 * 65535 (request, head) pairs.
+// Items of a request and KV head, and units of one of them (whole: items are not cut, each counts 1). All units of a call
+// fit 32 bits: 4 items of each of up to 1024 * 65535 (request, head) pairs, each of 4 units and one more for 8 pages,
+// which are fewer than 2^31: at most 2^30 + 2^30 units.
 __device__ __forceinline__ uint32_t tr_node_tiles(const TrArgs& a, int T) {  // T / tile_nodes, rounded up
   return __umulhi(static_cast<uint32_t>(T) + a.tile_nodes - 1, a.node_magic);
 }
@@ -251,7 +265,7 @@ __device__ __forceinline__ uint32_t tr_off(int t, int c) {
   return static_cast<uint32_t>((t >> 3) * (8 * D * 2) + (c >> 3) * 1024 + (t & 7) * 128 + (((c & 7) ^ (t & 7)) << 4));
 }
 
-// Columns col .. col + 31 of a row: the infinities and NaN of the nodes' value rows in `bad` that this piece holds.
+// The infinities and NaN in column col of the nodes' value rows in `bad` that this piece holds (0 if there are none).
 template <int D, bool kFp8>
 __device__ __noinline__ float tr_nonfinite(const TrArgs& a, const TrPiece* pc, unsigned long long bad, int col) {
   float sum = 0.f;
@@ -277,26 +291,30 @@ __device__ __forceinline__ void tr_load64(uint32_t taddr, uint32_t (&x)[2][32]) 
   tmem_ld32(taddr + 32, x[1]);
   tmem_ld_wait();
 }
-__device__ __forceinline__ float tr_max64(const uint32_t (&x)[2][32], float2 sc2) {
+__device__ __forceinline__ float tr_max64(const uint32_t (&x)[2][32]) {
   float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F;
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-      const float2 t = __fmul2_rn(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc2);
-      m0 = fmaxf(m0, t.x);
-      m1 = fmaxf(m1, t.y);
+      m0 = fmaxf(m0, __uint_as_float(x[c][e]));
+      m1 = fmaxf(m1, __uint_as_float(x[c][e + 1]));
     }
   return fmaxf(m0, m1);
 }
-// P = 2^(s * scale - m) of 64 columns, as bf16 over 32 columns; their sum joins l2
+// the weight of a score or of a part whose maximum lies d <= 0 below the row's
+__device__ __forceinline__ float tr_weight(float d, float scale_log2) { return ex2(d * scale_log2); }
+// P = 2^((s - m) * scale) of 64 columns, as bf16 over 32 columns; their sum joins l2. The difference comes first: the
+// largest score's weight is 2^0 whatever its size, where s * scale - m * scale as one multiply-add leaves the rounding of
+// m * scale, which for scores past 2^30 is a weight of infinity or 0.
 __device__ __forceinline__ void tr_exp64(uint32_t taddr, const uint32_t (&x)[2][32], float2 sc2, float2 nm2, float2& l2) {
   uint32_t pk[32];
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-      const float2 t = __ffma2_rn(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), sc2, nm2);
+      const float2 t =
+          __fmul2_rn(__fadd2_rn(make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), nm2), sc2);
       const float2 p = make_float2(ex2(t.x), ex2(t.y));
       l2 = __fadd2_rn(l2, p);
       pk[c * 16 + (e >> 1)] = pack_bf16x2(p.x, p.y);
@@ -320,7 +338,7 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
     if (tid == 0) set_status(a.status, PKV_ERR_MISALIGNED);
     return;
   }
-  if (warp == kTrMmaWarp) {
+  if (warp == kTrQkWarp) {
     tmem_alloc(&ctl->tmem, kTrTmemCols);
     tmem_relinquish();
   } else if (warp == kTrTmaWarp && lane == 0) {
@@ -408,8 +426,8 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
     // whole items where all are small, or where the CTAs' largest number of them is as good a balance as shares would be
     // (within a quarter; every CTA computes the same floats)
     const float rounds = ceilf(static_cast<float>(items) / static_cast<float>(a.ctas));
-    const bool whole = largest <= kSmallItem ||
-                       4.f * static_cast<float>(largest) * rounds * static_cast<float>(a.ctas) <= 5.f * static_cast<float>(units);
+    const float longest = static_cast<float>(largest) * rounds * static_cast<float>(a.ctas);
+    const bool whole = largest <= kSmallItem || 4.f * longest <= 5.f * static_cast<float>(units);
     if (whole) units = items;
     // CTA c's share: units / ctas of them, one more for the first units % ctas
     const uint32_t ctas = min(units, static_cast<uint32_t>(a.ctas)), me = blockIdx.x;
@@ -569,7 +587,7 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       for (uint32_t i = pi > 1 ? pi - 1 : 0; i <= pi; ++i)
         mbar_wait_bounded(&ctl->q_full[i % a.q_bufs], (i / a.q_bufs) & 1u, kDrainCycles);
     }
-  } else if (warp == kTrMmaWarp) {
+  } else if (warp == kTrQkWarp) {
     if constexpr (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Dm::kRegsOther));
     // ---------------------------------------------------------------- S = Q K^T
     const uint64_t q_desc = sdesc_sw128(smem_u32(smem + Dm::kOffQ), 16, 1024);
@@ -597,7 +615,7 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
           for (int half = 0; half < Dm::kHalves; ++half)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              mma_ss(tmem + kTrColS + 128 * w, qa + half * q_half + 2 * i, kb + half * (1024 >> 4) + 2 * i, Dm::kIdescQK,
+              mma_ss(tmem + kTrColS + 128 * w, qa + half * q_half + 2 * i, kb + half * (1024 >> 4) + 2 * i, a.idesc_qk,
                      half + i > 0 ? 1u : 0u);
           mma_commit(&ctl->s_full[w]);
           mma_commit(&ctl->k_empty[st]);
@@ -658,8 +676,7 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
     const int own_node = r / a.grp, own_head = r - own_node * a.grp;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lanes + kTrColS + 128 * w, t_o = tmem + lanes + kTrColO;
-    // what a masked score is set to: -infinity once it is scaled
-    const uint32_t masked = __float_as_uint(a.scale_log2 < 0.f ? CUDART_INF_F : -CUDART_INF_F);
+    const uint32_t masked = __float_as_uint(-CUDART_INF_F);
     const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
     uint32_t g = 0, pi = 0;
     for (;; ++pi) {
@@ -682,7 +699,7 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
         if (!(ok = tr_wait(&ctl->s_full[w], g >> 1, ctl, a.status))) continue;
         if (work) {
           tc_fence_after();
-          uint32_t x[2][32];
+          uint32_t x[2][32];  // half of the row's 128 scores
           if ((k + 1) * kTrKeys > P) {
             // nodes, or keys past the end, among the tile's: 128 bits of what the row sees
             const int sh = P - k * kTrKeys;  // keys of the prefix in this tile
@@ -712,14 +729,14 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
           // the second half for its maximum, the first half, which then stays in registers; the weights of the first
           // half overwrite its own columns alone
           tr_load64(t_s + 64, x);
-          float mx = tr_max64(x, sc2);
+          float mx = tr_max64(x);
           tr_load64(t_s, x);
-          mx = fmaxf(mx, tr_max64(x, sc2));
+          mx = fmaxf(mx, tr_max64(x));
           // the maximum moves, and O with it, only when it grows by more than 2^8 (weights up to 2^8 are fine)
           const float m_new = fmaxf(m, mx);
-          const bool grow = m == -CUDART_INF_F ? m_new != -CUDART_INF_F : m_new - m > 8.f;
+          const bool grow = m == -CUDART_INF_F ? m_new != -CUDART_INF_F : (m_new - m) * a.scale_log2 > 8.f;
           if (__any_sync(0xffffffffu, grow)) {
-            const float alpha = !grow ? 1.f : m == -CUDART_INF_F ? 0.f : ex2(m - m_new);
+            const float alpha = !grow ? 1.f : m == -CUDART_INF_F ? 0.f : tr_weight(m - m_new, a.scale_log2);
             if (!fresh) {
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
@@ -759,18 +776,20 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       const float m0 = ctl->stat[0][0][r], l0 = ctl->stat[0][1][r], m1 = ctl->stat[1][0][r], l1 = ctl->stat[1][1][r];
       const float M = fmaxf(m0, m1);
       // (a half that saw nothing has sum 0, or NaN where every score was NaN)
-      const float a0 = m0 == -CUDART_INF_F ? 0.f : ex2(m0 - M), a1 = m1 == -CUDART_INF_F ? 0.f : ex2(m1 - M);
+      const float a0 = m0 == -CUDART_INF_F ? 0.f : tr_weight(m0 - M, a.scale_log2);
+      const float a1 = m1 == -CUDART_INF_F ? 0.f : tr_weight(m1 - M, a.scale_log2);
       const float L = (m0 == -CUDART_INF_F ? l0 : l0 * a0) + (m1 == -CUDART_INF_F ? l1 : l1 * a1);
       const bool have0 = k1 - k0 > 1 || (g0 & 1u) == 0, have1 = k1 - k0 > 1 || (g0 & 1u) == 1;
       const int slot = pc->slot;
-      const unsigned long long bad = k1 * kTrKeys > P ? mask & *reinterpret_cast<const volatile unsigned long long*>(&pc->bad) : 0;
+      unsigned long long bad = 0;  // nodes that this row sees whose value rows hold a NaN or an infinity
+      if (k1 * kTrKeys > P) bad = mask & *reinterpret_cast<const volatile unsigned long long*>(&pc->bad);
       const float inv = L == 0.f ? 0.f : 1.f / L;
       const int col0 = w * (D / 2);
       __nv_bfloat16* orow =
           a.out + (static_cast<size_t>(row0 + own_node) * a.hq + pc->h * a.grp + own_head) * D + col0;
       float4* rec = reinterpret_cast<float4*>(a.records + (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * kTrRecFloats);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {  // 16 columns at a time: this code runs once an item, its size is its cost
+      for (int c = 0; c < D / 32; ++c) {  // 16 columns at a time (with 32, which spilled, batches took 3 us longer)
         float o[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[e] = 0.f;
@@ -812,7 +831,7 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       if (slot >= 0 && live && w == 0) rec[r] = make_float4(M, L, 0.f, 0.f);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&ctl->o_free);
+      if (lane == 0) mbar_arrive_cta(&ctl->o_free);  // O is read: the next piece's products may overwrite it
       piece_done(pi);
     }
   } else if (warp == kTrMendWarp && !kFp8) {
@@ -937,15 +956,15 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kTrMmaWarp) tmem_dealloc(tmem, kTrTmemCols);
+  if (warp == kTrQkWarp) tmem_dealloc(tmem, kTrTmemCols);
 }
 
 // The records of cut items, joined: o = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M), each warp over every eighth
 // record, then over the warps, in order: the same bits every time. CTA (i, part, quarter) takes 4 N columns and 32 rows (a
 // thread to a row) of cut item i. N = 8 keeps the grid within one wave of CTAs for batches (152 x 4 for 32 rows); few items
-// are spread over more CTAs with N = 2. A kernel of its own: joined by the last CTA of
-// an item instead, the 20 records of a long request's item took that one SM 17 us; shared out between the item's CTAs by
-// atomics, each of which takes 0.8 us, 5 us.
+// are spread over more CTAs with N = 2 (one request of 40k tokens 1.7 us less). A kernel of its own: joined by the last CTA
+// of an item instead, the 20 records of a long request's item took that one SM 17 us; shared out between the item's CTAs
+// by atomics, each of which takes 0.8 us, 5 us.
 constexpr int kJoinWarps = 8;
 template <int D, int N>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TrArgs a) {
@@ -958,6 +977,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TrArgs
   const int rows = cut.x, row0 = cut.y, h = cut.z, c0 = cut.w & 0xffff, c1 = static_cast<uint32_t>(cut.w) >> 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.z * 32 + lane;
   if (static_cast<int>(blockIdx.z) * 32 >= rows) return;
+  // (a call that gave up may leave another call's descriptors: nothing of them reaches past this call's buffers)
+  if (rows > kTrRows || row0 < 0 || row0 + (rows + a.grp - 1) / a.grp > a.total || h < 0 || h >= a.hkv || c1 >= a.ctas) return;
   float M = -CUDART_INF_F, L = 0.f;
   float4 o[N];
 #pragma unroll
@@ -972,7 +993,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TrArgs
 #pragma unroll
     for (int q = 0; q < N; ++q) y[q] = __ldcg(x + (q0 + q + 1) * kTrRows);
     const float top = fmaxf(M, ml.x);
-    const float old = M == -CUDART_INF_F ? 0.f : ex2(M - top), now = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - top);
+    const float old = M == -CUDART_INF_F ? 0.f : tr_weight(M - top, a.scale_log2);
+    const float now = ml.x == -CUDART_INF_F ? 0.f : tr_weight(ml.x - top, a.scale_log2);
     L = (M == -CUDART_INF_F ? L : L * old) + (ml.x == -CUDART_INF_F ? ml.y : ml.y * now);
 #pragma unroll
     for (int q = 0; q < N; ++q) {
@@ -996,7 +1018,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TrArgs
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) {
-    const float m = part_m[w][lane], l = part_l[w][lane], now = m == -CUDART_INF_F ? 0.f : ex2(m - top);
+    const float m = part_m[w][lane], l = part_l[w][lane];
+    const float now = m == -CUDART_INF_F ? 0.f : tr_weight(m - top, a.scale_log2);
     const float4 y = part_o[w][warp][lane];
     sum += m == -CUDART_INF_F ? l : l * now;
     s.x += y.x * now;
@@ -1098,7 +1121,8 @@ int launch_tree_attn(const TreeAttn& t, int num_q_heads, int num_kv_heads, int h
   a.node_tiles = (t.max_nodes + a.tile_nodes - 1) / a.tile_nodes;
   const long long items = static_cast<long long>(t.num_seqs) * num_kv_heads * a.node_tiles;
   a.by_item = items <= num_sms ? static_cast<int>(items) : 0;
-  a.scale_log2 = t.scale * kLog2e;
+  a.scale_log2 = fabsf(t.scale) * kLog2e;
+  a.idesc_qk = idesc_bf16_f32(kTrRows, kTrKeys, false) | (t.scale < 0.f ? 1u << 13 : 0u);  // bit 13 negates A
   if (a.scale_log2 == 0.f) a.scale_log2 = FLT_MIN;  // a masked score, infinity, times 0 would be NaN
 
   const cuuint64_t hd = static_cast<cuuint64_t>(head_dim);
