@@ -606,14 +606,16 @@ size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t num_seqs, in
  *  max_nodes:    host-side upper bound on any request's nodes, 1 .. 64
  *                (PKV_ERR_UNSUPPORTED beyond)
  *  num_seqs:     0 .. 1024 (PKV_ERR_UNSUPPORTED beyond); num_seqs *
- *                max_pages_per_seq * max(num_kv_heads, 8) < 2^31
+ *                max_pages_per_seq * max(num_kv_heads, 8) < 2^31;
+ *                max_pages_per_seq <= 2^27 - 8
  *  workspace:    >= pkv_tree_workspace_bytes(...), its status header zeroed once
  *                by pkv_workspace_init; a call writes what it reads of the rest.
  *                It serves tree attention calls only
  * Two kernels where a request's keys may be cut between CTAs (tables of more than
- * 32 pages), else one. A request whose lengths are out of bounds, or that has more than max_nodes
- * nodes, sets PKV_ERR_OUT_OF_BOUNDS and its rows are not written. A page id
- * outside the pool sets it too; the rows of that request are then undefined.
+ * 32 pages), else one. A request whose lengths are out of bounds, or that has more
+ * than max_nodes nodes, sets PKV_ERR_OUT_OF_BOUNDS and its rows are not written. A
+ * page id outside the pool sets it too; the rows of that request are then
+ * undefined.
  * Geometry: head_dim 64 or 128, 1 to 8 query heads per KV head, page_size 16.
  */
 int pkv_tree_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
@@ -624,7 +626,7 @@ int pkv_tree_attn(const void* q, const void* k_pages, const void* v_pages, const
 /*
  * pkv_tree_attn_fp8 -- pkv_tree_attn over the 8-bit cache. The rows that it
  * stands for are exact in bf16: the outputs are those of pkv_expand_fp8 followed
- * by pkv_tree_attn, bit for bit. max_pages_per_seq <= 2^27 - 2.
+ * by pkv_tree_attn, bit for bit.
  */
 int pkv_tree_attn_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
                       const int32_t* block_table, const int32_t* prefix_lens, const int32_t* cu_nodes,
@@ -654,11 +656,11 @@ int pkv_tree_attn_fp8(const void* q, const void* k_pages, const void* v_pages, c
  *  prefix_lens, block_table: as for pkv_tree_attn; no two requests may have
  *                the same page among those that hold their nodes
  *  num_seqs:     >= 0 (0 launches nothing); num_seqs * max_pages_per_seq *
- *                max(num_kv_heads, 8) < 2^31
- *  max_path:     1 .. 64 (PKV_ERR_UNSUPPORTED beyond)
+ *                max(num_kv_heads, 8) < 2^31; max_pages_per_seq <= 2^27 - 2
+ *  max_path:     0 .. 64 (PKV_ERR_UNSUPPORTED beyond; 0 launches nothing)
  *  k_pages, v_pages, kv_scales: HOST arrays of n_layers device pointers, one
- *                pool per layer, read during the call only; all pools of the
- *                geometry of `desc`. kv_scales NULL: bf16 pools; else 8-bit ones
+ *                pool per layer, no pool twice, read during the call only; all
+ *                pools of the geometry of `desc`. kv_scales NULL: bf16 pools; else 8-bit ones
  *  n_layers:     >= 0 (0 launches nothing); one launch per 64 layers
  *  workspace:    as for pkv_append (may be NULL)
  */

@@ -114,11 +114,12 @@ __global__ void __launch_bounds__(kKeepThreads) keep_nodes_kernel(const __grid_c
       const long long at = static_cast<long long>(prefix) + x, put = static_cast<long long>(prefix) + i;
       if (i < n) {
         bool fine = x > prev && x >= i && at < static_cast<long long>(a.max_pages) * kPageSize;
-        if (fine && x != i) {
+        if (fine) {
           const int* row = a.block_table + static_cast<size_t>(s) * a.max_pages;
           p = __ldg(row + at / kPageSize);
           q = __ldg(row + put / kPageSize);
-          move = fine = p >= 0 && p < a.num_pages && q >= 0 && q < a.num_pages;
+          fine = p >= 0 && p < a.num_pages && q >= 0 && q < a.num_pages;
+          move = fine && x != i;
         }
         if (!fine) set_status(a.status, PKV_ERR_OUT_OF_BOUNDS);
       }

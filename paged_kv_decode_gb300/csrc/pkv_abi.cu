@@ -505,7 +505,8 @@ static int tree_attn(const pkv::TreeAttn& t, bool fp8, pkv_stream_t stream, cons
   int rc = check_desc_decode(desc);
   if (rc != PKV_OK) return rc;
   if (t.num_seqs < 0 || t.total_nodes < 0 || t.max_nodes < 0 || t.max_pages < 1) return PKV_ERR_BAD_SHAPE;
-  if (t.max_pages > kMaxTablePages || !table_fits(t.num_seqs, t.max_pages, desc->num_kv_heads)) return PKV_ERR_BAD_SHAPE;
+  // (the end of the last tile of 128 keys fits 32 bits as well)
+  if (t.max_pages > kMaxTablePages - 6 || !table_fits(t.num_seqs, t.max_pages, desc->num_kv_heads)) return PKV_ERR_BAD_SHAPE;
   if (t.num_seqs > pkv::tree_max_seqs() || t.max_nodes > pkv::tree_max_nodes()) return PKV_ERR_UNSUPPORTED;
   if (workspace == nullptr) return PKV_ERR_NULL_ARG;
   if (workspace_bytes < PKV_STATUS_BYTES) return PKV_ERR_WORKSPACE_TOO_SMALL;

@@ -206,6 +206,18 @@ def test_bad_entries_are_reported_and_skipped(cuda_device, fp8):
 
 
 @pytest.mark.gpu
+def test_nodes_that_stay_in_a_bad_page_are_reported(cuda_device):
+    """A path that moves nothing, whose rows lie in a page outside the pool."""
+    p = Pools(14, 1, 4, 8, 128, False, cuda_device)
+    for table, status in (([[0, 4]], pkv.ERR_CODES["PKV_ERR_OUT_OF_BOUNDS"]), ([[0, 3]], 0)):
+        p.ws = pkv.Workspace(pkv.PKV_STATUS_BYTES, cuda_device)
+        pkv.keep_nodes(i32([[0, 1, 2]], cuda_device), i32([3], cuda_device), i32([16], cuda_device), i32(table, cuda_device),
+                       *p.given("stacked"), workspace=p.ws)
+        p.same()
+        assert p.ws.status() == status
+
+
+@pytest.mark.gpu
 def test_binding_refuses_bad_tensors(cuda_device):
     prefix, path, length, table = _requests(12, 3, 4, 9)
     p = Pools(13, 2, table.size, 2, 64, True, cuda_device)

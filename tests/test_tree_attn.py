@@ -51,7 +51,8 @@ def test_host_argument_checks(lib, fp8):
         assert call(desc=bad) == -3
     assert call(desc=_desc(num_pages=0)) == -2
     assert call(seqs=-1) == -2 and call(total=-1) == -2 and call(most=-1) == -2 and call(pages=0) == -2
-    assert call(pages=(1 << 27) - 1, seqs=1) == -2 and call(seqs=1024, pages=1 << 18) == -2
+    # (the end of the last tile of 128 keys, 128 ceil(16 pages / 128), is past 2^31 - 1 from 2^27 - 7 pages on)
+    assert call(pages=(1 << 27) - 7, seqs=1) == -2 and call(seqs=1024, pages=1 << 18) == -2
     assert call(seqs=1025) == -3 and call(most=65) == -3
     assert call(ws=None) == -1 and call(nb=64) == -4
     assert call(seqs=0) == 0 and call(total=0) == 0 and call(most=0) == 0  # nothing to do, no device
