@@ -34,7 +34,7 @@
 //    the bf16 kernel: the outputs are those of pkv_expand_fp8 followed by the
 //    bf16 call, bit for bit.
 //  * P is rounded to bf16 before it multiplies V, the operand type of the product
-//    (off by at most 2^-9 of a weight); the sum l keeps the unrounded weights in
+//    (off by at most 2^-8 of a weight); the sum l keeps the unrounded weights in
 //    fp32.
 //  * Value rows behind the last node are zeroed in shared memory (they may hold
 //    anything, and 0 * NaN = NaN). A node's value row that holds infinities or
@@ -43,15 +43,17 @@
 //
 // Measured on one GB300 (us in a graph, inputs resident, of 16 / 8 / 128 where not
 // said otherwise; in brackets the cache's bytes at 6682 GB/s): 16 requests of 300
-// to 3000 tokens with 16 nodes 31.8 (20.0), one of 40k tokens with 32 nodes 35.6
-// (24.6), 27 ragged requests of 32 / 8 / 128 118 (65), two of 37 and 200 tokens
-// 7.4; 8-bit cache: the 16 requests 35.5 (10.2). What is left: long batches run at 92 % of the
-// memory's rate (16 requests of 6600 tokens: 70.2 of 64.9); shorter ones pay 4 us
-// from the launch to the first tile (the lengths, the table and the tile are
-// three dependent reads), 2 us an item and 3.5 us for the join and its launch.
-// Neither the products nor the softmax bound it: leaving out either changes no
-// time. The 8-bit form is bound by the expansion of its tiles (without it 1.25
-// instead of 1.85 us a tile).
+// to 3000 tokens with 16 nodes 32.0 (20.0), one of 40k tokens with 32 nodes 35.7
+// (24.6), 27 ragged requests of 32 / 8 / 128 119 (65), two of 37 and 200 tokens
+// 7.4; 8-bit cache: the 16 requests 35.8 (10.2). What is left: long batches run at
+// 92 % of the memory's rate (16 requests of 6600 tokens: 70.2 of 64.9); shorter
+// ones pay 4 us from the launch to the first tile (the lengths, the table and the
+// tile are three dependent reads), 2 us an item and 3.5 us for the join and its
+// launch. Where a request has more than 128 rows each tile of rows reads the keys
+// for itself, at the copies' rate (1.3 us a tile). Neither the products nor the
+// softmax bound any of these: leaving out either changes no time. The 8-bit form
+// is bound by the expansion of its tiles (without it 1.25 instead of 1.85 us a
+// tile; twice as many expanding warps change nothing).
 #include <cuda.h>
 #include <float.h>
 #include <math_constants.h>
