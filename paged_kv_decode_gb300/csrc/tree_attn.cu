@@ -45,18 +45,20 @@
 // said otherwise; in brackets the cache's bytes at 6682 GB/s): 16 requests of 300
 // to 3000 tokens with 16 nodes 32.0 (20.0), one of 40k tokens with 32 nodes 35.7
 // (24.6), 27 ragged requests of 32 / 8 / 128 119 (65), two of 37 and 200 tokens
-// 7.4; 8-bit cache: the 16 requests 35.8 (10.2). What is left: long batches run at
+// 7.4; 8-bit cache: the 16 requests 32.0 (10.2). What is left: long batches run at
 // 92 % of the memory's rate (16 requests of 6600 tokens: 70.2 of 64.9); shorter
 // ones pay 4 us from the launch to the first tile (the lengths, the table and the
 // tile are three dependent reads), 2 us an item and 3.5 us for the join and its
 // launch. Where a request has more than 128 rows each tile of rows reads the keys
 // for itself, at the copies' rate (1.3 us a tile). Neither the products nor the
 // softmax bound any of these: leaving out either changes no time. The 8-bit form
-// is bound by the expansion of its tiles (without it 1.25 instead of 1.85 us a
-// tile; twice as many expanding warps change nothing).
+// is bound by the instructions that expand its tiles (27 us without them; with
+// twice as many expanding warps 34).
 #include <cuda.h>
 #include <float.h>
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "pkv_device.cuh"
 #include "pkv_fp8.cuh"
@@ -884,6 +886,11 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
       uint64_t* empty = kv ? ctl->v_empty : ctl->k_empty;
       uint64_t* raw_full = kv ? ctl->raw_v_full : ctl->raw_k_full;
       uint64_t* raw_empty = kv ? ctl->raw_v_empty : ctl->raw_k_empty;
+      // this lane's row and its places in the first 8 rows of the raw and of the expanded tile
+      const int bit = D == 128 ? (lane >> 2) & 1 : 0;
+      const int t0 = 32 * sub + (D == 128 ? (lane >> 3) * 2 + bit : lane >> 2);
+      const int c0 = (lane & 3) + 4 * bit;
+      const uint32_t src0 = t0 * D + c0 * 16, dst0 = tr_off<D>(t0, 2 * c0);
       uint32_t g = 0;
       bool ok = true;
       for (uint32_t pi = 0; ok; ++pi) {
@@ -900,48 +907,53 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
           const bool tail = kv && (k + 1) * kTrKeys > P;
           const int len = P + T - k * kTrKeys;
           // 16 values a lane at a time. Of 8 lanes four take one half of a row, four the other half of the next, so
-          // that the reads (128-byte rows) and the writes (swizzled) both hit every bank once.
+          // that the reads (128-byte rows) and the writes (swizzled) both hit every bank once. The expansion is bound
+          // by its instructions: tiles with rows to mend take a loop of their own and addresses differ by constants
+          // (16 requests 36.0 -> 32.0 us); two steps unrolled, as the roles share the SM's instruction caches (four
+          // 35.3, eight 39.6).
           constexpr int kSteps = D / 16;
+          auto expand = [&](auto mend) {
 #pragma unroll 2
-          for (int i = 0; i < kSteps; ++i) {
-            int t, c;
-            if constexpr (D == 128) {
-              const int bit = (lane >> 2) & 1;
-              t = 32 * sub + (i >> 1) * 8 + (lane >> 3) * 2 + bit;
-              c = (lane & 3) + 4 * (bit ^ (i & 1));
-            } else {
-              t = 32 * sub + i * 8 + (lane >> 2);
-              c = lane & 3;
-            }
-            const uint4 x = *reinterpret_cast<const uint4*>(src + t * D + c * 16);
-            const float s = __uint_as_float(static_cast<uint32_t>(sc[t]) << 23);
-            const float2 s2 = make_float2(s, s);
-            uint32_t y[8];
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+            for (int i = 0; i < kSteps; ++i) {
+              const int rows8 = D == 128 ? i >> 1 : i;  // groups of 8 rows ahead
+              const int odd = D == 128 ? i & 1 : 0;
+              const uint4 x = *reinterpret_cast<const uint4*>(src + (src0 ^ odd << 6) + rows8 * (8 * D));
+              const float s = __uint_as_float(static_cast<uint32_t>(sc[t0 + rows8 * 8]) << 23);
+              const float2 s2 = make_float2(s, s);
+              uint32_t y[8];
+              const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t lo2, hi2;
-              e4m3x4_to_f16x4(xs[q], lo2, hi2);
-              const float2 u = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&lo2)), s2);
-              const float2 v = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&hi2)), s2);
-              y[2 * q] = pack_bf16x2(u.x, u.y);
-              y[2 * q + 1] = pack_bf16x2(v.x, v.y);
-            }
-            if (tail && k * kTrKeys + t >= P) {
-              bool odd = false;
+              for (int q = 0; q < 4; ++q) {
+                uint32_t lo2, hi2;
+                e4m3x4_to_f16x4(xs[q], lo2, hi2);
+                const float2 u = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&lo2)), s2);
+                const float2 v = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&hi2)), s2);
+                y[2 * q] = pack_bf16x2(u.x, u.y);
+                y[2 * q + 1] = pack_bf16x2(v.x, v.y);
+              }
+              if constexpr (decltype(mend)::value) {
+                const int t = t0 + rows8 * 8;
+                if (k * kTrKeys + t >= P) {
+                  bool bad = false;
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                if (t >= len) y[q] = 0u;
-                if (nonfinite_bf16x2(y[q])) {
-                  odd = true;
-                  y[q] = finite_bf16x2(y[q]);
+                  for (int q = 0; q < 8; ++q) {
+                    if (t >= len) y[q] = 0u;
+                    if (nonfinite_bf16x2(y[q])) {
+                      bad = true;
+                      y[q] = finite_bf16x2(y[q]);
+                    }
+                  }
+                  if (bad) atomicOr(&ctl->piece[pi % Dm::kPieces].bad, 1ull << (k * kTrKeys + t - P));
                 }
               }
-              if (odd) atomicOr(&ctl->piece[pi % Dm::kPieces].bad, 1ull << (k * kTrKeys + t - P));
+              *reinterpret_cast<uint4*>(dst + (dst0 ^ odd << 10) + rows8 * (8 * D * 2)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(dst + (dst0 ^ (odd << 10 | 16)) + rows8 * (8 * D * 2)) = make_uint4(y[4], y[5], y[6], y[7]);
             }
-            *reinterpret_cast<uint4*>(dst + tr_off<D>(t, 2 * c)) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(dst + tr_off<D>(t, 2 * c + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-          }
+          };
+          if (tail)
+            expand(std::true_type{});
+          else
+            expand(std::false_type{});
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
