@@ -360,6 +360,9 @@ int pkv_append_rope(const void* q, int64_t q_stride, const void* k_new, int64_t 
  *    (4 exponent bits, 3 mantissa bits, largest value 448, no infinities).
  *  - kv_scales: one byte per row, [num_pages][num_kv_heads][2][page_size]: the
  *    K rows' scales, then the V rows'. Byte b stands for 2^(b - 127) (e8m0).
+ *    The appends write 47 .. 227. Of the other bytes, which only a caller can
+ *    put there, pkv_expand_fp8 and pkv_tree_attn_fp8 take 255 (NaN in e8m0) as
+ *    infinity and 0 as zero; a product past bf16's range is infinite.
  *  - A row x stands for 2^e v: e is the least integer with max |x_i| <= 448 *
  *    2^e over the finite x_i, clamped to [-80, 100] (-80 for a row of zeros),
  *    and v_i = x_i * 2^-e rounded to e4m3, ties to even, saturating at 448

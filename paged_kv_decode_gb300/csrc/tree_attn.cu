@@ -278,12 +278,18 @@ __device__ __noinline__ float tr_nonfinite(const TrArgs& a, const TrPiece* pc, u
     if (!(bad >> j & 1ull) || pos < pc->k0 * kTrKeys || pos >= pc->k1 * kTrKeys) continue;
     const int id = __ldg(a.block_table + static_cast<size_t>(pc->n) * a.max_pages + pos / kPageSize);
     if (id < 0 || id >= a.num_pages) continue;
-    const size_t at = ((static_cast<size_t>(id) * a.hkv + pc->h) * kPageSize + pos % kPageSize) * D + col;
+    const size_t tile = static_cast<size_t>(id) * a.hkv + pc->h;
+    const size_t at = (tile * kPageSize + pos % kPageSize) * D + col;
     float x;
-    if constexpr (kFp8)
-      x = (a.v_raw[at] & 0x7f) == 0x7f ? CUDART_NAN_F : 0.f;
-    else
+    if constexpr (kFp8) {  // the expansion's arithmetic: the scale byte, too, can make infinities and NaN
+      const uint32_t e = a.scales[tile * kScaleBytes + kPageSize + pos % kPageSize];
+      uint32_t lo, hi;
+      e4m3x4_to_f16x4(a.v_raw[at], lo, hi);
+      const float v = __half2float(__ushort_as_half(static_cast<unsigned short>(lo)));
+      x = __bfloat162float(__float2bfloat16_rn(v * __uint_as_float(e << 23)));
+    } else {
       x = __bfloat162float(a.v_pages[at]);
+    }
     if (!(fabsf(x) < CUDART_INF_F)) sum += x;
   }
   return sum;
