@@ -1147,7 +1147,9 @@ int launch_tree_attn(const TreeAttn& t, int num_q_heads, int num_kv_heads, int h
   a.by_item = items <= num_sms ? static_cast<int>(items) : 0;
   a.scale_log2 = fabsf(t.scale) * kLog2e;
   a.idesc_qk = idesc_bf16_f32(kTrRows, kTrKeys, false) | (t.scale < 0.f ? 1u << 13 : 0u);  // bit 13 negates A
-  if (a.scale_log2 == 0.f) a.scale_log2 = FLT_MIN;  // a masked score, infinity, times 0 would be NaN
+  // a masked score, infinity, times 0 would be NaN; times this, differences of up to 2^128 have weights of 2^(-2^-21) (with
+  // FLT_MIN scores of 2^119 and more were told apart)
+  if (a.scale_log2 == 0.f) a.scale_log2 = FLT_TRUE_MIN;
 
   const cuuint64_t hd = static_cast<cuuint64_t>(head_dim);
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};

@@ -1,4 +1,5 @@
-"""Tree attention where values leave the ordinary range: value rows that are no numbers because of their scale byte."""
+"""Tree attention where values or scores leave the ordinary range: value rows that are no numbers because of their scale byte,
+and scales of zero and next to it with scores of any size."""
 import numpy as np
 import pytest
 import torch
@@ -53,3 +54,16 @@ def test_scale_bytes_that_make_no_numbers_of_a_value_row(cuda_device, geom, reqs
             else:
                 assert torch.equal(_bits(got)[n], clean[n])
     assert c.ws.status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-42, 1e-45])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_scales_of_nothing_with_large_scores(cuda_device, scale, fp8):
+    """Scores up to 2^126 and a scale that takes them to zero: every visible key has the same weight (the bound of the scores'
+    own rounding, in proportion to the scale, is below 2^-30 here)."""
+    c = Tree(42, GEOMS["12q4kv128"], [(130, 20), (0, 3), (700, 9)], cuda_device, fp8=fp8, q_size=2.0 ** 120)
+    assert 2.0 ** 122 < float(c.q.abs().max()) < 2.0 ** 123.5
+    c.scale = scale
+    c.step()
+    c.check()
