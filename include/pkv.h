@@ -150,7 +150,7 @@ const char* pkv_status_string(int status);
  *  n_tokens:      >= 0 (0 launches nothing).
  *  k_pages, v_pages: the pools, updated in place. Bit-exact copy.
  *  workspace:     may be NULL (device errors then go unreported); otherwise
- *                 at least PKV_STATUS_BYTES.
+ *                 at least PKV_STATUS_BYTES, 4-byte aligned.
  */
 int pkv_append(const void* k_new, const void* v_new, const int32_t* slot_mapping, int32_t n_tokens,
                void* k_pages, void* v_pages, const pkv_cache_desc* desc, pkv_stream_t stream,

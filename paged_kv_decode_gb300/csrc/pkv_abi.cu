@@ -67,6 +67,8 @@ int check_desc_decode(const pkv_cache_desc* d) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// The status word of the calls that use nothing else of a workspace: an int, updated by atomics.
+bool aligned_status(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Largest block table the kernels index with 32-bit counts of (request, KV
 // head, page) triples (the decode kernel's flattened list: at most rows *
@@ -123,7 +125,7 @@ int pkv_append(const void* k_new, const void* v_new, const int32_t* slot_mapping
   if (workspace != nullptr && workspace_bytes < PKV_STATUS_BYTES) return PKV_ERR_WORKSPACE_TOO_SMALL;
   if (n_tokens == 0) return PKV_OK;
   if (!k_new || !v_new || !slot_mapping || !k_pages || !v_pages) return PKV_ERR_NULL_ARG;
-  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages))
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned_status(workspace))
     return PKV_ERR_MISALIGNED;
   int sms = 0;
   rc = current_device(&sms);
@@ -333,7 +335,8 @@ static int append_rope(const void* q, int64_t q_stride, const void* k_new, int64
   if (n_tokens > 1 && ((q != nullptr && q_stride < hq * d) || k_stride < hkv * d || v_stride < hkv * d))
     return PKV_ERR_BAD_SHAPE;
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(cos_sin) || !aligned16(q_weight) ||
-      !aligned16(k_weight) || !aligned16(q_out) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(kv_scales))
+      !aligned16(k_weight) || !aligned16(q_out) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(kv_scales) ||
+      !aligned_status(workspace))
     return PKV_ERR_MISALIGNED;
   if (n_tokens > 1 && ((q != nullptr && q_stride % 8 != 0) || k_stride % 8 != 0 || v_stride % 8 != 0))
     return PKV_ERR_MISALIGNED;
@@ -468,7 +471,8 @@ int pkv_expand_fp8(const void* k_pages, const void* v_pages, const void* kv_scal
   if (num_seqs == 0) return PKV_OK;
   if (!k_pages || !v_pages || !kv_scales || !block_table || !seq_lens || !k_out || !v_out || !out_block_table)
     return PKV_ERR_NULL_ARG;
-  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(kv_scales) || !aligned16(k_out) || !aligned16(v_out))
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(kv_scales) || !aligned16(k_out) || !aligned16(v_out) ||
+      !aligned_status(workspace))
     return PKV_ERR_MISALIGNED;
   int sms = 0;
   rc = current_device(&sms);
@@ -569,6 +573,7 @@ int pkv_keep_nodes(const int32_t* path, const int32_t* path_lens, const int32_t*
   if (workspace != nullptr && workspace_bytes < PKV_STATUS_BYTES) return PKV_ERR_WORKSPACE_TOO_SMALL;
   if (num_seqs == 0 || max_path == 0 || n_layers == 0) return PKV_OK;
   if (!path || !path_lens || !prefix_lens || !block_table || !k_pages || !v_pages) return PKV_ERR_NULL_ARG;
+  if (!aligned_status(workspace)) return PKV_ERR_MISALIGNED;
   pkv::MovePools pools;
   for (int32_t l0 = 0; l0 < n_layers; l0 += pkv::kMoveLayers) {  // all layers are checked before anything is launched
     rc = move_pools(k_pages, v_pages, kv_scales, l0, n_layers - l0 < pkv::kMoveLayers ? n_layers - l0 : pkv::kMoveLayers, &pools);
@@ -597,6 +602,7 @@ int pkv_copy_pages(const int32_t* src, const int32_t* dst, int32_t n_pairs, void
   if (workspace != nullptr && workspace_bytes < PKV_STATUS_BYTES) return PKV_ERR_WORKSPACE_TOO_SMALL;
   if (n_pairs == 0 || n_layers == 0) return PKV_OK;
   if (!src || !dst || !k_pages || !v_pages) return PKV_ERR_NULL_ARG;
+  if (!aligned_status(workspace)) return PKV_ERR_MISALIGNED;
   pkv::MovePools pools;
   for (int32_t l0 = 0; l0 < n_layers; l0 += pkv::kMoveLayers) {
     rc = move_pools(k_pages, v_pages, kv_scales, l0, n_layers - l0 < pkv::kMoveLayers ? n_layers - l0 : pkv::kMoveLayers, &pools);
