@@ -606,8 +606,8 @@ size_t pkv_tree_workspace_bytes(const pkv_cache_desc* desc, int32_t num_seqs, in
  *                total_nodes. A request without nodes (padding) costs nothing
  *  tree_mask:    int64 [total_nodes], 8-byte aligned, or NULL. Bits at and
  *                past T are ignored
- *  max_nodes:    host-side upper bound on any request's nodes, 1 .. 64
- *                (PKV_ERR_UNSUPPORTED beyond)
+ *  max_nodes:    host-side upper bound on any request's nodes, 0 .. 64
+ *                (PKV_ERR_UNSUPPORTED beyond; 0 launches nothing)
  *  num_seqs:     0 .. 1024 (PKV_ERR_UNSUPPORTED beyond); num_seqs *
  *                max_pages_per_seq * max(num_kv_heads, 8) < 2^31;
  *                max_pages_per_seq <= 2^27 - 8
@@ -629,7 +629,9 @@ int pkv_tree_attn(const void* q, const void* k_pages, const void* v_pages, const
 /*
  * pkv_tree_attn_fp8 -- pkv_tree_attn over the 8-bit cache. The rows that it
  * stands for are exact in bf16: the outputs are those of pkv_expand_fp8 followed
- * by pkv_tree_attn, bit for bit.
+ * by pkv_tree_attn, bit for bit, the softmax weights in bf16 (pkv_decode_attn_fp8
+ * holds them in fp16). It halves the cache's memory, not the time: the expansion
+ * takes what the bytes save.
  */
 int pkv_tree_attn_fp8(const void* q, const void* k_pages, const void* v_pages, const void* kv_scales,
                       const int32_t* block_table, const int32_t* prefix_lens, const int32_t* cu_nodes,

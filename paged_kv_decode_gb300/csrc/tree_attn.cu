@@ -16,7 +16,7 @@
 //
 //  * An item is (request, KV head, tile of up to 128 / G nodes): its rows are
 //    the M = 128 rows of the products, node-major, heads of a node side by side
-//    (one 3-D TMA box). Items cost kItemCost + ceil((P + T) / 128) units; every
+//    (a 3-D TMA box for each 64 dims). Items cost kItemCost + ceil((P + T) / 128) units; every
 //    CTA (one per SM) takes an equal contiguous share of the units, cutting
 //    items; a cut item's partial results go to records, and a second small
 //    kernel joins them in CTA order (the same bits every time). Where all items
@@ -35,7 +35,9 @@
 //    bf16 call, bit for bit.
 //  * P is rounded to bf16 before it multiplies V, the operand type of the product
 //    (off by at most 2^-8 of a weight); the sum l keeps the unrounded weights in
-//    fp32.
+//    fp32. Against 64 bits outputs are off by 0.0022 (relative, in the square mean)
+//    where the bf16 output's own rounding gives 0.0017. The 8-bit decode kernel's
+//    weights are fp16, three bits more: its operands are.
 //  * Value rows behind the last node are zeroed in shared memory (they may hold
 //    anything, and 0 * NaN = NaN). A node's value row that holds infinities or
 //    NaN would reach rows that do not see the node the same way: such elements
@@ -43,17 +45,20 @@
 //
 // Measured on one GB300 (us in a graph, inputs resident, of 16 / 8 / 128 where not
 // said otherwise; in brackets the cache's bytes at 6682 GB/s): 16 requests of 300
-// to 3000 tokens with 16 nodes 32.0 (20.0), one of 40k tokens with 32 nodes 35.7
+// to 3000 tokens with 16 nodes 31.8 (20.0), one of 40k tokens with 32 nodes 35.5
 // (24.6), 27 ragged requests of 32 / 8 / 128 119 (65), two of 37 and 200 tokens
-// 7.4; 8-bit cache: the 16 requests 32.0 (10.2). What is left: long batches run at
-// 92 % of the memory's rate (16 requests of 6600 tokens: 70.2 of 64.9); shorter
-// ones pay 4 us from the launch to the first tile (the lengths, the table and the
-// tile are three dependent reads), 2 us an item and 3.5 us for the join and its
-// launch. Where a request has more than 128 rows each tile of rows reads the keys
-// for itself, at the copies' rate (1.3 us a tile). Neither the products nor the
-// softmax bound any of these: leaving out either changes no time. The 8-bit form
-// is bound by the instructions that expand its tiles (27 us without them; with
-// twice as many expanding warps 34).
+// 7.4; 8-bit cache: the 16 requests 32.0 (10.2), the one 33.3 (12.4), about the
+// times of the bf16 cache. What is left: long batches run at 92 % of the memory's
+// rate (16 requests of 6600 tokens: 70.7 of 65.2, in 8 bits 74.7 of 33.0); shorter
+// ones pay 4 us from the launch to the first tile
+// (the lengths, the table and the tile are three dependent reads), 2 us an item and
+// 3.5 us for the join and its launch. Where a request has more than 128 rows each
+// tile of rows reads the keys for itself, at the copies' rate (1.3 us a tile).
+// Neither the products nor the softmax bound the bf16 form (the ragged requests
+// took 119.8 us, 119.9 without the softmax, 120.4 without the value product). The
+// 8-bit form is bound by the instructions that expand its tiles, then by the
+// softmax (of 36.0 us at one stage 27.0 were left without the expansion's steps,
+// 33.4 without the softmax; 34 with twice as many expanding warps).
 #include <cuda.h>
 #include <float.h>
 #include <math_constants.h>
@@ -77,8 +82,11 @@ constexpr int kTrQkWarp = 8, kTrTmaWarp = 9, kTrMendWarp = 10, kTrPvWarp = 11;
 constexpr uint32_t kTrColS = 0, kTrColO = 256, kTrTmemCols = 512;  // S_w, O_w at + 128 w
 constexpr long long kDrainCycles = 20000000LL;                     // 10 ms: far more than a copy in flight takes
 
-// Fixed work of an item (query load, pipeline fill and drain, epilogue) in key tiles; and the largest item, in the
-// same units, that is never cut where all items are that small.
+// Fixed work of an item (query load, pipeline fill and drain, epilogue) in key tiles: 27 ragged requests of 32 / 8 / 128 take
+// 119 us with 3, 126 with 2. And the largest item, in the same units, that is never cut where all items are that small: with
+// 7 two requests of 37 and 200 tokens take 9.1 us and 16 of 50 to 490 12.3, cut into shares 10.5 and 14.4 (as nothing can be
+// cut at up to 32 pages, the join is not launched there either: 7.4 and 10.8). Many such requests would rather be cut: 64 of
+// them take 34.1 us whole, 30.0 in shares.
 #ifndef PKV_TREE_ITEM_COST
 #define PKV_TREE_ITEM_COST 3
 #endif
@@ -434,7 +442,9 @@ __global__ void __launch_bounds__(TrDim<D, kFp8>::kThreads, 1)
     items = __reduce_add_sync(0xffffffffu, items);
     largest = __reduce_max_sync(0xffffffffu, largest);
     // whole items where all are small, or where the CTAs' largest number of them is as good a balance as shares would be
-    // (within a quarter; every CTA computes the same floats)
+    // (within a quarter; every CTA computes the same floats): 16 requests of 4000 tokens 46.9 us, in shares 51.1; 36 of 3000
+    // 73.5 and 77.3; 16 of 1500 24.1 and 26.0 (a bound of a tenth leaves the first and the last in shares, one of a half changes
+    // nothing)
     const float rounds = ceilf(static_cast<float>(items) / static_cast<float>(a.ctas));
     const float longest = static_cast<float>(largest) * rounds * static_cast<float>(a.ctas);
     const bool whole = largest <= kSmallItem || 4.f * longest <= 5.f * static_cast<float>(units);
@@ -1090,7 +1100,7 @@ int launch(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& 
   if (launch_pdl(tree_attn_kernel<D, kFp8>, dim3(static_cast<unsigned>(a.ctas)), dim3(TrDim<D, kFp8>::kThreads),
                  tr_smem_bytes<D, kFp8>(), stream, qmap, kmap, vmap, a) != cudaSuccess)
     return PKV_ERR_CUDA;
-  // a table so narrow that no item can be cut needs no joining
+  // a table so narrow that no item can be cut needs no joining (a join that finds nothing to do takes 1.6 us)
   if (kItemCost + (static_cast<long long>(a.max_pages) + kTrTilePages - 1) / kTrTilePages <= kSmallItem) return PKV_OK;
   const unsigned items = static_cast<unsigned>(a.by_item > 0 ? a.by_item : a.ctas);
   const unsigned quarters = static_cast<unsigned>((a.box_rows + 31) / 32);
